@@ -31,11 +31,19 @@ EPLB_S_BAD_LOAD = 16
 EPLB_S_OVERFLOW = 17
 EPLB_S_BAD_MAP = 18
 EPLB_S_BAD_TOPOLOGY = 19
+EPLB_DTYPE_F32 = 0
+EPLB_DTYPE_BF16 = 1
+EPLB_DTYPE_F16 = 2
+EPLB_SCORE_SIGMOID = 0
+EPLB_SCORE_SOFTMAX = 1
 
 EXPORTS = ("eplb_load_hist", "eplb_rebalance", "eplb_redirect", "eplb_hist_redirect",
            "eplb_load_ema", "eplb_ema_redirect", "eplb_placement_load", "eplb_rearrange", "eplb_lp_solve", "eplb_lp_redirect",
            "eplb_lp_redirect_workspace_bytes", "eplb_status_string",
-           "eplb_rebalance_lds_bytes", "eplb_rebalance_max_count", "eplb_lp_redirect_noalloc")
+           "eplb_rebalance_lds_bytes", "eplb_rebalance_max_count", "eplb_lp_redirect_noalloc",
+           "eplb_gate", "eplb_gate_loss", "eplb_gate_loss_workspace_bytes", "eplb_balance_loss", "eplb_gate_backward",
+           "eplb_group_rows", "eplb_group_rows_workspace_bytes", "eplb_quantize_rows", "eplb_quantize_columns",
+           "eplb_quantize_weights", "eplb_expert_matmul", "eplb_expert_wgrad")
 
 
 def _load() -> ctypes.CDLL:
@@ -78,6 +86,33 @@ def _load() -> ctypes.CDLL:
     lib.eplb_rebalance_max_count.restype = i32
     lib.eplb_lp_redirect_noalloc.argtypes = [p, i64, i64, i32, i32, p, p, i32, i32, p, p]
     lib.eplb_lp_redirect_noalloc.restype = i32
+    f32 = ctypes.c_float
+    choice = [i32, i32, i32, i32, f32, p]     # G, top_groups, group_top, normalize, scale, mask
+    lib.eplb_gate.argtypes = [p, i32, i64, i64, i32, i32, i32, p, *choice, p, p, p]
+    lib.eplb_gate.restype = i32
+    lib.eplb_gate_loss.argtypes = [p, i32, i64, i64, i32, i32, i32, p, *choice, p, i64, f32, p, i64,
+                                   p, p, p, p, p, p, p]
+    lib.eplb_gate_loss.restype = i32
+    lib.eplb_gate_loss_workspace_bytes.argtypes = [i64, i32, i64]
+    lib.eplb_gate_loss_workspace_bytes.restype = i64
+    lib.eplb_balance_loss.argtypes = [p, i32, i64, i64, i32, p, i32, i32, p, p, i64, f32, p, i64, p, p, p, p, p]
+    lib.eplb_balance_loss.restype = i32
+    lib.eplb_gate_backward.argtypes = [p, i32, i64, i64, i32, p, i32, i32, i32, f32, p, p, p, i64, f32, p, p, p, p, p]
+    lib.eplb_gate_backward.restype = i32
+    lib.eplb_group_rows.argtypes = [p, i64, i64, i32, i32, p, i64, p, p, p, p]
+    lib.eplb_group_rows.restype = i32
+    lib.eplb_group_rows_workspace_bytes.argtypes = [i64, i64, i32]
+    lib.eplb_group_rows_workspace_bytes.restype = i64
+    lib.eplb_quantize_rows.argtypes = [p, i32, i64, i64, i64, p, p, p]
+    lib.eplb_quantize_rows.restype = i32
+    lib.eplb_quantize_columns.argtypes = [p, i32, i64, i64, i64, p, i64, i32, p, i32, i64, p, p, p]
+    lib.eplb_quantize_columns.restype = i32
+    lib.eplb_quantize_weights.argtypes = [p, i32, i32, i64, i64, p, p, p, p, p]
+    lib.eplb_quantize_weights.restype = i32
+    lib.eplb_expert_matmul.argtypes = [p, p, i64, p, p, p, i32, p, i64, i32, i64, i64, i32, p, p]
+    lib.eplb_expert_matmul.restype = i32
+    lib.eplb_expert_wgrad.argtypes = [p, p, p, p, p, i32, i64, i64, i64, i64, i32, p, p]
+    lib.eplb_expert_wgrad.restype = i32
     return lib
 
 
@@ -474,4 +509,372 @@ def lp_redirect_noalloc(idx: torch.Tensor, E: int, rep: torch.Tensor, flow: torc
                                       _dev(flow, torch.int64, "flow"), RK, R, _dev(out, torch.int32, "out"),
                                       _stream(idx.device))
     _check(rc, "eplb_lp_redirect_noalloc")
+    return out
+
+
+# ---------------------------------------------------------------- router
+_DTYPES = {torch.float32: EPLB_DTYPE_F32, torch.bfloat16: EPLB_DTYPE_BF16, torch.float16: EPLB_DTYPE_F16}
+_SCORING = {"sigmoid": EPLB_SCORE_SIGMOID, "softmax": EPLB_SCORE_SOFTMAX}
+F8 = torch.float8_e4m3fn     # 1 sign, 4 exponent and 3 mantissa bits; largest value 448
+BLOCK = 128                  # elements a scale covers along an axis
+
+
+def _dtype(dtype: torch.dtype, name: str) -> int:
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """(pointer, dtype code, row stride) of a 2-D tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _dtype(t.dtype, name)
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU, got {t.device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if (t.shape[1] > 1 and t.stride(1) != 1) or ld < t.shape[1]:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), code, ld
+
+
+def _f8(t: torch.Tensor, name: str) -> int:
+    if isinstance(t, torch.Tensor) and t.dtype == torch.uint8:
+        return _dev(t, torch.uint8, name)
+    return _dev(t, F8, name)
+
+
+def _optional(t, dtype: torch.dtype, shape: tuple, name: str) -> int | None:
+    if t is None:
+        return None
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _dev(t, dtype, name)
+
+
+def _mask(mask, T: int) -> int | None:
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    return _optional(mask, torch.uint8, (T,), "mask")
+
+
+def _scoring(scoring: str) -> int:
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
+    return _SCORING[scoring]
+
+
+def _workspace(workspace, need: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty((max(need, 4),), dtype=torch.uint8, device=device)
+    if workspace.device.type != "cuda" or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    return workspace
+
+
+def _shapes(out: tuple, shapes: tuple, what: str) -> None:
+    if len(out) != len(shapes) or any(tuple(t.shape) != s for t, s in zip(out, shapes)):
+        raise ValueError(f"{what} must have the shapes {[list(s) for s in shapes]}")
+
+
+def gate(logits: torch.Tensor, K: int, *, scoring: str = "sigmoid", bias: torch.Tensor | None = None, G: int = 1,
+         top_groups: int | None = None, group_top: int = 1, normalize: bool = True, scale: float = 1.0,
+         mask: torch.Tensor | None = None, out: tuple | None = None):
+    """The K experts with the largest keys of every token, and their weights.
+
+    logits [T, E] float32, bfloat16 or float16 (rows may be strided); bias [E]
+    float32 is added to the key only; with G groups only the experts of the
+    top_groups best groups may be chosen (a group's score: the sum of its
+    group_top largest keys); mask [T] bool or uint8: rows to route.  Equal keys
+    go to the lowest index.  Returns (ids [T, K] int32, weights [T, K]
+    float32); id -1 with weight 0 where nothing is left to choose.
+    """
+    ptr, dt, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    if out is None:
+        out = (torch.empty((T, K), dtype=torch.int32, device=dev),
+               torch.empty((T, K), dtype=torch.float32, device=dev))
+    _shapes(out, ((T, K), (T, K)), "out")
+    rc = lib.eplb_gate(ptr, dt, ld, T, E, K, _scoring(scoring), _optional(bias, torch.float32, (E,), "bias"), G,
+                       G if top_groups is None else top_groups, group_top, int(normalize), scale, _mask(mask, T),
+                       _dev(out[0], torch.int32, "ids"), _dev(out[1], torch.float32, "weights"), _stream(dev))
+    _check(rc, "eplb_gate")
+    return out
+
+
+def gate_loss_workspace_bytes(T: int, E: int, S: int) -> int:
+    n = lib.eplb_gate_loss_workspace_bytes(T, E, S)
+    if n < 0:
+        raise EplbError(-n, "eplb_gate_loss_workspace_bytes")
+    return n
+
+
+def _loss_out(out, S: int, E: int, dev, first: tuple) -> tuple:
+    shapes = tuple(s for s, _ in first) + ((S,), (S, E), (S, E), (S,))
+    if out is None:
+        types = tuple(d for _, d in first) + (torch.float32, torch.int32, torch.float32, torch.int32)
+        out = tuple(torch.empty(s, dtype=d, device=dev) for s, d in zip(shapes, types))
+    _shapes(out, shapes, "out")
+    return out
+
+
+def gate_loss(logits: torch.Tensor, K: int, seg: torch.Tensor, alpha: float, *, scoring: str = "sigmoid",
+              bias: torch.Tensor | None = None, G: int = 1, top_groups: int | None = None, group_top: int = 1,
+              normalize: bool = True, scale: float = 1.0, mask: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, out: tuple | None = None):
+    """gate with the balance loss of S segments of rows (seg [S + 1] int32:
+    segment s holds rows seg[s] .. seg[s + 1] - 1).
+
+    loss = alpha * sum over e of (E * counts / (K * tokens)) * prob, where prob
+    is the mean share of an expert in the rows' scores.  Returns (ids [T, K]
+    int32, weights [T, K] float32, loss [S] float32, counts [S, E] int32, prob
+    [S, E] float32, tokens [S] int32).
+    """
+    ptr, dt, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    if seg.dim() != 1 or seg.shape[0] < 2:
+        raise ValueError("seg must be [S + 1]")
+    S, dev = seg.shape[0] - 1, logits.device
+    out = _loss_out(out, S, E, dev, (((T, K), torch.int32), ((T, K), torch.float32)))
+    ids, weights, loss, counts, prob, tokens = out
+    ws = _workspace(workspace, gate_loss_workspace_bytes(T, E, S), dev)
+    rc = lib.eplb_gate_loss(ptr, dt, ld, T, E, K, _scoring(scoring), _optional(bias, torch.float32, (E,), "bias"), G,
+                            G if top_groups is None else top_groups, group_top, int(normalize), scale, _mask(mask, T),
+                            _dev(seg, torch.int32, "seg"), S, alpha, ws.data_ptr(), ws.numel() * ws.element_size(),
+                            _dev(ids, torch.int32, "ids"), _dev(weights, torch.float32, "weights"),
+                            _dev(loss, torch.float32, "loss"), _dev(counts, torch.int32, "counts"),
+                            _dev(prob, torch.float32, "prob"), _dev(tokens, torch.int32, "tokens"), _stream(dev))
+    _check(rc, "eplb_gate_loss")
+    return out
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, seg: torch.Tensor, alpha: float, *,
+                 scoring: str = "sigmoid", mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 out: tuple | None = None):
+    """gate_loss's loss for choices made elsewhere (ids [T, K] int32).
+    Returns (loss [S], counts [S, E], prob [S, E], tokens [S])."""
+    ptr, dt, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must be [{T}, K]")
+    if seg.dim() != 1 or seg.shape[0] < 2:
+        raise ValueError("seg must be [S + 1]")
+    S, dev = seg.shape[0] - 1, logits.device
+    out = _loss_out(out, S, E, dev, ())
+    loss, counts, prob, tokens = out
+    ws = _workspace(workspace, gate_loss_workspace_bytes(T, E, S), dev)
+    rc = lib.eplb_balance_loss(ptr, dt, ld, T, E, _dev(ids, torch.int32, "ids"), ids.shape[1], _scoring(scoring),
+                               _mask(mask, T), _dev(seg, torch.int32, "seg"), S, alpha, ws.data_ptr(),
+                               ws.numel() * ws.element_size(), _dev(loss, torch.float32, "loss"),
+                               _dev(counts, torch.int32, "counts"), _dev(prob, torch.float32, "prob"),
+                               _dev(tokens, torch.int32, "tokens"), _stream(dev))
+    _check(rc, "eplb_balance_loss")
+    return out
+
+
+def gate_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor | None, *,
+                  scoring: str = "sigmoid", normalize: bool = True, scale: float = 1.0,
+                  mask: torch.Tensor | None = None, seg: torch.Tensor | None = None, alpha: float = 0.0,
+                  counts: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                  d_loss: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of sum(d_weights * weights) + sum(d_loss * loss) with respect
+    to the logits: [T, E] in the logits' dtype.  Either term may be left out
+    (d_weights or d_loss None); the loss's needs seg, counts and tokens."""
+    ptr, dt, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must be [{T}, K]")
+    K, dev = ids.shape[1], logits.device
+    S = 0
+    if d_loss is not None:
+        if seg is None or counts is None or tokens is None:
+            raise ValueError("the loss's gradient needs seg, counts and tokens")
+        S = d_loss.shape[0]
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _shapes((out,), ((T, E),), "out")
+    given = d_loss is not None
+    rc = lib.eplb_gate_backward(ptr, dt, ld, T, E, _dev(ids, torch.int32, "ids"), K, _scoring(scoring), int(normalize),
+                                scale, _mask(mask, T), _optional(d_weights, torch.float32, (T, K), "d_weights"),
+                                _optional(seg, torch.int32, (S + 1,), "seg") if given else None, S, alpha,
+                                _optional(counts, torch.int32, (S, E), "counts") if given else None,
+                                _optional(tokens, torch.int32, (S,), "tokens") if given else None,
+                                _optional(d_loss, torch.float32, (S,), "d_loss"), _dev(out, logits.dtype, "out"),
+                                _stream(dev))
+    _check(rc, "eplb_gate_backward")
+    return out
+
+
+# ---------------------------------------------------------------- grouping
+def group_rows_workspace_bytes(L: int, n: int, P: int) -> int:
+    b = lib.eplb_group_rows_workspace_bytes(L, n, P)
+    if b < 0:
+        raise EplbError(-b, "eplb_group_rows_workspace_bytes")
+    return b
+
+
+def group_rows(ids: torch.Tensor, P: int, first: int = 0, workspace: torch.Tensor | None = None,
+               out: tuple | None = None):
+    """Rows (t, k) of every layer grouped by slot (slots first .. first + P - 1).
+
+    ids [L, T, K] or [L, n] int32 (redirect's output).  Returns (offsets [L, P +
+    1], order [L, n], place [L, n]), all int32: rows offsets[g] .. offsets[g +
+    1] - 1 of the grouped order belong to slot g, order names the position of
+    each in ids, place is its inverse.  Ids of no slot come last, in order.
+    """
+    if ids.dim() not in (2, 3):
+        raise ValueError("ids must be [L, T, K] or [L, n]")
+    L = ids.shape[0]
+    n = ids.shape[1] * (ids.shape[2] if ids.dim() == 3 else 1)
+    dev = ids.device
+    if out is None:
+        out = (torch.empty((L, P + 1), dtype=torch.int32, device=dev),
+               torch.empty((L, n), dtype=torch.int32, device=dev),
+               torch.empty((L, n), dtype=torch.int32, device=dev))
+    _shapes(out, ((L, P + 1), (L, n), (L, n)), "out")
+    need = group_rows_workspace_bytes(L, n, P)
+    ws = _workspace(workspace, need, dev) if need > 0 or workspace is not None else None
+    rc = lib.eplb_group_rows(_dev(ids, torch.int32, "ids"), L, n, first, P, None if ws is None else ws.data_ptr(),
+                             0 if ws is None else ws.numel() * ws.element_size(),
+                             _dev(out[0], torch.int32, "offsets"), _dev(out[1], torch.int32, "order"),
+                             _dev(out[2], torch.int32, "place"), _stream(dev))
+    _check(rc, "eplb_group_rows")
+    return out
+
+
+# ---------------------------------------------------------------- 8-bit blocks and products
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def quantize_rows(x: torch.Tensor, out: tuple | None = None):
+    """x [R, C] (rows may be strided) as 8-bit floating point with a scale for
+    each 128 elements of a row: (q [R, C] float8_e4m3fn, scale [R, ceil(C /
+    128)] float32)."""
+    ptr, dt, ld = _rows(x, "x")
+    R, C = x.shape
+    if out is None:
+        out = (torch.empty((R, C), dtype=F8, device=x.device),
+               torch.empty((R, _blocks(C)), dtype=torch.float32, device=x.device))
+    _shapes(out, ((R, C), (R, _blocks(C))), "out")
+    rc = lib.eplb_quantize_rows(ptr, dt, ld, R, C, _f8(out[0], "q"), _dev(out[1], torch.float32, "scale"),
+                                _stream(x.device))
+    _check(rc, "eplb_quantize_rows")
+    return out
+
+
+def padded_rows(R: int, G: int) -> int:
+    """Columns of quantize_columns' output: R rows in G groups, each group
+    rounded up to a multiple of 128."""
+    return (R + (BLOCK - 1) * G) // BLOCK * BLOCK
+
+
+def _grouping(offsets: torch.Tensor, rows: torch.Tensor | None, R: int | None, X: int, K: int) -> tuple[int, int]:
+    """(groups, grouped rows) of a grouping over an operand of X rows."""
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be [G + 1]")
+    if rows is not None and rows.dim() != 1:
+        raise ValueError("rows must be [R]")
+    n = X if rows is None else rows.shape[0]
+    if R is not None and R != n:
+        raise ValueError(f"out has {R} rows for {n} grouped rows")
+    return offsets.shape[0] - 1, n
+
+
+def quantize_columns(x: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None, K: int = 1,
+                     out: tuple | None = None):
+    """Grouped rows of x [X, C] transposed, in 8 bits with a scale for each 128
+    rows of a group: (q [C, Rp] float8_e4m3fn, scale [Rp / 128, C] float32)
+    with Rp = padded_rows(R, G).  Grouped row r is row rows[r] // K of x
+    (group_rows' order), or row r without rows."""
+    ptr, dt, ld = _rows(x, "x")
+    X, C = x.shape
+    G, R = _grouping(offsets, rows, None, X, K)
+    Rp = padded_rows(R, G)
+    if out is None:
+        out = (torch.empty((C, Rp), dtype=F8, device=x.device),
+               torch.empty((Rp // BLOCK, C), dtype=torch.float32, device=x.device))
+    _shapes(out, ((C, Rp), (Rp // BLOCK, C)), "out")
+    rc = lib.eplb_quantize_columns(ptr, dt, ld, X, C, _optional(rows, torch.int32, (R,), "rows"), R, K,
+                                   _dev(offsets, torch.int32, "offsets"), G, Rp, _f8(out[0], "q"),
+                                   _dev(out[1], torch.float32, "scale"), _stream(x.device))
+    _check(rc, "eplb_quantize_columns")
+    return out
+
+
+def quantize_weights(w: torch.Tensor, transpose: bool = False, out: tuple | None = None):
+    """w [G, N, K] as 8-bit floating point with a scale for each 128 x 128
+    block: (q [G, N, K], scale [G, ceil(N / 128), ceil(K / 128)]), and with
+    transpose also (qt [G, K, N], scale_t), the same values transposed."""
+    if w.dim() != 3:
+        raise ValueError("w must be [G, N, K]")
+    code = _dtype(w.dtype, "w")
+    G, N, K = w.shape
+    shapes = ((G, N, K), (G, _blocks(N), _blocks(K)), (G, K, N), (G, _blocks(K), _blocks(N)))[:4 if transpose else 2]
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.float32 if i & 1 else F8, device=w.device)
+                    for i, s in enumerate(shapes))
+    _shapes(out, shapes, "out")
+    rc = lib.eplb_quantize_weights(_dev(w, w.dtype, "w"), code, G, N, K, _f8(out[0], "q"),
+                                   _dev(out[1], torch.float32, "scale"), _f8(out[2], "qt") if transpose else None,
+                                   _dev(out[3], torch.float32, "scale_t") if transpose else None, _stream(w.device))
+    _check(rc, "eplb_quantize_weights")
+    return out
+
+
+def expert_matmul(q: torch.Tensor, scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                  offsets: torch.Tensor, rows: torch.Tensor | None = None, K: int = 1,
+                  dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Every grouped row times the transposed weights of its expert, both in 8
+    bits with a scale for each block of 128.
+
+    q [X, C], scale: quantize_rows' outputs; w [G, N, C], w_scale:
+    quantize_weights'; offsets [G + 1] int32: rows offsets[g] .. offsets[g + 1]
+    - 1 belong to expert g.  Grouped row r reads row rows[r] // K of q
+    (group_rows' order), or row r without rows.  Returns [R, N] in ``dtype``;
+    rows of no expert are 0.  offsets = [0, R] is the plain product.
+    """
+    if q.dim() != 2 or w.dim() != 3 or w.shape[2] != q.shape[1]:
+        raise ValueError("q [X, C] and w [G, N, C] expected")
+    X, C = q.shape
+    G, N, _ = w.shape
+    g, R = _grouping(offsets, rows, None if out is None else out.shape[0], X, K)
+    if g != G:
+        raise ValueError(f"offsets must be [{G + 1}]")
+    if out is None:
+        out = torch.empty((R, N), dtype=dtype, device=q.device)
+    _shapes((scale, w_scale, out), ((X, _blocks(C)), (G, _blocks(N), _blocks(C)), (R, N)), "scale, w_scale, out")
+    rc = lib.eplb_expert_matmul(_f8(q, "q"), _dev(scale, torch.float32, "scale"), X, _f8(w, "w"),
+                                _dev(w_scale, torch.float32, "w_scale"), _dev(offsets, torch.int32, "offsets"), G,
+                                _optional(rows, torch.int32, (R,), "rows"), R, K, N, C, _dtype(out.dtype, "out"),
+                                _dev(out, out.dtype, "out"), _stream(q.device))
+    _check(rc, "eplb_expert_matmul")
+    return out
+
+
+def expert_wgrad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
+                 offsets: torch.Tensor, R: int | None = None, dtype: torch.dtype = torch.float32,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of expert_matmul with respect to the weights: [G, N, C].
+
+    dy [N, Rp], dy_scale and x [C, Rp], x_scale: quantize_columns' outputs for
+    the same offsets.  R: the grouped rows (offsets past it are clamped);
+    default: as many as Rp allows."""
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[1] != x.shape[1] or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("dy [N, Rp], x [C, Rp] and offsets [G + 1] expected")
+    N, Rp = dy.shape
+    C = x.shape[0]
+    G = offsets.shape[0] - 1
+    if R is None:
+        R = max(0, Rp - (BLOCK - 1) * (G - 1)) if Rp else 0
+    if out is None:
+        out = torch.empty((G, N, C), dtype=dtype, device=dy.device)
+    _shapes((dy_scale, x_scale, out), ((Rp // BLOCK, N), (Rp // BLOCK, C), (G, N, C)), "dy_scale, x_scale, out")
+    rc = lib.eplb_expert_wgrad(_f8(dy, "dy"), _dev(dy_scale, torch.float32, "dy_scale"), _f8(x, "x"),
+                               _dev(x_scale, torch.float32, "x_scale"), _dev(offsets, torch.int32, "offsets"), G, R,
+                               Rp, N, C, _dtype(out.dtype, "out"), _dev(out, out.dtype, "out"), _stream(dy.device))
+    _check(rc, "eplb_expert_wgrad")
     return out

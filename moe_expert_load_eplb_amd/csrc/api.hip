@@ -1,6 +1,6 @@
 // C ABI of the EPLB hot path: host-side validation, then launches.
 // Declarations and the meaning of every argument: include/eplb.h.
-#include "eplb.h"
+#include "eplb_check.h"
 #include "eplb_internal.h"
 
 using namespace eplb;
@@ -15,51 +15,6 @@ int32_t check_stream_args(const void* idx, int64_t L, int64_t T, int32_t K, int3
   if (E > kMaxE || L > kMaxLayers) return EPLB_E_LIMIT;
   if (T > kMaxIdsPerLayer / K) return EPLB_E_RANGE;
   return EPLB_OK;
-}
-
-// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte (ends
-// taken in 128 bits, so a range reaching past the address space still
-// compares correctly).
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  if (a == nullptr || b == nullptr || na <= 0 || nb <= 0) return false;
-  const unsigned __int128 x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + (unsigned __int128)nb && y < x + (unsigned __int128)na;
-}
-
-// a * b * c bytes, saturated at 2^63 - 1 (a caller's window of W steps is
-// not bounded above, so its byte count may not fit).
-int64_t bytes_of(int64_t a, int64_t b, int64_t c) {
-  int64_t ab = 0, abc = 0;
-  if (__builtin_mul_overflow(a, b, &ab) || __builtin_mul_overflow(ab, c, &abc)) return INT64_MAX;
-  return abc;
-}
-
-// A call with B problems and these input and output ranges: every pointer
-// set, no output sharing a byte with an input or another output.
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-// No output shares a byte with an input or another output (empty ranges and
-// NULL pointers share nothing; the calls check NULLs themselves).
-template <int NI, int NO>
-int32_t check_disjoint(const Range (&in)[NI], const Range (&out)[NO]) {
-  for (int i = 0; i < NO; ++i) {
-    for (const Range& c : in)
-      if (overlap(out[i].p, out[i].bytes, c.p, c.bytes)) return EPLB_E_ARG;
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return EPLB_E_ARG;
-  }
-  return EPLB_OK;
-}
-
-template <int NI, int NO>
-int32_t check_buffers(const Range (&in)[NI], const Range (&out)[NO]) {
-  for (const Range& a : in)
-    if (a.p == nullptr) return EPLB_E_ARG;
-  for (const Range& a : out)
-    if (a.p == nullptr) return EPLB_E_ARG;
-  return check_disjoint(in, out);
 }
 
 }  // namespace

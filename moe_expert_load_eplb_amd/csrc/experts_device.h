@@ -1,0 +1,83 @@
+// Device code shared by the quantisers and the experts' products.
+#pragma once
+
+#include "experts_internal.h"
+
+namespace eplb {
+
+// A run of rows of one group that a workgroup works on.
+struct Tile {
+  int32_t g;                 // group; G and G + 1: rows of no group; -1: none
+  int32_t index;             // which of the group's tiles
+  int32_t row, rows;         // its rows
+  int32_t before;            // tiles of all groups before this group's
+};
+
+__device__ __forceinline__ int32_t clamp_row(int32_t v, int32_t R) { return v < 0 ? 0 : v > R ? R : v; }
+
+// Tile `want` when every group's rows are cut into tiles of `size` rows, in
+// the order of the groups; with `rest`, the rows behind the last group and
+// those before the first one follow as groups G and G + 1.  Each wave looks
+// at 64 groups at a time.
+__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int32_t G, int32_t R, int32_t size, int32_t want,
+                                          bool rest) {
+  const int lane = threadIdx.x & 63;
+  const int32_t n = rest ? G + 2 : G;
+  int32_t carry = 0;
+  for (int32_t g0 = 0; g0 < n; g0 += 64) {
+    const int32_t g = g0 + lane;
+    int32_t lo = 0, hi = 0;
+    if (g < G) {
+      lo = clamp_row(offsets[g], R);
+      hi = clamp_row(offsets[g + 1], R);
+    } else if (g == G && rest) {
+      lo = clamp_row(offsets[G], R);
+      hi = R;
+    } else if (g == G + 1 && rest) {
+      hi = clamp_row(offsets[0], R);
+    }
+    const int32_t tiles = hi > lo ? (int32_t)(((int64_t)hi - lo + size - 1) / size) : 0;
+    int32_t incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    const int32_t before = carry + incl - tiles;
+    const u64 here = __ballot(want >= before && want < before + tiles);
+    if (here != 0) {
+      const int src = __ffsll((unsigned long long)here) - 1;
+      Tile t;
+      t.g = __shfl(g, src);
+      t.before = __shfl(before, src);
+      t.index = want - t.before;
+      t.row = __shfl(lo, src) + t.index * size;
+      const int32_t left = __shfl(hi, src) - t.row;
+      t.rows = left < size ? left : size;
+      t.g = __builtin_amdgcn_readfirstlane(t.g);
+      t.before = __builtin_amdgcn_readfirstlane(t.before);
+      t.index = __builtin_amdgcn_readfirstlane(t.index);
+      t.row = __builtin_amdgcn_readfirstlane(t.row);
+      t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+      return t;
+    }
+    carry = __builtin_amdgcn_readfirstlane(__shfl(carry + incl, 63));
+  }
+  return Tile{-1, 0, 0, 0, 0};
+}
+
+// Scale of a block whose largest magnitude is amax (NaN: the block holds an
+// infinity or a NaN) and the factor its elements are multiplied with.
+__device__ __forceinline__ float block_scale(float amax, float& factor) {
+  const float a = fmaxf(amax, kAmaxMin);
+  factor = (1.0f / a) * kF8Max;
+  return a * (1.0f / kF8Max);
+}
+
+// Four 32-bit values to 8 bits, nearest, ties to even.
+__device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+}  // namespace eplb
