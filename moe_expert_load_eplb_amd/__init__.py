@@ -3,7 +3,7 @@
 Argument marshalling only: every step of the path runs in the HIP kernels of
 ``libeplb.so``; this module checks dtypes, devices and contiguity, passes raw
 device pointers and the current HIP stream through the C ABI declared in
-``include/eplb.h``, and raises :class:`EplbError` on a non-zero return code.
+``include/eplb.h`` and ``include/eplb_experts.h``, and raises :class:`EplbError` on a non-zero return code.
 PyTorch supplies device memory and streams.
 
 Importing this package loads the library; if it has not been built

@@ -1,7 +1,8 @@
 // C ABI of the router, the grouping and the experts' products: host-side
 // validation, then launches.  Declarations and the meaning of every argument:
-// include/eplb.h.
+// include/eplb_experts.h.
 #include "eplb_check.h"
+#include "eplb_experts.h"
 #include "experts_internal.h"
 
 using namespace eplb;
