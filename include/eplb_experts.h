@@ -35,9 +35,9 @@ extern "C" {
  * experts of the top_groups best groups may be chosen; a group's score is the
  * sum of its group_top (1 or 2) largest keys.  Of the experts left, the K
  * largest keys are chosen, in descending order; equal keys (and equal group
- * scores) go to the lowest index.  A key of minus infinity or NaN is never
- * chosen: where fewer than K experts are left, the remaining ids are -1 and
- * their weights 0.  The weights are the scores, without the bias:
+ * scores) go to the lowest index.  An expert whose logit or key is minus
+ * infinity or NaN is never chosen: where fewer than K experts are left, the
+ * remaining ids are -1 and their weights 0.  The weights are the scores, without the bias:
  *   w[t][k] = scale * s[t][ids[t][k]] / (sum over the chosen of s + 1e-20)
  * or, with normalize = 0, scale * s.  A row whose mask byte is 0 (padding)
  * gets ids -1 and weights 0.
@@ -85,7 +85,8 @@ int32_t eplb_gate(const void* logits, int32_t dtype, int64_t ld, int64_t T, int3
  *   counts     [S][E] int32      out
  *   prob       [S][E] float32    out
  *   tokens     [S] int32         out: n of each segment
- * Other arguments and errors: as for eplb_gate; S is 1 .. 2^20; EPLB_E_ARG
+ * Other arguments and errors: as for eplb_gate; S is 1 .. 2^20 and S * ceil(E
+ * / 64) at most 2^21 (EPLB_E_LIMIT); EPLB_E_ARG
  * also for a workspace that is too small, misaligned, or shares a byte with
  * another array.
  */

@@ -44,7 +44,7 @@ int32_t check_loss(int64_t T, int32_t E, const int32_t* seg, int64_t S, const vo
                    const void* tokens) {
   if (S < 1 || seg == nullptr || loss == nullptr || counts == nullptr || prob == nullptr || tokens == nullptr)
     return EPLB_E_ARG;
-  if (S > kMaxSegments) return EPLB_E_LIMIT;
+  if (S > kMaxSegments || S * ceil_div(E, 64) > kMaxLossParts) return EPLB_E_LIMIT;
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < gate_loss_part_bytes(T, E, S))
     return EPLB_E_ARG;
   return EPLB_OK;
@@ -76,7 +76,7 @@ int32_t eplb_gate(const void* logits, int32_t dtype, int64_t ld, int64_t T, int3
 
 int64_t eplb_gate_loss_workspace_bytes(int64_t T, int32_t E, int64_t S) {
   if (T < 0 || E < 1 || S < 1) return -EPLB_E_ARG;
-  if (T > kMaxTokens || E > kMaxE || S > kMaxSegments) return -EPLB_E_LIMIT;
+  if (T > kMaxTokens || E > kMaxE || S > kMaxSegments || S * ceil_div(E, 64) > kMaxLossParts) return -EPLB_E_LIMIT;
   return gate_loss_part_bytes(T, E, S);
 }
 

@@ -15,6 +15,7 @@ constexpr int64_t kMaxTokens = int64_t(1) << 25;    // tokens of one router call
 constexpr int kMaxK = 64;                           // choices of a token
 constexpr int kMaxGroups = 64;                      // expert groups of the router
 constexpr int64_t kMaxSegments = int64_t(1) << 20;  // segments of one balance loss
+constexpr int64_t kMaxLossParts = int64_t(1) << 21; // runs of 64 experts over all segments (1024 work-items each)
 constexpr int kBlock = 128;                         // elements a scale covers along an axis
 constexpr int kMaxSlots = 8192;                     // slots of a grouping, groups of a product
 constexpr int64_t kMaxDim = int64_t(1) << 24;       // columns of an operand
@@ -55,7 +56,10 @@ struct GateArgs {
   int32_t given;             // ids are an input (no choice is made)
   int32_t* ids;
   float* weights;
+  bool vec;                  // four logits can be loaded at once
   float* part;               // partial sums of the loss
+  float* terms;              // the loss by runs of 64 experts
+  int32_t* ticket;           // workgroups of a segment that are done
   float* loss;
   int32_t* counts;
   float* prob;
@@ -76,6 +80,7 @@ struct GateBackwardArgs {
   const int32_t* tokens;
   const float* d_loss;
   void* d_logits;
+  bool vec, vec_out;         // four logits / gradients at once
 };
 
 int64_t gate_loss_part_bytes(int64_t T, int32_t E, int64_t S);
