@@ -8,11 +8,12 @@
 // every butterfly), 64 for few (shorter chains).
 //
 // What bounds the choice is arithmetic, not memory: an exponential and a
-// division per logit (about 20 instructions), and the selection.  For the K
-// largest of a row: every lane's own largest key goes to LDS; the K-th
-// largest of those bounds the K-th largest key from below, so that only a
-// few more than K keys (11 of 256 for K = 8) can be among the K largest.
-// They are compacted into LDS and ranked by counting.
+// division per logit (about 20 instructions), and the selection, so all of it
+// is free of branches that differ between lanes.  For the K largest of a row:
+// the largest keys of 16 parts of it go to LDS; the K-th largest of those
+// bounds the K-th largest key from below, so that only a few more than K keys
+// (11 of 256 for K = 8) can be among the K largest.  They are compacted into
+// LDS and ranked by counting.
 #include "experts_internal.h"
 
 namespace eplb {
@@ -20,9 +21,11 @@ namespace eplb {
 namespace {
 
 constexpr int kGateThreads = 256;
-constexpr int kLossRows = 32;                // rows of one workgroup of the loss
+constexpr int kLossThreads = 512;
+constexpr int kLossBlocks = 512;             // workgroups of the loss, at most
 constexpr int kV = 4;                        // consecutive experts of a lane
 constexpr int64_t kManyRows = 2048;          // rows from which 16 lanes take one
+constexpr int kParts = 16;                   // parts of a row whose maxima bound the choice
 
 // LDS between lanes of one wave: its own operations stay in order, the
 // compiler has to keep them so.
@@ -35,6 +38,11 @@ __device__ __forceinline__ void wave_sync() {
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), kCtrl, 0xF, 0xF, true));
+}
+
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ int dpp_or_zero(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, kCtrl, kRowMask, 0xF, false);
 }
 
 __device__ __forceinline__ float lane_value(float v, int lane) {
@@ -64,12 +72,33 @@ __device__ __forceinline__ float row_max(float v) {
   return row_reduce<LPR>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// 1 / d correctly rounded, for d >= 1: the hardware's approximation, one
-// Newton step, and Markstein's correction by the remainder, which rounds
-// correctly where no intermediate is denormal.  Half the instructions of the
-// general division, and the same bits.
+// Sum over the row's lanes up to and with this one.
+template <int LPR>
+__device__ __forceinline__ int row_scan(int v) {
+  v += dpp_or_zero<0x111, 0xF>(v);           // row_shr 1, 2, 4, 8
+  v += dpp_or_zero<0x112, 0xF>(v);
+  v += dpp_or_zero<0x114, 0xF>(v);
+  v += dpp_or_zero<0x118, 0xF>(v);
+  if (LPR == 64) {
+    v += dpp_or_zero<0x142, 0xA>(v);         // row_bcast 15 into rows 1 and 3
+    v += dpp_or_zero<0x143, 0xC>(v);         // row_bcast 31 into rows 2 and 3
+  }
+  return v;
+}
+
+// The value of the row's last lane.
+template <int LPR>
+__device__ __forceinline__ int row_last(int v) {
+  if (LPR == 64) return __builtin_amdgcn_readlane(v, 63);
+  return __builtin_amdgcn_mov_dpp(v, 0x15F, 0xF, 0xF, true);   // row_newbcast 15
+}
+
+// 1 / d correctly rounded, for 1 <= d <= 2^126: the hardware's approximation,
+// one Newton step, and Markstein's correction by the remainder, which rounds
+// correctly where no intermediate is denormal (compared with the division for
+// every such d).  Half the instructions of the general division, and the same
+// bits.
 __device__ __forceinline__ float reciprocal(float d) {
-  if (d > 0x1p100f) return 1.0f / d;
   float r = __builtin_amdgcn_rcpf(d);
   r = fmaf(fmaf(-d, r, 1.0f), r, r);
   return fmaf(fmaf(-d, r, 1.0f), r, r);
@@ -78,7 +107,7 @@ __device__ __forceinline__ float reciprocal(float d) {
 // Each step is one correctly rounded 32-bit operation (and the library's
 // exponential), so that a choice between near equal keys does not depend on
 // how the expression is compiled.
-__device__ __forceinline__ float sigmoid(float x) { return reciprocal(1.0f + expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // Expert of value j of a lane.
 template <int LPR>
@@ -86,49 +115,72 @@ __device__ __forceinline__ int expert_of(int j, int lane) {
   return (j / kV * LPR + lane) * kV + j % kV;
 }
 
-// A row's logits in 32 bits; experts past E hold minus infinity.
+// A row's logits in 32 bits; experts past E hold minus infinity.  `on`:
+// whether the row is read at all.  vec: E and the rows' addresses are
+// multiples of four logits.
 template <int LPR, int VPL>
-__device__ __forceinline__ void load_logits(const void* logits, int32_t dtype, bool vec, int64_t at, int32_t E,
+__device__ __forceinline__ void load_logits(const void* logits, int32_t dtype, bool vec, int64_t at, int32_t E, bool on,
                                             int lane, float (&x)[VPL]) {
+  if (!on) at = 0;                           // row 0 is always there
+  const int end = on ? E : 0;
+  if (vec) {
+    if (dtype == kF32) {
+      const float* p = static_cast<const float*>(logits) + at;
 #pragma unroll
-  for (int j = 0; j < VPL; j += kV) {
-    const int e = expert_of<LPR>(j, lane);
-    if (vec && e + kV <= E) {
-      if (dtype == kF32) {
-        const f32x4 f = *reinterpret_cast<const f32x4*>(static_cast<const float*>(logits) + at + e);
+      for (int j = 0; j < VPL; j += kV) {
+        const f32x4 f = *reinterpret_cast<const f32x4*>(p + min(expert_of<LPR>(j, lane), E - kV));
 #pragma unroll
-        for (int i = 0; i < kV; ++i) x[j + i] = f[i];
-      } else {
-        const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const u16*>(logits) + at + e);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const u16 v = (u16)((i < 2 ? h.x : h.y) >> (16 * (i & 1)));
-          x[j + i] = dtype == kBf16 ? bf16_to_float(v) : f16_to_float(v);
-        }
+        for (int k = 0; k < kV; ++k) x[j + k] = f[k];
       }
     } else {
+      const u16* p = static_cast<const u16*>(logits) + at;
+      uint2 h[VPL / kV];
 #pragma unroll
-      for (int i = 0; i < kV; ++i) x[j + i] = e + i < E ? load_as_float(logits, dtype, at + e + i) : -INFINITY;
+      for (int j = 0; j < VPL; j += kV)
+        h[j / kV] = *reinterpret_cast<const uint2*>(p + min(expert_of<LPR>(j, lane), E - kV));
+      if (dtype == kBf16) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+          const uint32_t w = j % kV < 2 ? h[j / kV].x : h[j / kV].y;
+          x[j] = __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) x[j] = f16_to_float((u16)((j % kV < 2 ? h[j / kV].x : h[j / kV].y) >> (16 * (j & 1))));
+      }
     }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) x[j] = expert_of<LPR>(j / kV * kV, lane) < end ? x[j] : -INFINITY;
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) x[j] = load_as_float(logits, dtype, at + min(expert_of<LPR>(j, lane), E - 1));
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) x[j] = expert_of<LPR>(j, lane) < end ? x[j] : -INFINITY;
   }
 }
 
 // Scores of a row.  Returns what a share of the balance loss is multiplied
 // with (softmax: 1; sigmoid: 1 / (sum of the scores + 1e-20)); softmax also
-// leaves the row's maximum and 1 / (its sum + 1e-20), sigmoid the sum.
+// leaves the row's maximum and 1 / (its sum + 1e-20).
 template <int LPR, int VPL>
-__device__ __forceinline__ float scores(int32_t scoring, int32_t E, int lane, const float (&x)[VPL], float (&s)[VPL],
-                                        float& m, float& z) {
+__device__ __forceinline__ float scores(int32_t scoring, const float (&x)[VPL], float (&s)[VPL], float& m, float& z) {
   if (scoring == kSigmoid) {
-    z = 0.0f;
-    m = 0.0f;
+    m = z = 0.0f;
+    bool far = false;                        // some logit is below -87
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      s[j] = expert_of<LPR>(j, lane) < E ? sigmoid(x[j]) : 0.0f;
-      z += s[j];
+      const float d = 1.0f + expf(-x[j]);
+      const float r = reciprocal(d);
+      s[j] = x[j] == -INFINITY ? 0.0f : r;
+      far |= (d > 0x1p126f) & (x[j] > -INFINITY);
     }
-    z = row_sum<LPR>(z) + kScoreEps;
-    return 1.0f / z;
+    if (__any(far)) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) s[j] = sigmoid(x[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) z += s[j];
+    return 1.0f / (row_sum<LPR>(z) + kScoreEps);
   }
   m = -INFINITY;
 #pragma unroll
@@ -147,149 +199,179 @@ __device__ __forceinline__ float scores(int32_t scoring, int32_t E, int lane, co
   return 1.0f;
 }
 
-// LDS of one row: its keys for the group scores, the lanes' largest keys and
-// the candidates of the choice.  The keys share their place with the rest.
-constexpr int row_lds_words(int LPR) { return LPR * 2 + LPR * 2 * 3; }
+// The two largest of both pairs, each in order.
+__device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
+  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+  a1 = fmaxf(a1, b1);
+}
+
+template <int kCtrl>
+__device__ __forceinline__ void merge2_dpp(float& a1, float& a2) {
+  const float b1 = dpp<kCtrl>(a1), b2 = dpp<kCtrl>(a2);
+  merge2(a1, a2, b1, b2);
+}
+
+constexpr int kGroupWords = kMaxGroups + 4;  // LDS words of the groups' scores
 
 // Keys of the experts outside the top_groups best groups become minus
-// infinity.  The row's keys pass through LDS so that lane g can scan group g;
-// the scans start at different places, as the groups' starts may share a bank.
+// infinity.  The groups' scores meet in LDS; lane g then ranks group g.
 template <int LPR, int VPL>
 __device__ __forceinline__ void limit_groups(const GateArgs& a, int lane, float* row, float (&key)[VPL]) {
   constexpr int kC = kMaxGroups / LPR;
+  const int size = a.E / a.G;
+  const int lanes = size / kV;               // lanes of a group, where it has whole ones
+  const bool whole = size % kV == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0;
+  auto score = [&](float b1, float b2) {
+    const float v = a.group_top == 2 ? b1 + b2 : b1;
+    return v == v ? v : -INFINITY;           // +infinity and -infinity met
+  };
+  if (lane < 4) row[a.G + lane] = -INFINITY; // the scores are read by fours
+  if (whole) {
+    // a group is `lanes` neighbouring lanes in one turn of the row
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = expert_of<LPR>(j, lane);
-    if (e < a.E) row[e] = key[j];
+    for (int j = 0; j < VPL; j += kV) {
+      float b1 = fmaxf(key[j], key[j + 1]), b2 = fminf(key[j], key[j + 1]);
+      merge2(b1, b2, fmaxf(key[j + 2], key[j + 3]), fminf(key[j + 2], key[j + 3]));
+      if (lanes > 1) merge2_dpp<0xB1>(b1, b2);
+      if (lanes > 2) merge2_dpp<0x4E>(b1, b2);
+      if (lanes > 4) merge2_dpp<0x141>(b1, b2);
+      if (lanes > 8) merge2_dpp<0x140>(b1, b2);
+      const int e = expert_of<LPR>(j, lane);
+      if (e < a.E) row[fastdiv_apply((uint32_t)e, a.fd_group)] = score(b1, b2);
+    }
+  } else {
+    // group g by lane g, through LDS; the scans start at different places, as
+    // the groups' starts may share a bank
+    float* keys = row + kGroupWords;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int e = expert_of<LPR>(j, lane);
+      if (e < a.E) keys[e] = key[j];
+    }
+    wave_sync();
+    for (int g = lane; g < a.G; g += LPR) {
+      float b1 = -INFINITY, b2 = -INFINITY;
+      const int first = g % size;
+#pragma unroll 4
+      for (int n = 0; n < size; ++n) {
+        const int i = first + n;
+        merge2(b1, b2, keys[g * size + (i < size ? i : i - size)], -INFINITY);
+      }
+      row[g] = score(b1, b2);
+    }
   }
   wave_sync();
-  const int size = a.E / a.G;
   u64 keep = 0;
-  float score[kC];                           // of group c * LPR + lane
 #pragma unroll
   for (int c = 0; c < kC; ++c) {
-    score[c] = -INFINITY;
-    if (c * LPR >= a.G) continue;
+    if (c * LPR >= a.G) break;
     const int g = c * LPR + lane;
-    float b1 = -INFINITY, b2 = -INFINITY;
-    if (g < a.G) {
-      int i = g % size;
-      for (int n = 0; n < size; ++n) {
-        const float v = row[g * size + i];
-        i = i + 1 < size ? i + 1 : 0;
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
-      }
-    }
-    const float sum = a.group_top == 2 ? b1 + b2 : b1;
-    score[c] = sum != sum ? -INFINITY : sum;
-  }
-#pragma unroll
-  for (int c = 0; c < kC; ++c) {
-    if (c * LPR >= a.G) continue;
-    const int g = c * LPR + lane;
+    const float own = row[min(g, a.G)];
     int before = 0;
+    for (int i = 0; i < a.G; i += 4) {
+      const f32x4 o = *reinterpret_cast<const f32x4*>(row + i);
 #pragma unroll
-    for (int d = 0; d < kC; ++d) {
-      const int n = min(LPR, a.G - d * LPR);
-      for (int i = 0; i < n; ++i) {
-        const float o = __shfl(score[d], i, LPR);
-        before += o > score[c] || (o == score[c] && d * LPR + i < g);
-      }
+      for (int u = 0; u < 4; ++u) before += (int)(o[u] > own) | ((int)(o[u] == own) & (int)(i + u < g));
     }
     const u64 all = __ballot(g < a.G && before < a.top_groups);
     const int shift = (threadIdx.x & 63) / LPR * LPR;
     const u64 mine = LPR == 64 ? all : (all >> shift) & ((u64(1) << (LPR & 63)) - 1);
     keep |= mine << (c * LPR & 63);
   }
+  if (whole) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = expert_of<LPR>(j, lane);
-    const int g = (int)fastdiv_apply((uint32_t)e, a.fd_group);
-    if (e < a.E && !(keep >> g & 1)) key[j] = -INFINITY;
+    for (int j = 0; j < VPL; j += kV) {
+      const uint32_t g = fastdiv_apply((uint32_t)expert_of<LPR>(j, lane), a.fd_group);
+      const bool in = keep >> (g & 63) & 1;  // experts past E hold minus infinity already
+#pragma unroll
+      for (int k = 0; k < kV; ++k) key[j + k] = in ? key[j + k] : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const uint32_t g = fastdiv_apply((uint32_t)expert_of<LPR>(j, lane), a.fd_group);
+      key[j] = keep >> (g & 63) & 1 ? key[j] : -INFINITY;
+    }
   }
-  wave_sync();                               // the keys' place is used again
+  wave_sync();                               // the place is used again
 }
 
+// LDS words of the choice of one row (kCap candidates, a place for what is
+// none, their scores, the parts' maxima).
+constexpr int choose_cap(int LPR) { return LPR == 16 ? 48 : 64; }
+constexpr int choose_lds_words(int LPR) { return choose_cap(LPR) * 3 + 4 + kParts; }
+
 // The choice of a row: the K largest keys above minus infinity, ties to the
-// lowest expert.  Calls put(rank, expert, score, in) for this lane's share of
-// the ranks; in: whether the rank has an expert.  The lanes that call put
-// cover every rank below K once.
+// lowest expert.  Calls put(slot, rank, expert, score, in) for this lane's
+// share of the ranks, at most one per slot (below kSlots); in: whether the rank has an
+// expert.  The row's lanes cover every rank below K once.
 template <int LPR, int VPL, typename Put>
 __device__ __forceinline__ void choose(int32_t K, int lane, float* row, float (&key)[VPL], const float (&s)[VPL],
                                        Put put) {
-  constexpr int kCap = 2 * LPR;
-  u64* cand = reinterpret_cast<u64*>(row);   // [kCap] ordered key above the complement of the expert
-  float* cand_s = row + 2 * kCap;            // [kCap] scores
-  u64* top = reinterpret_cast<u64*>(row + 3 * kCap);   // [LPR] the lanes' largest
-  if (K <= LPR) {
-    // floats as integers of the same order; -0 counts as 0
-    auto ordered = [](float v, int e) {
-      const uint32_t b = __float_as_uint(v + 0.0f);
-      const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-      return (u64)o << 32 | (uint32_t)~e;
-    };
-    float best = -INFINITY;
-    int be = 0;
+  constexpr int kCap = choose_cap(LPR), kSlots = kCap / LPR;
+  u64* cand = reinterpret_cast<u64*>(row);   // [kCap + 1] ordered key above the complement of the expert
+  float* cand_s = row + 2 * kCap + 2;        // [kCap + 1] scores
+  float* top = row + 3 * kCap + 4;           // [kParts]
+  if (K <= kParts) {
+    float best = key[0];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (key[j] > best) best = key[j], be = expert_of<LPR>(j, lane);
-    const u64 mine = ordered(best, be);
-    top[lane] = mine;
+    for (int j = 1; j < VPL; ++j) best = fmaxf(best, key[j]);
+    if (LPR == 64) {                         // lanes l, l + 16, l + 32 and l + 48 make a part
+      best = fmaxf(best, __shfl_xor(best, 16));
+      best = fmaxf(best, __shfl_xor(best, 32));
+    }
+    top[lane % kParts] = best;
+#pragma unroll
+    for (int i = 0; i < kCap; i += LPR) cand[i + lane] = 0;
     wave_sync();
-    int before = 0;
+    int above = 0;                           // parts whose maximum is as large
 #pragma unroll
-    for (int i = 0; i < LPR; ++i) before += top[i] > mine;
-    // lane maxima differ unless both are minus infinity; then the bound is that
-    const u64 at_rank = __ballot(before == K - 1 && best > -INFINITY);
-    const int shift = (threadIdx.x & 63) / LPR * LPR;
-    const u64 in_row = LPR == 64 ? at_rank : (at_rank >> shift) & ((u64(1) << (LPR & 63)) - 1);
-    const int src = in_row != 0 ? __ffsll((unsigned long long)in_row) - 1 : 0;
-    const float bound = in_row != 0 ? __shfl(best, src, LPR) : -INFINITY;
-    const int bound_e = __shfl(be, src, LPR);
+    for (int i = 0; i < kParts; ++i) above += top[i] >= best;
+    const float bound = fmaxf(row_max<LPR>(above >= K ? best : -INFINITY), -3.4028235e38f);
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      n += key[j] > bound || (key[j] == bound && bound > -INFINITY && expert_of<LPR>(j, lane) <= bound_e);
-    int incl = n;
-#pragma unroll
-    for (int d = 1; d < LPR; d <<= 1) {
-      const int v = __shfl_up(incl, d, LPR);
-      if (lane >= d) incl += v;
-    }
-    const int total = __shfl(incl, LPR - 1, LPR);
+    for (int j = 0; j < VPL; ++j) n += key[j] >= bound;
+    const int incl = row_scan<LPR>(n);
+    const int total = row_last<LPR>(incl);
     if (!__any(total > kCap)) {
       int at = incl - n;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        const int e = expert_of<LPR>(j, lane);
-        if (key[j] > bound || (key[j] == bound && bound > -INFINITY && e <= bound_e)) {
-          cand[at] = ordered(key[j], e);
-          cand_s[at] = s[j];
-          ++at;
-        }
+        // floats as integers of the same order; -0 counts as 0
+        const uint32_t b = __float_as_uint(key[j] + 0.0f);
+        const uint32_t o = b ^ (uint32_t)((int32_t)b >> 31 | (int32_t)0x80000000);
+        const bool in = key[j] >= bound;
+        const int to = in ? at : kCap;
+        cand[to] = (u64)o << 32 | (uint32_t)~expert_of<LPR>(j, lane);
+        cand_s[to] = s[j];
+        at += in;
       }
       wave_sync();
       int most = total;
+      if (LPR == 16)
+        most = max(max(__builtin_amdgcn_readlane(total, 0), __builtin_amdgcn_readlane(total, 16)),
+                   max(__builtin_amdgcn_readlane(total, 32), __builtin_amdgcn_readlane(total, 48)));
+      most = __builtin_amdgcn_readfirstlane(most);
 #pragma unroll
-      for (int d = LPR; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (c * LPR >= most) break;
+      for (int c = 0; c < kSlots; ++c) {
         const int i = c * LPR + lane;
-        const u64 own = i < total ? cand[i] : 0;
+        if (c * LPR >= most) break;
+        const u64 own = cand[i];
         int rank = 0;
-        for (int o = 0; o < most; ++o) rank += o < total && cand[o] > own;
-        if (i < total && rank < K) put(rank, (int)~(uint32_t)own, cand_s[i], true);
+        for (int o = 0; o < most; o += 4) {  // kCap is a multiple of 4, unused places are 0
+#pragma unroll
+          for (int u = 0; u < 4; ++u) rank += cand[o + u] > own;
+        }
+        if (i < total && rank < K) put(c, rank, (int)~(uint32_t)own, cand_s[i], true);
       }
-      if (lane >= total && lane < K) put(lane, -1, 0.0f, false);
+      if (lane >= total && lane < K) put(kSlots - 1, lane, -1, 0.0f, false);
       wave_sync();
       return;
     }
     wave_sync();
   }
-  // one by one: more choices than lanes, or more candidates than places (many
-  // equal keys, or fewer lanes than K with any key at all)
+  // one by one: more choices than parts, or more candidates than places (many
+  // equal keys, or fewer parts than K with any key at all)
   for (int k = 0; k < K; ++k) {
     float best = -INFINITY, bs = 0.0f;
     int be = 1 << 30;
@@ -305,7 +387,7 @@ __device__ __forceinline__ void choose(int32_t K, int lane, float* row, float (&
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
       if (expert_of<LPR>(j, lane) == be) key[j] = -INFINITY;
-    if (lane == k % LPR) put(k, best > -INFINITY ? be : -1, bs, best > -INFINITY);
+    if (lane == k % LPR) put(0, k, best > -INFINITY ? be : -1, bs, best > -INFINITY);
   }
 }
 
@@ -315,51 +397,66 @@ template <int LPR, int VPL, bool LOSS>
 __device__ __forceinline__ void gate_row(const GateArgs& a, int64_t t, bool real, int lane, float* row, int32_t* cnt,
                                          float (&psum)[VPL]) {
   float x[VPL], s[VPL], m, z;
-  load_logits<LPR, VPL>(a.logits, a.dtype, a.vec, t * a.ld, real ? a.E : 0, lane, x);
-  const float rz = scores<LPR, VPL>(a.scoring, a.E, lane, x, s, m, z);
-  if (LOSS && real) {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) psum[j] += s[j] * rz;
-  }
-  if (LOSS && a.given) {
-    if (real)
-      for (int k = lane; k < a.K; k += LPR) {
-        const int32_t e = a.ids[t * a.K + k];
-        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&cnt[e], 1);
-      }
-    return;
-  }
+  load_logits<LPR, VPL>(a.logits, a.dtype, a.vec, t * a.ld, a.E, real, lane, x);
   float key[VPL];
 #pragma unroll
+  for (int j = 0; j < VPL; ++j) key[j] = 0.0f;
+  if (a.bias != nullptr) {
+if (a.vec) {
+#pragma unroll
+      for (int j = 0; j < VPL; j += kV) {
+        const f32x4 b = *reinterpret_cast<const f32x4*>(a.bias + min(expert_of<LPR>(j, lane), a.E - kV));
+#pragma unroll
+        for (int k = 0; k < kV; ++k) key[j + k] = b[k];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) key[j] = a.bias[min(expert_of<LPR>(j, lane), a.E - 1)];
+    }
+  }
+  const float rz = scores<LPR, VPL>(a.scoring, x, s, m, z);
+  if (LOSS) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) psum[j] += real ? s[j] * rz : 0.0f;
+    if (a.given) {
+      if (real)
+        for (int k = lane; k < a.K; k += LPR) {
+          const int32_t e = a.ids[t * a.K + k];
+          if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&cnt[e], 1);
+        }
+      return;
+    }
+  }
+#pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const int e = expert_of<LPR>(j, lane);
-    float v = a.scoring == kSigmoid ? s[j] : x[j];
-    if (a.bias != nullptr && e < a.E) v += a.bias[e];
-    key[j] = e < a.E && real && x[j] > -INFINITY && v == v ? v : -INFINITY;
+    const float v = (a.scoring == kSigmoid ? s[j] : x[j]) + key[j];
+    key[j] = ((x[j] > -INFINITY) & (v == v)) ? v : -INFINITY;
   }
   if (a.top_groups < a.G) limit_groups<LPR, VPL>(a, lane, row, key);
-  // a lane holds at most two ranks (K <= LPR)
-  float chosen = 0.0f, kept[2] = {0.0f, 0.0f};
-  int at[2] = {-1, -1};
+  constexpr int kSlots = choose_cap(LPR) / LPR;
+  float kept[kSlots], chosen = 0.0f;
+  int at[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) kept[i] = 0.0f, at[i] = -1;
   const int64_t out = t * a.K;
   const bool inside = t < a.T;
-  choose<LPR, VPL>(a.K, lane, row, key, s, [&](int k, int e, float v, bool in) {
-    if (!inside) return;
-    a.ids[out + k] = e;
-    if (LOSS && in) atomicAdd(&cnt[e], 1);
-    chosen += v;
-    if (at[0] < 0) at[0] = k, kept[0] = v;
-    else at[1] = k, kept[1] = v;
+  choose<LPR, VPL>(a.K, lane, row, key, s, [&](int slot, int k, int e, float v, bool in) {
+    if (inside) a.ids[out + k] = e;
+    if (LOSS && in && inside) atomicAdd(&cnt[e], 1);
+    at[slot] = inside ? k : -1;
+    kept[slot] = v;
   });
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) chosen += kept[i];
   const float sum = a.normalize ? row_sum<LPR>(chosen) + kScoreEps : 1.0f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < kSlots; ++i)
     if (at[i] >= 0) a.weights[out + at[i]] = a.normalize ? a.scale * kept[i] / sum : a.scale * kept[i];
 }
 
 template <int LPR, int VPL>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a, int32_t row_words) {
-  extern __shared__ float lds[];             // [rows at once][row_words]
+  extern __shared__ __attribute__((aligned(16))) float lds[];             // [rows at once][row_words]
   constexpr int kRows = kGateThreads / LPR;
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const int64_t t = (int64_t)blockIdx.x * kRows + sub;
@@ -388,26 +485,32 @@ __device__ __forceinline__ int64_t piece_end(const int32_t* seg, int64_t S, int6
 // Floats of one partial sum: E sums of shares, E counts, the rows counted.
 __host__ __device__ inline int64_t part_stride(int32_t E) { return (2 * (int64_t)E + 1 + 3) / 4 * 4; }
 
-// Workgroup c takes rows c * kLossRows on, piece by piece where a segment
-// ends.  The piece of segment s goes to partial sum c + s: two pieces never
+// Rows of one workgroup of the loss: one row to a lane group where there are
+// few, else as many as make kLossBlocks workgroups (and partial sums).
+int32_t loss_chunk(int64_t T) {
+  const int64_t least = kLossThreads / (T >= kManyRows ? 16 : 64);
+  return (int32_t)std::max<int64_t>(least, ceil_div(ceil_div(T, kLossBlocks), least) * least);
+}
+
+// Workgroup c takes rows c * chunk on, piece by piece where a segment ends.  The piece of segment s goes to partial sum c + s: two pieces never
 // share one, as each next piece has a larger c or a larger s.
 template <int LPR, int VPL>
-__global__ __launch_bounds__(kGateThreads) void gate_loss_kernel(GateArgs a, int32_t row_words) {
-  extern __shared__ float lds[];             // [rows at once][row_words]: the choice's, then shares; [E] counts
-  constexpr int kRows = kGateThreads / LPR;
+__global__ __launch_bounds__(kLossThreads) void gate_loss_kernel(GateArgs a, int32_t row_words, int32_t chunk) {
+  extern __shared__ __attribute__((aligned(16))) float lds[];             // [rows at once][row_words]: the choice's, then shares; [E] counts
+  constexpr int kRows = kLossThreads / LPR;
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   float* row = lds + sub * row_words;
   int32_t* cnt = reinterpret_cast<int32_t*>(lds + kRows * row_words);
   __shared__ int32_t kept;
   // the reduction's tickets (behind the partial sums) start at zero
-  for (int64_t s = (int64_t)blockIdx.x * kGateThreads + threadIdx.x; s < a.S; s += (int64_t)gridDim.x * kGateThreads)
+  for (int64_t s = (int64_t)blockIdx.x * kLossThreads + threadIdx.x; s < a.S; s += (int64_t)gridDim.x * kLossThreads)
     a.ticket[s] = 0;
-  const int64_t row0 = (int64_t)blockIdx.x * kLossRows;
-  const int64_t row1 = row0 + kLossRows < a.T ? row0 + kLossRows : a.T;
+  const int64_t row0 = (int64_t)blockIdx.x * chunk;
+  const int64_t row1 = row0 + chunk < a.T ? row0 + chunk : a.T;
   for (int64_t r = row0; r < row1;) {
     const int64_t s = segment_of(a.seg, a.S, r);
     const int64_t end = piece_end(a.seg, a.S, s, r, row1);
-    for (int e = threadIdx.x; e < a.E; e += kGateThreads) cnt[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += kLossThreads) cnt[e] = 0;
     if (threadIdx.x == 0) kept = 0;
     __syncthreads();
     float psum[VPL];
@@ -430,7 +533,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_loss_kernel(GateArgs a, int
         if (e < a.E) row[e] = psum[j];
       }
       __syncthreads();
-      for (int e = threadIdx.x; e < a.E; e += kGateThreads) {
+      for (int e = threadIdx.x; e < a.E; e += kLossThreads) {
         float v = 0.0f;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) v += lds[i * row_words + e];
@@ -450,7 +553,7 @@ constexpr int kReduceParts = kReduceThreads / 64;    // partial sums read at onc
 // 64 experts of segment s: wave w adds the partial sums w, w + 16, ... in
 // order, then the 16 sums are added in order.  The last workgroup of a segment
 // (by a ticket) adds the loss's terms, in the order of the experts.
-__global__ __launch_bounds__(kReduceThreads) void gate_loss_reduce_kernel(GateArgs a, int32_t parts) {
+__global__ __launch_bounds__(kReduceThreads) void gate_loss_reduce_kernel(GateArgs a, int32_t parts, int32_t chunk) {
   __shared__ float sums[kReduceParts][64];
   __shared__ int32_t counts[kReduceParts][64];
   __shared__ int32_t rows[kReduceParts];
@@ -460,18 +563,29 @@ __global__ __launch_bounds__(kReduceThreads) void gate_loss_reduce_kernel(GateAr
   int64_t lo = a.seg[s], hi = a.seg[s + 1];
   if (lo < 0) lo = 0;
   if (hi > a.T) hi = a.T;
-  const int64_t c0 = lo / kLossRows, c1 = hi > lo ? (hi - 1) / kLossRows + 1 : c0;
+  const int32_t c0 = (int32_t)(lo / chunk), c1 = hi > lo ? (int32_t)((hi - 1) / chunk) + 1 : c0;
   const int64_t stride = part_stride(a.E);
+  const int at = e < a.E ? e : a.E - 1;
   float p = 0.0f;
   int32_t k = 0, n = 0;
-#pragma unroll 4
-  for (int64_t c = c0 + wave; c < c1; c += kReduceParts) {
-    const float* part = a.part + (c + s) * stride;
-    if (e < a.E) {
-      p += part[e];
-      k += reinterpret_cast<const int32_t*>(part)[a.E + e];
+  for (int32_t c = c0 + wave; c < c1; c += 8 * kReduceParts) {
+    float vp[8];
+    int32_t vk[8], vn[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {            // all loads in flight at once; past the end the last one again
+      const int32_t cc = c + u * kReduceParts;
+      const float* part = a.part + (min(cc, c1 - 1) + s) * stride;
+      vp[u] = part[at];
+      vk[u] = reinterpret_cast<const int32_t*>(part)[a.E + at];
+      vn[u] = reinterpret_cast<const int32_t*>(part)[2 * a.E];
     }
-    n += reinterpret_cast<const int32_t*>(part)[2 * a.E];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = c + u * kReduceParts < c1;
+      p += in ? vp[u] : 0.0f;
+      k += in ? vk[u] : 0;
+      n += in ? vn[u] : 0;
+    }
   }
   sums[wave][lane] = p;
   counts[wave][lane] = k;
@@ -518,7 +632,7 @@ template <int LPR, int VPL>
 __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwardArgs a, int32_t per_group) {
   extern __shared__ float grads[];           // [rows at once][E rounded up to 4], zero but for the row in work
   constexpr int kRows = kGateThreads / LPR;
-  constexpr int kC = LPR == 64 ? 1 : kMaxK / LPR;
+  constexpr int kC = 1;                      // K <= LPR
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   float* grad = grads + sub * ((a.E + 3) / 4 * 4 + 4);
 #pragma unroll
@@ -533,7 +647,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
     const bool inside = t < a.T;
     const bool real = inside && (a.mask == nullptr || a.mask[t] != 0);
     float x[VPL], s[VPL], m, z;
-    load_logits<LPR, VPL>(a.logits, a.dtype, a.vec, t * a.ld, real ? a.E : 0, lane, x);
+    load_logits<LPR, VPL>(a.logits, a.dtype, a.vec, t * a.ld, a.E, real, lane, x);
     int32_t id[kC];
     float gk[kC], xk[kC];
     if (a.d_weights != nullptr) {
@@ -558,12 +672,11 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
         coef[j] = has && e < a.E ? f * (float)a.counts[sg * a.E + e] : 0.0f;
       }
     }
-    const float rz = scores<LPR, VPL>(a.scoring, a.E, lane, x, s, m, z);
+    const float rz = scores<LPR, VPL>(a.scoring, x, s, m, z);
     if (a.d_weights != nullptr) {
       float sk[kC], D = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
-        if (c * LPR >= a.K) break;
         sk[c] = id[c] < 0 ? 0.0f : a.scoring == kSigmoid ? sigmoid(xk[c]) : expf(xk[c] - m) * z;
         D += sk[c];
         dot += gk[c] * sk[c];
@@ -574,23 +687,33 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
 #pragma unroll
         for (int c = 0; c < kC; ++c) gk[c] = id[c] >= 0 ? (gk[c] - dot) * rd : 0.0f;
       }
-      // an expert named twice gets the sum of both, taken in the order of k
+      // the chosen experts' gradients through LDS; an expert named twice (its
+      // place then holds another lane's mark) gets the sum in the order of k
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        if (c * LPR >= a.K) break;
-        float g = 0.0f;
-#pragma unroll
-        for (int d = 0; d < kC; ++d) {
-          const int n = min(LPR, a.K - d * LPR);
-          for (int q = 0; q < n; ++q) {
-            const int om = __shfl(id[d], q, LPR);
-            const float og = __shfl(gk[d], q, LPR);
-            if (om == id[c]) g += og;
-          }
-        }
-        if (id[c] >= 0) grad[id[c]] = g;
-      }
+      for (int c = 0; c < kC; ++c)
+        if (id[c] >= 0) grad[id[c]] = __int_as_float(c * LPR + lane);
       wave_sync();
+      bool twice = false;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) twice |= id[c] >= 0 && __float_as_int(grad[id[c] < 0 ? 0 : id[c]]) != c * LPR + lane;
+      wave_sync();
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        if (id[c] >= 0) grad[id[c]] = gk[c];
+      wave_sync();
+      if (__any(twice)) {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (id[c] >= 0) grad[id[c]] = 0.0f;
+        wave_sync();
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll 1
+          for (int k = 0; k < LPR; ++k) {
+            if (lane == k && id[c] >= 0) grad[id[c]] += gk[c];
+            wave_sync();
+          }
+      }
     }
     float g[VPL], dot = 0.0f;
 #pragma unroll
@@ -602,7 +725,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
       wave_sync();
 #pragma unroll
       for (int c = 0; c < kC; ++c)
-        if (c * LPR < a.K && id[c] >= 0) grad[id[c]] = 0.0f;
+        if (id[c] >= 0) grad[id[c]] = 0.0f;
       wave_sync();
     }
     if (a.scoring == kSigmoid) {
@@ -669,28 +792,29 @@ hipError_t by_width(int64_t T, int32_t E, int32_t K, F f) {
   return f(L64(), std::integral_constant<int, 64>());
 }
 
-// LDS words of a row in the choice; rows start 8 banks apart.
+// LDS words of a row in the choice: its group scores and keys, or its
+// candidates; rows start 8 banks apart.
 int32_t choice_words(int lpr, int32_t E, bool groups) {
-  const int32_t n = std::max(row_lds_words(lpr), groups ? E : 0);
+  const int32_t n = std::max(choose_lds_words(lpr), groups ? kGroupWords + E : 0);
   return (n + 31) / 32 * 32 + 8;
 }
 
 int64_t loss_parts(int32_t E) { return ceil_div(E, 64); }
 
-bool aligned4(const void* p, int32_t dtype, int64_t ld) {
-  return ((uintptr_t)p & (uintptr_t)(4 * dtype_size(dtype) - 1)) == 0 && ld % 4 == 0;
+bool aligned4(const void* p, int32_t dtype, int64_t ld, int32_t E) {
+  return ((uintptr_t)p & (uintptr_t)(4 * dtype_size(dtype) - 1)) == 0 && ld % 4 == 0 && E % 4 == 0;
 }
 
 }  // namespace
 
 int64_t gate_loss_part_bytes(int64_t T, int32_t E, int64_t S) {
-  return ((ceil_div(T, kLossRows) + S) * part_stride(E) + S * (loss_parts(E) + 1)) * 4;
+  return ((ceil_div(T, loss_chunk(T)) + S) * part_stride(E) + S * (loss_parts(E) + 1)) * 4;
 }
 
 hipError_t launch_gate(const GateArgs& args, hipStream_t stream) {
   if (args.T == 0) return hipSuccess;
   GateArgs a = args;
-  a.vec = aligned4(a.logits, a.dtype, a.ld);
+  a.vec = aligned4(a.logits, a.dtype, a.ld, a.E) && aligned4(a.bias, kF32, a.E, a.E);
   return by_width(a.T, a.E, a.K, [&](auto lpr, auto vpl) {
     constexpr int LPR = decltype(lpr)::value, VPL = decltype(vpl)::value, kRows = kGateThreads / LPR;
     const int32_t words = choice_words(LPR, a.E, a.top_groups < a.G);
@@ -702,27 +826,29 @@ hipError_t launch_gate(const GateArgs& args, hipStream_t stream) {
 
 hipError_t launch_gate_loss(const GateArgs& args, hipStream_t stream) {
   GateArgs a = args;
-  a.vec = aligned4(a.logits, a.dtype, a.ld);
+  a.vec = aligned4(a.logits, a.dtype, a.ld, a.E) && aligned4(a.bias, kF32, a.E, a.E);
   const int64_t parts = loss_parts(a.E);
-  a.terms = a.part + (ceil_div(a.T, kLossRows) + a.S) * part_stride(a.E);
+  a.terms = a.part + (ceil_div(a.T, loss_chunk(a.T)) + a.S) * part_stride(a.E);
   a.ticket = reinterpret_cast<int32_t*>(a.terms + a.S * parts);
   const hipError_t err = by_width(a.T, a.E, a.K, [&](auto lpr, auto vpl) {
-    constexpr int LPR = decltype(lpr)::value, VPL = decltype(vpl)::value, kRows = kGateThreads / LPR;
+    constexpr int LPR = decltype(lpr)::value, VPL = decltype(vpl)::value, kRows = kLossThreads / LPR;
     const int32_t words = choice_words(LPR, a.E, true);      // the shares' sums pass through the same place
-    const unsigned grid = (unsigned)std::max<int64_t>(1, ceil_div(a.T, kLossRows));
-    gate_loss_kernel<LPR, VPL><<<dim3(grid), dim3(kGateThreads), ((size_t)kRows * words + a.E) * 4, stream>>>(a, words);
+    const unsigned grid = (unsigned)std::max<int64_t>(1, ceil_div(a.T, loss_chunk(a.T)));
+    gate_loss_kernel<LPR, VPL><<<dim3(grid), dim3(kLossThreads), ((size_t)kRows * words + a.E) * 4, stream>>>(
+        a, words, loss_chunk(a.T));
     return hipGetLastError();
   });
   if (err != hipSuccess) return err;
-  gate_loss_reduce_kernel<<<dim3((unsigned)(a.S * parts)), dim3(kReduceThreads), 0, stream>>>(a, (int32_t)parts);
+  gate_loss_reduce_kernel<<<dim3((unsigned)(a.S * parts)), dim3(kReduceThreads), 0, stream>>>(a, (int32_t)parts,
+                                                                                              loss_chunk(a.T));
   return hipGetLastError();
 }
 
 hipError_t launch_gate_backward(const GateBackwardArgs& args, hipStream_t stream) {
   if (args.T == 0) return hipSuccess;
   GateBackwardArgs a = args;
-  a.vec = aligned4(a.logits, a.dtype, a.ld);
-  a.vec_out = aligned4(a.d_logits, a.dtype, a.E);
+  a.vec = aligned4(a.logits, a.dtype, a.ld, a.E);
+  a.vec_out = aligned4(a.d_logits, a.dtype, a.E, a.E);
   return by_width(a.T, a.E, a.K, [&](auto lpr, auto vpl) {
     constexpr int LPR = decltype(lpr)::value, VPL = decltype(vpl)::value, kRows = kGateThreads / LPR;
     const size_t lds = (size_t)kRows * ((a.E + 3) / 4 * 4 + 4) * 4;
