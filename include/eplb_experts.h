@@ -235,7 +235,7 @@ int32_t eplb_quantize_weights(const void* w, int32_t dtype, int32_t G, int64_t N
  * Errors: EPLB_E_ARG (a size outside its range, K % 16, a pointer not
  * aligned, an unknown dtype, a NULL array, y sharing a byte with an input),
  * EPLB_E_LIMIT (N or K > 2^24, R or X > 2^31 - 1, G > 8192, or more than
- * 2^24 - 1 tiles of the output), EPLB_E_HIP.
+ * 2^23 - 1 tiles of the output), EPLB_E_HIP.
  */
 int32_t eplb_expert_matmul(const uint8_t* q, const float* scale, int64_t X, const uint8_t* w, const float* w_scale,
                            const int32_t* offsets, int32_t G, const int32_t* rows, int64_t R, int32_t topk, int64_t N,

@@ -18,6 +18,15 @@ namespace {
 constexpr int kTile = 128;                   // rows of each operand per workgroup
 constexpr int kMmThreads = 256;              // four waves, 64 x 64 of the tile each
 
+// Whether the matrix cores' rate bounds a product, rather than its bytes or
+// the launch: then 16-bit outputs come from the 8-bit matrix instruction.
+// out rows x in columns over a contraction of `inner`, and the bytes of its
+// operands and output.
+bool matrix_bound(double out, double in, double inner, double bytes) {
+  const double ops = 2.0 * out * in * inner;
+  return ops >= 0x1p34 && ops >= 256.0 * bytes;
+}
+
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -101,6 +110,195 @@ __device__ __forceinline__ void store4(void* p, int32_t dtype, int64_t at, int l
     if (j < left) store_float(p, dtype, at + j, v[j]);
 }
 
+// ---------------------------------------------------------------- few rows
+// Streaming form, for groups of few rows: the weights are read once, from
+// memory to registers, and bound the time.  A wave takes 16 n of one group
+// through all of K against TT x 16 rows; the fragments of kAhead blocks are in
+// flight at once (2 KiB each), so that the waves of a CU keep 16 KiB and more
+// outstanding.  With the memory as the bound, 16-bit products cost nothing and
+// keep 32-bit sums.
+constexpr int kStreamThreads = 256;
+constexpr int kStreamN = 64;                 // n of a workgroup: 16 of each wave
+constexpr int kAhead = 4;
+
+// The two 16-byte parts of block kb that a lane of `quad` holds; at the end of
+// a row that has no such part, its first ones (the caller zeroes the other
+// operand there).
+__device__ __forceinline__ void load_parts(const uint8_t* row, int kb, int quad, int K, i32x4& lo, i32x4& hi) {
+  const int64_t k0 = (int64_t)kb * kBlock + quad * 16, k1 = k0 + 64;
+  lo = *reinterpret_cast<const i32x4*>(row + (k0 < K ? k0 : 0));
+  hi = *reinterpret_cast<const i32x4*>(row + (k1 < K ? k1 : 0));
+}
+
+// The row of the operand that grouped row `r` reads, or -1.
+__device__ __forceinline__ int32_t source_row(const MatmulArgs& a, int32_t r) {
+  int32_t from = r;
+  if (a.rows != nullptr) {
+    from = a.rows[r];
+    from = from < 0 ? -1 : (int32_t)fastdiv_apply((uint32_t)from, a.fd_topk);
+  }
+  return from < a.X ? from : -1;
+}
+
+// 16 rows: both operands go straight to registers.
+__global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulArgs a, int32_t n_tiles) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quad = lane >> 4, col = lane & 15;
+  const int n0 = (int)(blockIdx.x % n_tiles) * kStreamN + wave * 16;
+  const Tile t = find_tile(a.offsets, a.G, a.R, 16, (int32_t)(blockIdx.x / n_tiles), true);
+  if (t.g < 0 || n0 >= a.N) return;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (t.g < a.G) {
+    const int32_t from = col < t.rows ? source_row(a, t.row + col) : -1;
+    const int n = n0 + col < a.N ? n0 + col : a.N - 1;
+    const uint8_t* w = a.w + ((int64_t)t.g * a.N + n) * a.K;
+    const uint8_t* x = a.q + (int64_t)(from < 0 ? 0 : from) * a.K;
+    const float* xs = a.scale + (int64_t)(from < 0 ? 0 : from) * a.KB;
+    const float* ws = a.w_scale + ((int64_t)t.g * a.NB + n0 / kBlock) * a.KB;
+    i32x4 rw[kAhead][2], rx[kAhead][2];
+    float sx[kAhead];
+    auto load = [&](int slot, int kb) {
+      load_parts(w, kb, quad, a.K, rw[slot][0], rw[slot][1]);
+      if (a.X > 0) {
+        load_parts(x, kb, quad, a.K, rx[slot][0], rx[slot][1]);
+        sx[slot] = xs[kb];
+      }
+    };
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p)
+      if (p < a.KB) load(p, p);
+    for (int kb0 = 0; kb0 < a.KB; kb0 += kAhead) {
+#pragma unroll
+      for (int p = 0; p < kAhead; ++p) {
+        const int kb = kb0 + p;
+        if (kb >= a.KB) break;
+        const i32x4 zero = {0, 0, 0, 0};
+        const bool lo = from >= 0 && kb * kBlock + quad * 16 < a.K, hi = from >= 0 && kb * kBlock + quad * 16 + 64 < a.K;
+        Fragment<true> fw, fx;
+        fw.set(rw[p][0], rw[p][1]);
+        fx.set(lo ? rx[p][0] : zero, hi ? rx[p][1] : zero);
+        const float sc = from >= 0 ? ws[kb] * sx[p] : 0.0f;
+        if (kb + kAhead < a.KB) load(p, kb + kAhead);
+        const f32x4 d = mfma_block(fw, fx);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += d[j] * sc;
+      }
+    }
+    if (from < 0) acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const int n = n0 + quad * 4;
+  if (col < t.rows) store4(a.y, a.dtype, (int64_t)(t.row + col) * a.N + n, a.N - n, a.N % 4 == 0, acc);
+}
+
+// Up to TT x 16 rows: the rows of a block stand in LDS (two buffers) for the
+// workgroup's waves; the even blocks of K are taken by the first four waves,
+// the odd ones by the others, and their sums meet in LDS at the end.
+template <int TT>
+__global__ __launch_bounds__(2 * kStreamThreads) void expert_stream_kernel(MatmulArgs a, int32_t n_tiles) {
+  constexpr int kRows = TT * 16;
+  constexpr int kParts = kRows * 8 / kStreamThreads;       // 16-byte parts of a block per thread
+  __shared__ __attribute__((aligned(16))) uint8_t xt[2][2][kRows * kBlock];
+  __shared__ int32_t src[kRows];
+  const int half = threadIdx.x / kStreamThreads, tid = threadIdx.x % kStreamThreads;
+  const int lane = tid & 63, wave = tid >> 6, quad = lane >> 4, col = lane & 15;
+  const int n0 = (int)(blockIdx.x % n_tiles) * kStreamN + wave * 16;
+  const Tile t = find_tile(a.offsets, a.G, a.R, kRows, (int32_t)(blockIdx.x / n_tiles), true);
+  if (t.g < 0) return;
+  f32x4 acc[TT];
+#pragma unroll
+  for (int o = 0; o < TT; ++o) acc[o] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (t.g < a.G) {
+    if ((int)threadIdx.x < kRows) src[threadIdx.x] = (int)threadIdx.x < t.rows ? source_row(a, t.row + threadIdx.x) : -1;
+    __syncthreads();
+    const int tiles = (t.rows + 15) >> 4;
+    const int n = n0 + col < a.N ? n0 + col : a.N - 1;
+    const uint8_t* w = a.w + ((int64_t)t.g * a.N + n) * a.K;
+    const float* ws = a.w_scale + ((int64_t)t.g * a.NB + (n0 < a.N ? n0 : 0) / kBlock) * a.KB;
+    const int blocks = (a.KB + 1 - half) / 2;              // blocks half, half + 2, ...
+    const int most = (a.KB + 1) / 2;
+    int32_t from[TT];
+#pragma unroll
+    for (int o = 0; o < TT; ++o) from[o] = src[o * 16 + col];
+    i32x4 rw[kAhead][2], rx[2][kParts];
+    float sx[2][TT];
+    auto load_w = [&](int slot, int b) { load_parts(w, 2 * b + half, quad, a.K, rw[slot][0], rw[slot][1]); };
+    auto load_x = [&](int slot, int b) {
+      const int kb = 2 * b + half;
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        const int r = (tid + p * kStreamThreads) >> 3;
+        const int64_t k = (int64_t)kb * kBlock + (tid & 7) * 16;
+        rx[slot][p] = i32x4{0, 0, 0, 0};
+        if (src[r] >= 0 && k < a.K) rx[slot][p] = *reinterpret_cast<const i32x4*>(a.q + (int64_t)src[r] * a.K + k);
+      }
+#pragma unroll
+      for (int o = 0; o < TT; ++o) sx[slot][o] = from[o] >= 0 ? a.scale[(int64_t)from[o] * a.KB + kb] : 0.0f;
+    };
+    auto put_x = [&](int slot, int buffer) {
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        const int r = (tid + p * kStreamThreads) >> 3;
+        *reinterpret_cast<i32x4*>(xt[half][buffer] + lds_at(r, tid & 7)) = rx[slot][p];
+      }
+    };
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p)
+      if (p < blocks) load_w(p, p);
+    if (blocks > 0) load_x(0, 0);
+    if (blocks > 1) load_x(1, 1);
+    for (int b0 = 0; b0 < most; b0 += kAhead) {
+#pragma unroll
+      for (int p = 0; p < kAhead; ++p) {
+        const int b = b0 + p;
+        if (b >= most) break;
+        const int slot = p & 1;
+        if (b < blocks) put_x(slot, slot);
+        __syncthreads();                     // one is enough: the buffer written next was read before this one
+        if (b >= blocks) continue;
+        float sc[TT];
+        const float wk = ws[2 * b + half];
+#pragma unroll
+        for (int o = 0; o < TT; ++o) sc[o] = sx[slot][o] * wk;
+        if (b + 2 < blocks) load_x(slot, b + 2);
+        Fragment<true> fw;
+        fw.set(rw[p][0], rw[p][1]);
+        if (b + kAhead < blocks) load_w(p, b + kAhead);
+#pragma unroll
+        for (int o = 0; o < TT; ++o) {
+          if (o >= tiles) break;
+          const Fragment<true> fx = fragment<true>(xt[half][slot], o * 16 + col, quad);
+          const f32x4 d = mfma_block(fw, fx);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[o][j] += d[j] * sc[o];
+        }
+      }
+    }
+    // the second half's sums to the first
+    __syncthreads();
+    f32x4* sums = reinterpret_cast<f32x4*>(xt);            // TT * 256 vectors: half of xt
+    if (half == 1) {
+#pragma unroll
+      for (int o = 0; o < TT; ++o) sums[o * kStreamThreads + tid] = acc[o];
+    }
+    __syncthreads();
+    if (half == 1) return;
+#pragma unroll
+    for (int o = 0; o < TT; ++o) {
+      const f32x4 v = sums[o * kStreamThreads + tid];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[o][j] = from[o] >= 0 ? acc[o][j] + v[j] : 0.0f;
+    }
+  } else if (half == 1) {
+    return;
+  }
+  const int n = n0 + quad * 4;
+  if (n >= a.N) return;
+#pragma unroll
+  for (int o = 0; o < TT; ++o)
+    if (o * 16 + col < t.rows)
+      store4(a.y, a.dtype, (int64_t)(t.row + o * 16 + col) * a.N + n, a.N - n, a.N % 4 == 0, acc[o]);
+}
+
+// ---------------------------------------------------------------- tiles
 template <bool WIDE>
 __global__ __launch_bounds__(kMmThreads) void expert_matmul_kernel(MatmulArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t wt[kTile * kBlock];
@@ -266,24 +464,57 @@ __global__ __launch_bounds__(kMmThreads) void expert_wgrad_kernel(WgradArgs a, i
   }
 }
 
+// The form of a product: rows to a tile and n to a workgroup.
+enum MatmulForm { kStream16, kStream, kTiles };
+
+struct MatmulPlan {
+  MatmulForm form;
+  int rows, n;
+};
+
+MatmulPlan plan_matmul(int64_t R, int32_t G) {
+  const int64_t average = ceil_div(R, G);
+  if (average <= 8) return {kStream16, 16, kStreamN};
+  if (average <= 96) return {kStream, 128, kStreamN};
+  return {kTiles, kTile, kTile};
+}
+
 }  // namespace
 
-int64_t matmul_tiles(int64_t R, int64_t N, int32_t G) { return (R / kTile + G + 2) * ceil_div(N, kTile); }
+int64_t matmul_tiles(int64_t R, int64_t N, int32_t G) {
+  const MatmulPlan p = plan_matmul(R, G);
+  return (R / p.rows + G + 2) * ceil_div(N, p.n);
+}
 
 int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G) { return G * ceil_div(N, kTile) * ceil_div(K, kTile); }
 
-hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
-  if (a.R == 0) return hipSuccess;
+hipError_t launch_expert_matmul(const MatmulArgs& args, hipStream_t stream) {
+  if (args.R == 0) return hipSuccess;
+  MatmulArgs a = args;
+  a.large = matrix_bound(a.R, a.N, a.K, (double)a.R * a.K + (double)a.G * a.N * a.K + 2.0 * a.R * a.N);
+  const MatmulPlan p = plan_matmul(a.R, a.G);
   const dim3 grid((unsigned)matmul_tiles(a.R, a.N, a.G));
-  if (a.dtype == kF32) expert_matmul_kernel<true><<<grid, dim3(kMmThreads), 0, stream>>>(a);
-  else expert_matmul_kernel<false><<<grid, dim3(kMmThreads), 0, stream>>>(a);
+  const int32_t n_tiles = (int32_t)ceil_div(a.N, p.n);
+  switch (p.form) {
+    case kStream16:
+      expert_stream16_kernel<<<grid, dim3(kStreamThreads), 0, stream>>>(a, n_tiles);
+      break;
+    case kStream:
+      expert_stream_kernel<8><<<grid, dim3(2 * kStreamThreads), 0, stream>>>(a, n_tiles);
+      break;
+    case kTiles:
+      if (a.dtype == kF32 || !a.large) expert_matmul_kernel<true><<<grid, dim3(kMmThreads), 0, stream>>>(a);
+      else expert_matmul_kernel<false><<<grid, dim3(kMmThreads), 0, stream>>>(a);
+      break;
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_expert_wgrad(const WgradArgs& a, hipStream_t stream) {
   const int32_t ni = (int32_t)ceil_div(a.K, kTile), no = (int32_t)ceil_div(a.N, kTile);
   const dim3 grid((unsigned)wgrad_tiles(a.N, a.K, a.G));
-  if (a.dtype == kF32) expert_wgrad_kernel<true><<<grid, dim3(kMmThreads), 0, stream>>>(a, ni, no);
+  const bool large = matrix_bound(a.N, a.K, a.R, (double)a.R * (a.N + a.K) + 2.0 * a.G * a.N * a.K);
+  if (a.dtype == kF32 || !large) expert_wgrad_kernel<true><<<grid, dim3(kMmThreads), 0, stream>>>(a, ni, no);
   else expert_wgrad_kernel<false><<<grid, dim3(kMmThreads), 0, stream>>>(a, ni, no);
   return hipGetLastError();
 }

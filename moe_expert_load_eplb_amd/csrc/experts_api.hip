@@ -9,7 +9,7 @@ using namespace eplb;
 
 namespace {
 
-constexpr int64_t kMaxTiles = (int64_t(1) << 24) - 1;   // workgroups of one launch (256 work-items each)
+constexpr int64_t kMaxTiles = (int64_t(1) << 23) - 1;   // workgroups of one launch (512 work-items each at most)
 
 int32_t result(hipError_t err) { return err == hipSuccess ? EPLB_OK : EPLB_E_HIP; }
 

@@ -114,6 +114,7 @@ struct MatmulArgs {
   void* y;
   int64_t X;
   int32_t R, N, K, KB, NB, G, topk, dtype;
+  bool large;                // 16-bit outputs come from the 8-bit matrix instruction
   FastDiv fd_topk;
 };
 
