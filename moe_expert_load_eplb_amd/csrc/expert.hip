@@ -111,21 +111,22 @@ __device__ __forceinline__ void store4(void* p, int32_t dtype, int64_t at, int l
 }
 
 // ---------------------------------------------------------------- few rows
-// Streaming form, for groups of few rows: the weights are read once, from
+// Streaming forms, for groups of few rows: the weights are read once, from
 // memory to registers, and bound the time.  A wave takes 16 n of one group
-// through all of K against TT x 16 rows; the fragments of kAhead blocks are in
-// flight at once (2 KiB each), so that the waves of a CU keep 16 KiB and more
-// outstanding.  With the memory as the bound, 16-bit products cost nothing and
-// keep 32-bit sums.
+// through K; the fragments of several blocks of 128 are in flight at once
+// (2 KiB each).  With the memory as the bound, 16-bit products cost nothing
+// and keep 32-bit sums.  No load stands behind a branch (rows and blocks past
+// the end are clamped to the last ones and not used): a load that may or may
+// not have been issued makes every wait behind it wait for all of them.
 constexpr int kStreamThreads = 256;
-constexpr int kStreamN = 64;                 // n of a workgroup: 16 of each wave
-constexpr int kAhead = 4;
+constexpr int kStream16N = 64;               // n of a workgroup: 16 of each wave
+constexpr int kStreamN = 32;                 // n of a workgroup, of each wave
 
 // The two 16-byte parts of block kb that a lane of `quad` holds; at the end of
 // a row that has no such part, its first ones (the caller zeroes the other
 // operand there).
 __device__ __forceinline__ void load_parts(const uint8_t* row, int kb, int quad, int K, i32x4& lo, i32x4& hi) {
-  const int64_t k0 = (int64_t)kb * kBlock + quad * 16, k1 = k0 + 64;
+  const int k0 = kb * kBlock + quad * 16, k1 = k0 + 64;
   lo = *reinterpret_cast<const i32x4*>(row + (k0 < K ? k0 : 0));
   hi = *reinterpret_cast<const i32x4*>(row + (k1 < K ? k1 : 0));
 }
@@ -140,48 +141,72 @@ __device__ __forceinline__ int32_t source_row(const MatmulArgs& a, int32_t r) {
   return from < a.X ? from : -1;
 }
 
+// A row of per-block scales that is the same for the whole wave: lane i holds
+// the scale of the i-th block from one on, for two runs of blocks (this one,
+// the next).
+struct ScaleRow {
+  const float* p;
+  int n;
+  float now, next;
+  __device__ __forceinline__ ScaleRow(const float* row, int blocks) : p(row), n(blocks), next(0.0f) {
+    now = p[min((int)(threadIdx.x & 63), n - 1)];
+  }
+  __device__ __forceinline__ void load_next(int from) { next = p[min(from + (int)(threadIdx.x & 63), n - 1)]; }
+  __device__ __forceinline__ void advance() { now = next; }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now), i));
+  }
+};
+
 // 16 rows: both operands go straight to registers.
+constexpr int kAhead16 = 8;
+
 __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulArgs a, int32_t n_tiles) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quad = lane >> 4, col = lane & 15;
-  const int n0 = (int)(blockIdx.x % n_tiles) * kStreamN + wave * 16;
+  const int n0 = (int)(blockIdx.x % n_tiles) * kStream16N + wave * 16;
   const Tile t = find_tile(a.offsets, a.G, a.R, 16, (int32_t)(blockIdx.x / n_tiles), true);
   if (t.g < 0 || n0 >= a.N) return;
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (t.g < a.G) {
-    const int32_t from = col < t.rows ? source_row(a, t.row + col) : -1;
+  if (t.g < a.G && a.X > 0) {
     const int n = n0 + col < a.N ? n0 + col : a.N - 1;
     const uint8_t* w = a.w + ((int64_t)t.g * a.N + n) * a.K;
+    i32x4 rw[kAhead16][2], rx[kAhead16][2];
+    float sx[kAhead16];
+    // loads return in order: the short ones that the next addresses need go first
+    const int32_t from = col < t.rows ? source_row(a, t.row + col) : -1;
+#pragma unroll
+    for (int p = 0; p < kAhead16; ++p) load_parts(w, min(p, a.KB - 1), quad, a.K, rw[p][0], rw[p][1]);
+    ScaleRow ws(a.w_scale + ((int64_t)t.g * a.NB + n0 / kBlock) * a.KB, a.KB);
     const uint8_t* x = a.q + (int64_t)(from < 0 ? 0 : from) * a.K;
     const float* xs = a.scale + (int64_t)(from < 0 ? 0 : from) * a.KB;
-    const float* ws = a.w_scale + ((int64_t)t.g * a.NB + n0 / kBlock) * a.KB;
-    i32x4 rw[kAhead][2], rx[kAhead][2];
-    float sx[kAhead];
-    auto load = [&](int slot, int kb) {
-      load_parts(w, kb, quad, a.K, rw[slot][0], rw[slot][1]);
-      if (a.X > 0) {
-        load_parts(x, kb, quad, a.K, rx[slot][0], rx[slot][1]);
-        sx[slot] = xs[kb];
-      }
-    };
 #pragma unroll
-    for (int p = 0; p < kAhead; ++p)
-      if (p < a.KB) load(p, p);
-    for (int kb0 = 0; kb0 < a.KB; kb0 += kAhead) {
+    for (int p = 0; p < kAhead16; ++p) {
+      const int kb = min(p, a.KB - 1);
+      load_parts(x, kb, quad, a.K, rx[p][0], rx[p][1]);
+      sx[p] = xs[kb];
+    }
+    for (int kb0 = 0; kb0 < a.KB; kb0 += kAhead16) {
+      ws.load_next(kb0 + kAhead16);
 #pragma unroll
-      for (int p = 0; p < kAhead; ++p) {
-        const int kb = kb0 + p;
-        if (kb >= a.KB) break;
+      for (int p = 0; p < kAhead16; ++p) {
+        const int i = kb0 + p;               // past the end: not added
         const i32x4 zero = {0, 0, 0, 0};
-        const bool lo = from >= 0 && kb * kBlock + quad * 16 < a.K, hi = from >= 0 && kb * kBlock + quad * 16 + 64 < a.K;
+        const int k = i * kBlock + quad * 16;
         Fragment<true> fw, fx;
         fw.set(rw[p][0], rw[p][1]);
-        fx.set(lo ? rx[p][0] : zero, hi ? rx[p][1] : zero);
-        const float sc = from >= 0 ? ws[kb] * sx[p] : 0.0f;
-        if (kb + kAhead < a.KB) load(p, kb + kAhead);
+        fx.set(k < a.K ? rx[p][0] : zero, k + 64 < a.K ? rx[p][1] : zero);
+        const float sc = ws.get(p) * sx[p];
+        const int next = min(i + kAhead16, a.KB - 1);
+        load_parts(w, next, quad, a.K, rw[p][0], rw[p][1]);
+        load_parts(x, next, quad, a.K, rx[p][0], rx[p][1]);
+        sx[p] = xs[next];
         const f32x4 d = mfma_block(fw, fx);
+        if (i < a.KB) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] += d[j] * sc;
+          for (int j = 0; j < 4; ++j) acc[j] += d[j] * sc;
+        }
       }
+      ws.advance();
     }
     if (from < 0) acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -189,113 +214,114 @@ __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulA
   if (col < t.rows) store4(a.y, a.dtype, (int64_t)(t.row + col) * a.N + n, a.N - n, a.N % 4 == 0, acc);
 }
 
-// Up to TT x 16 rows: the rows of a block stand in LDS (two buffers) for the
-// workgroup's waves; the even blocks of K are taken by the first four waves,
-// the odd ones by the others, and their sums meet in LDS at the end.
-template <int TT>
-__global__ __launch_bounds__(2 * kStreamThreads) void expert_stream_kernel(MatmulArgs a, int32_t n_tiles) {
-  constexpr int kRows = TT * 16;
-  constexpr int kParts = kRows * 8 / kStreamThreads;       // 16-byte parts of a block per thread
-  __shared__ __attribute__((aligned(16))) uint8_t xt[2][2][kRows * kBlock];
-  __shared__ int32_t src[kRows];
-  const int half = threadIdx.x / kStreamThreads, tid = threadIdx.x % kStreamThreads;
-  const int lane = tid & 63, wave = tid >> 6, quad = lane >> 4, col = lane & 15;
-  const int n0 = (int)(blockIdx.x % n_tiles) * kStreamN + wave * 16;
-  const Tile t = find_tile(a.offsets, a.G, a.R, kRows, (int32_t)(blockIdx.x / n_tiles), true);
-  if (t.g < 0) return;
-  f32x4 acc[TT];
+// Up to 96 rows of one group against 32 n: the workgroup's four waves take
+// every fourth block of K each, all operands straight from memory (the rows,
+// read by every workgroup of the group, from the caches), and add their sums
+// in LDS at the end, in order.  Without a barrier in the loop the waves run
+// free; a tile's next rows are loaded as soon as its last ones are used.
+constexpr int kStreamSplit = kStreamThreads / 64;          // waves that share a tile's K
+
+// The loop for NT tiles of 16 rows (all of them present).
+template <int NT>
+__device__ __forceinline__ void stream_tiles(const MatmulArgs& a, const Tile& t, int n0, int wave, f32x4* sums) {
+  constexpr int kAheadW = 2;                 // blocks of the weights in flight
+  const int lane = threadIdx.x & 63, quad = lane >> 4, col = lane & 15;
+  f32x4 acc[NT][2];
 #pragma unroll
-  for (int o = 0; o < TT; ++o) acc[o] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (t.g < a.G) {
-    if ((int)threadIdx.x < kRows) src[threadIdx.x] = (int)threadIdx.x < t.rows ? source_row(a, t.row + threadIdx.x) : -1;
-    __syncthreads();
-    const int tiles = (t.rows + 15) >> 4;
-    const int n = n0 + col < a.N ? n0 + col : a.N - 1;
-    const uint8_t* w = a.w + ((int64_t)t.g * a.N + n) * a.K;
-    const float* ws = a.w_scale + ((int64_t)t.g * a.NB + (n0 < a.N ? n0 : 0) / kBlock) * a.KB;
-    const int blocks = (a.KB + 1 - half) / 2;              // blocks half, half + 2, ...
-    const int most = (a.KB + 1) / 2;
-    int32_t from[TT];
+  for (int o = 0; o < NT; ++o) acc[o][0] = acc[o][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint8_t* w[2];
 #pragma unroll
-    for (int o = 0; o < TT; ++o) from[o] = src[o * 16 + col];
-    i32x4 rw[kAhead][2], rx[2][kParts];
-    float sx[2][TT];
-    auto load_w = [&](int slot, int b) { load_parts(w, 2 * b + half, quad, a.K, rw[slot][0], rw[slot][1]); };
-    auto load_x = [&](int slot, int b) {
-      const int kb = 2 * b + half;
+  for (int u = 0; u < 2; ++u) w[u] = a.w + ((int64_t)t.g * a.N + min(n0 + u * 16 + col, a.N - 1)) * a.K;
+  i32x4 rw[kAheadW][2][2], rx[NT][2];
+  float sx[NT];
+  auto block = [&](int b) { return min(b * kStreamSplit + wave, a.KB - 1); };
+  auto load_w = [&](int slot, int b) {
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        const int r = (tid + p * kStreamThreads) >> 3;
-        const int64_t k = (int64_t)kb * kBlock + (tid & 7) * 16;
-        rx[slot][p] = i32x4{0, 0, 0, 0};
-        if (src[r] >= 0 && k < a.K) rx[slot][p] = *reinterpret_cast<const i32x4*>(a.q + (int64_t)src[r] * a.K + k);
+    for (int u = 0; u < 2; ++u) load_parts(w[u], block(b), quad, a.K, rw[slot][u][0], rw[slot][u][1]);
+  };
+  int32_t from[NT];
+#pragma unroll
+  for (int o = 0; o < NT; ++o) from[o] = o * 16 + col < t.rows ? source_row(a, t.row + o * 16 + col) : -1;
+  ScaleRow ws(a.w_scale + ((int64_t)t.g * a.NB + n0 / kBlock) * a.KB, a.KB);
+  load_w(0, 0);
+  auto load_x = [&](int o, int b) {
+    const int64_t row = max(from[o], 0);
+    load_parts(a.q + row * a.K, block(b), quad, a.K, rx[o][0], rx[o][1]);
+    sx[o] = a.scale[row * a.KB + block(b)];
+  };
+#pragma unroll
+  for (int o = 0; o < NT; ++o) load_x(o, 0);
+#pragma unroll
+  for (int p = 1; p < kAheadW; ++p) load_w(p, p);
+  const int steps = (a.KB + kStreamSplit - 1) / kStreamSplit;
+  for (int b0 = 0; b0 < steps; b0 += kAheadW) {
+    ws.load_next((b0 + kAheadW) * kStreamSplit);
+#pragma unroll
+    for (int p = 0; p < kAheadW; ++p) {
+      const int b = b0 + p, kb = b * kStreamSplit + wave;
+      const i32x4 zero = {0, 0, 0, 0};
+      const bool lo = kb * kBlock + quad * 16 < a.K, hi = kb * kBlock + quad * 16 + 64 < a.K;
+      const bool in = kb < a.KB;             // past the end: not added
+      const float wk = ws.get(p * kStreamSplit + wave);
+      Fragment<true> fw[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) fw[u].set(rw[p][u][0], rw[p][u][1]);
+#pragma unroll
+      for (int o = 0; o < NT; ++o) {
+        Fragment<true> fx;
+        fx.set(lo ? rx[o][0] : zero, hi ? rx[o][1] : zero);
+        const float sc = sx[o] * wk;
+        load_x(o, b + 1);
+        f32x4 d[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) d[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[u].v[c], fx.v[c], d[u], 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[o][u][j] = in ? acc[o][u][j] + d[u][j] * sc : acc[o][u][j];
       }
-#pragma unroll
-      for (int o = 0; o < TT; ++o) sx[slot][o] = from[o] >= 0 ? a.scale[(int64_t)from[o] * a.KB + kb] : 0.0f;
-    };
-    auto put_x = [&](int slot, int buffer) {
-#pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        const int r = (tid + p * kStreamThreads) >> 3;
-        *reinterpret_cast<i32x4*>(xt[half][buffer] + lds_at(r, tid & 7)) = rx[slot][p];
-      }
-    };
-#pragma unroll
-    for (int p = 0; p < kAhead; ++p)
-      if (p < blocks) load_w(p, p);
-    if (blocks > 0) load_x(0, 0);
-    if (blocks > 1) load_x(1, 1);
-    for (int b0 = 0; b0 < most; b0 += kAhead) {
-#pragma unroll
-      for (int p = 0; p < kAhead; ++p) {
-        const int b = b0 + p;
-        if (b >= most) break;
-        const int slot = p & 1;
-        if (b < blocks) put_x(slot, slot);
-        __syncthreads();                     // one is enough: the buffer written next was read before this one
-        if (b >= blocks) continue;
-        float sc[TT];
-        const float wk = ws[2 * b + half];
-#pragma unroll
-        for (int o = 0; o < TT; ++o) sc[o] = sx[slot][o] * wk;
-        if (b + 2 < blocks) load_x(slot, b + 2);
-        Fragment<true> fw;
-        fw.set(rw[p][0], rw[p][1]);
-        if (b + kAhead < blocks) load_w(p, b + kAhead);
-#pragma unroll
-        for (int o = 0; o < TT; ++o) {
-          if (o >= tiles) break;
-          const Fragment<true> fx = fragment<true>(xt[half][slot], o * 16 + col, quad);
-          const f32x4 d = mfma_block(fw, fx);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[o][j] += d[j] * sc[o];
-        }
-      }
+      load_w(p, b + kAheadW);                // behind the rows' loads: loads return in order
     }
-    // the second half's sums to the first
-    __syncthreads();
-    f32x4* sums = reinterpret_cast<f32x4*>(xt);            // TT * 256 vectors: half of xt
-    if (half == 1) {
-#pragma unroll
-      for (int o = 0; o < TT; ++o) sums[o * kStreamThreads + tid] = acc[o];
-    }
-    __syncthreads();
-    if (half == 1) return;
-#pragma unroll
-    for (int o = 0; o < TT; ++o) {
-      const f32x4 v = sums[o * kStreamThreads + tid];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[o][j] = from[o] >= 0 ? acc[o][j] + v[j] : 0.0f;
-    }
-  } else if (half == 1) {
-    return;
+    ws.advance();
   }
-  const int n = n0 + quad * 4;
-  if (n >= a.N) return;
 #pragma unroll
-  for (int o = 0; o < TT; ++o)
-    if (o * 16 + col < t.rows)
-      store4(a.y, a.dtype, (int64_t)(t.row + o * 16 + col) * a.N + n, a.N - n, a.N % 4 == 0, acc[o]);
+  for (int o = 0; o < NT; ++o)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) sums[(o * 2 + u) * 64 + lane] = from[o] >= 0 ? acc[o][u] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+__global__ __launch_bounds__(kStreamThreads, 2) void expert_stream_kernel(MatmulArgs a, int32_t n_tiles, int32_t rows) {
+  extern __shared__ __attribute__((aligned(16))) f32x4 sums[];   // [wave][rows / 16][2][64]
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = (int)(blockIdx.x % n_tiles) * kStreamN;
+  const Tile t = find_tile(a.offsets, a.G, a.R, rows, (int32_t)(blockIdx.x / n_tiles), true);
+  if (t.g < 0) return;
+  const bool some = t.g < a.G && a.X > 0;
+  const int tiles = (t.rows + 15) >> 4, each = rows * 8;
+  if (some) {
+    // a loop of its own for every number of tiles: no load behind a branch
+    f32x4* mine = sums + wave * each;
+    switch (tiles) {
+      case 1: stream_tiles<1>(a, t, n0, wave, mine); break;
+      case 2: stream_tiles<2>(a, t, n0, wave, mine); break;
+      case 3: stream_tiles<3>(a, t, n0, wave, mine); break;
+      case 4: stream_tiles<4>(a, t, n0, wave, mine); break;
+      case 5: stream_tiles<5>(a, t, n0, wave, mine); break;
+      default: stream_tiles<6>(a, t, n0, wave, mine); break;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tiles * 128; i += kStreamThreads) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (some) {
+#pragma unroll
+      for (int k = 0; k < kStreamSplit; ++k) v += sums[k * each + i];
+    }
+    const int r = (i >> 7) * 16 + (i & 15), n = n0 + (i >> 6 & 1) * 16 + (i >> 4 & 3) * 4;
+    if (r < t.rows && n < a.N) store4(a.y, a.dtype, (int64_t)(t.row + r) * a.N + n, a.N - n, a.N % 4 == 0, v);
+  }
 }
 
 // ---------------------------------------------------------------- tiles
@@ -474,8 +500,9 @@ struct MatmulPlan {
 
 MatmulPlan plan_matmul(int64_t R, int32_t G) {
   const int64_t average = ceil_div(R, G);
-  if (average <= 8) return {kStream16, 16, kStreamN};
-  if (average <= 96) return {kStream, 128, kStreamN};
+  if (average <= 8) return {kStream16, 16, kStream16N};
+  // room for groups half as large again as the average, so that few need a second tile
+  if (average <= 64) return {kStream, average <= 42 ? 64 : 96, kStreamN};
   return {kTiles, kTile, kTile};
 }
 
@@ -483,7 +510,8 @@ MatmulPlan plan_matmul(int64_t R, int32_t G) {
 
 int64_t matmul_tiles(int64_t R, int64_t N, int32_t G) {
   const MatmulPlan p = plan_matmul(R, G);
-  return (R / p.rows + G + 2) * ceil_div(N, p.n);
+  // every group adds at most one tile that is not full, and a tile has a row
+  return (std::min(R, R / p.rows + G) + 2) * ceil_div(N, p.n);
 }
 
 int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G) { return G * ceil_div(N, kTile) * ceil_div(K, kTile); }
@@ -500,7 +528,7 @@ hipError_t launch_expert_matmul(const MatmulArgs& args, hipStream_t stream) {
       expert_stream16_kernel<<<grid, dim3(kStreamThreads), 0, stream>>>(a, n_tiles);
       break;
     case kStream:
-      expert_stream_kernel<8><<<grid, dim3(2 * kStreamThreads), 0, stream>>>(a, n_tiles);
+      expert_stream_kernel<<<grid, dim3(kStreamThreads), (size_t)kStreamSplit * p.rows * 8 * 16, stream>>>(a, n_tiles, p.rows);
       break;
     case kTiles:
       if (a.dtype == kF32 || !a.large) expert_matmul_kernel<true><<<grid, dim3(kMmThreads), 0, stream>>>(a);
