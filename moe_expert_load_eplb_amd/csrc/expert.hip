@@ -15,8 +15,6 @@ namespace eplb {
 
 namespace {
 
-constexpr int kTile = 128;                   // rows of each operand per workgroup
-constexpr int kMmThreads = 256;              // four waves, 64 x 64 of the tile each
 
 // Whether the matrix cores' rate bounds a product, rather than its bytes or
 // the launch: then 16-bit outputs come from the 8-bit matrix instruction.
@@ -325,203 +323,354 @@ __global__ __launch_bounds__(kStreamThreads, 2) void expert_stream_kernel(Matmul
 }
 
 // ---------------------------------------------------------------- tiles
-template <bool WIDE>
-__global__ __launch_bounds__(kMmThreads) void expert_matmul_kernel(MatmulArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t wt[kTile * kBlock];
-  __shared__ __attribute__((aligned(16))) uint8_t xt[kTile * kBlock];
-  __shared__ int32_t src[kTile];
-  const int nb = (int)(blockIdx.x % a.NB);
-  const Tile t = find_tile(a.offsets, a.G, a.R, kTile, (int32_t)(blockIdx.x / a.NB), true);
-  if (t.g < 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int quad = lane >> 4, col = lane & 15;
-  const int wi = (wave & 1) * 64, wo = (wave >> 1) * 64;
-  if (tid < kTile) {
-    int32_t from = -1;
-    if (tid < t.rows && t.g < a.G) {
-      from = t.row + tid;
-      if (a.rows != nullptr) {
-        from = a.rows[from];
-        from = from < 0 ? -1 : (int32_t)fastdiv_apply((uint32_t)from, a.fd_topk);
-      }
-      if (from >= a.X) from = -1;
-    }
-    src[tid] = from;
+// Tiles of the output, for many rows.  A workgroup of WI x WO waves computes
+// (WI IT 32) inner x (WO OT 32) outer values, a wave IT x OT tiles of 32 x 32
+// (32 x 32 x 64 reaches 4.4 POPS on its own, 16 x 16 x 128 4.0).  The operands
+// of a block of 128 (rows of 128 bytes) and its scales go from memory to LDS
+// without passing through registers, STAGES - 1 blocks ahead; one barrier per
+// block.  Every wave issues the same number of such loads per block, so that
+// waiting for all but the later blocks' is waiting for this one's.
+//
+// A row's eight 16-byte parts are permuted (on the way in, by the address a
+// lane loads from) so that eight lanes that read one part of eight rows reach
+// all banks.  The inner rows of a wave are taken in an order that leaves a
+// lane with 16 IT consecutive inner values of one outer row.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __attribute__((aligned(16))) uint8_t g_zeros[16];   // read in place of what lies past the end of K
+
+__device__ __forceinline__ void load_to_lds16(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+__device__ __forceinline__ void load_to_lds4(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+}
+
+// Waits until at most N of this wave's loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Eight consecutive values of one output row; `left` of them are inside.
+__device__ __forceinline__ void store8(void* p, int32_t dtype, int64_t at, int left, int64_t width, const float* v) {
+  if (dtype != kF32 && left >= 8 && width % 8 == 0) {
+    u16 h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = dtype == kBf16 ? float_to_bf16(v[j]) : float_to_f16(v[j]);
+    uint4 w;
+    w.x = h[0] | (uint32_t)h[1] << 16;
+    w.y = h[2] | (uint32_t)h[3] << 16;
+    w.z = h[4] | (uint32_t)h[5] << 16;
+    w.w = h[6] | (uint32_t)h[7] << 16;
+    *reinterpret_cast<uint4*>(static_cast<u16*>(p) + at) = w;
+    return;
   }
-  __syncthreads();
-  f32x4 acc[4][4];
+  store4(p, dtype, at, left, width % 4 == 0, f32x4{v[0], v[1], v[2], v[3]});
+  if (left > 4) store4(p, dtype, at + 4, left - 4, width % 4 == 0, f32x4{v[4], v[5], v[6], v[7]});
+}
+
+// What a workgroup multiplies: both products in one form.
+struct TileJob {
+  const uint8_t* inner;      // first inner row of the tile
+  int64_t inner_ld;
+  int inner_rows;            // rows inside (the others read the last one and are not stored)
+  const float* inner_scale;  // matmul: [blocks], one for the tile; weight gradient: [blocks][inner_step], at the tile
+  int64_t inner_step;
+  const float* outer_scale;  // matmul: of this lane's row, next block 1 on; weight gradient: [blocks][outer_step]
+  int64_t outer_step;
+  int64_t block0, blocks, K; // first block, number of blocks, elements of a row (matmul: past it zeros)
+};
+
+template <int WI, int WO, int IT, int OT, int STAGES, bool WIDE, bool WGRAD>
+struct TileKernel {
+  static constexpr int kWaves = WI * WO, kThreads = kWaves * 64;
+  static constexpr int kInner = WI * IT * 32, kOuter = WO * OT * 32;
+  static constexpr int kInnerLoads = kInner / 8 / kWaves, kOuterLoads = kOuter / 8 / kWaves;   // of 8 rows, per wave
+  static constexpr int kOuterScaleWaves = (kOuter + 63) / 64, kInnerScaleWaves = WGRAD ? (kInner + 63) / 64 : 0;
+  static constexpr int kLoads = kInnerLoads + kOuterLoads + 1;
+  static constexpr int kScaleWords = (kOuterScaleWaves + kInnerScaleWaves + 1) * 64;
+  static constexpr int kStageBytes = (kInner + kOuter) * kBlock + kScaleWords * 4;
+  static_assert(kInner % (8 * kWaves) == 0 && kOuter % (8 * kWaves) == 0, "whole loads");
+  static_assert(kOuterScaleWaves + kInnerScaleWaves <= kWaves, "one load of scales per wave");
+
+  static __device__ __forceinline__ int inner_key(int r) { return (r & 3) | ((r / (16 * IT) & 1) << 2); }
+
+  // `outer_row(r)`: pointer to outer row r of the tile (any valid row where it has none).
+  template <typename OuterRow, typename OuterScale>
+  static __device__ __forceinline__ void run(const TileJob& job, uint8_t* lds, OuterRow outer_row,
+                                             OuterScale outer_scale, f32x16 (&acc)[OT][IT]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    const int wi = wave % WI * (IT * 32), wo = wave / WI * (OT * 32);
 #pragma unroll
-  for (int o = 0; o < 4; ++o)
+    for (int o = 0; o < OT; ++o)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[o][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (t.g < a.G) {
-    const uint8_t* w = a.w + (int64_t)t.g * a.N * a.K;
-    const float* ws = a.w_scale + ((int64_t)t.g * a.NB + nb) * a.KB;
-    int32_t from[4];
+      for (int t = 0; t < IT; ++t)
 #pragma unroll
-    for (int o = 0; o < 4; ++o) from[o] = src[wo + o * 16 + col];
-    for (int kb = 0; kb < a.KB; ++kb) {
-      i32x4 rw[4], rx[4];
+        for (int i = 0; i < 16; ++i) acc[o][t][i] = 0.0f;
+
+    // what this lane loads of every block
+    const uint8_t *ip[kInnerLoads], *op[kOuterLoads];
+    int ik[kInnerLoads], ok[kOuterLoads];    // its element of the block
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int r = (tid + p * kMmThreads) >> 3, c = tid & 7;
-        const int64_t k = (int64_t)kb * kBlock + c * 16;
-        const int n = nb * kTile + r;
-        rw[p] = rx[p] = i32x4{0, 0, 0, 0};
-        if (n < a.N && k < a.K) rw[p] = *reinterpret_cast<const i32x4*>(w + (int64_t)n * a.K + k);
-        if (src[r] >= 0 && k < a.K) rx[p] = *reinterpret_cast<const i32x4*>(a.q + (int64_t)src[r] * a.K + k);
+    for (int p = 0; p < kInnerLoads; ++p) {
+      const int r = (wave * kInnerLoads + p) * 8 + (lane >> 3);
+      ik[p] = ((lane & 7) ^ inner_key(r)) * 16;
+      ip[p] = job.inner + (int64_t)min(r, job.inner_rows - 1) * job.inner_ld;
+    }
+#pragma unroll
+    for (int p = 0; p < kOuterLoads; ++p) {
+      const int r = (wave * kOuterLoads + p) * 8 + (lane >> 3);
+      ok[p] = ((lane & 7) ^ (r & 7)) * 16;
+      op[p] = outer_row(r);
+    }
+    const float* sp;
+    int64_t s_step = job.outer_step;
+    int s_at = wave * 64;
+    if (wave < kOuterScaleWaves) {
+      sp = outer_scale(wave * 64 + lane);
+    } else if (WGRAD && wave < kOuterScaleWaves + kInnerScaleWaves) {
+      sp = job.inner_scale + min((wave - kOuterScaleWaves) * 64 + lane, job.inner_rows - 1);
+      s_step = job.inner_step;
+    } else {
+      sp = outer_scale(0);                   // keeps the count of loads equal; its place is not read
+      s_at = (kOuterScaleWaves + kInnerScaleWaves) * 64;
+    }
+    auto load = [&](int64_t b) {             // block b of the job to its stage; past the end the last one again
+      const int64_t blk = job.block0 + (b < job.blocks ? b : job.blocks - 1);
+      uint8_t* stage = lds + (int)(b % STAGES) * kStageBytes;
+      uint8_t* si = stage + wave * kInnerLoads * 1024;
+      uint8_t* so = stage + kInner * kBlock + wave * kOuterLoads * 1024;
+      if (WGRAD || (blk + 1) * kBlock <= job.K) {
+#pragma unroll
+        for (int p = 0; p < kInnerLoads; ++p) load_to_lds16(ip[p] + blk * kBlock + ik[p], si + p * 1024);
+#pragma unroll
+        for (int p = 0; p < kOuterLoads; ++p) load_to_lds16(op[p] + blk * kBlock + ok[p], so + p * 1024);
+      } else {                               // the end of K: any inner part of the row against zeros
+#pragma unroll
+        for (int p = 0; p < kInnerLoads; ++p)
+          load_to_lds16(ip[p] + (blk * kBlock + ik[p] < job.K ? blk * kBlock + ik[p] : 0), si + p * 1024);
+#pragma unroll
+        for (int p = 0; p < kOuterLoads; ++p)
+          load_to_lds16(blk * kBlock + ok[p] < job.K ? op[p] + blk * kBlock + ok[p] : g_zeros, so + p * 1024);
       }
-      float sc[4];
+      load_to_lds4(sp + blk * s_step, stage + (kInner + kOuter) * kBlock + s_at * 4);
+    };
 #pragma unroll
-      for (int o = 0; o < 4; ++o) sc[o] = from[o] >= 0 ? ws[kb] * a.scale[(int64_t)from[o] * a.KB + kb] : 0.0f;
-      __syncthreads();
+    for (int p = 0; p < STAGES - 1; ++p) load(p);
+    for (int64_t b = 0; b < job.blocks; ++b) {
+      wait_loads<kLoads * (STAGES - 2)>();   // this block's have arrived, of this wave
+      __syncthreads();                       // of all waves; and all are done with the block before
+      load(b + STAGES - 1);
+      const uint8_t* it = lds + (int)(b % STAGES) * kStageBytes;
+      const uint8_t* ot = it + kInner * kBlock;
+      const float* scales = reinterpret_cast<const float*>(ot + kOuter * kBlock);
+      const float one = WGRAD ? 1.0f : job.inner_scale[job.block0 + b];
+      auto part = [&](const uint8_t* tile, int row, int key, int g) {
+        return *reinterpret_cast<const i32x4*>(tile + row * kBlock + ((g ^ key) << 4));
+      };
+      // part 2 s' + half * 2 ... : a lane's 64 of the block's 128 elements, the same of both operands
+      i32x4 fi[IT][4];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int r = (tid + p * kMmThreads) >> 3, c = tid & 7;
-        *reinterpret_cast<i32x4*>(wt + lds_at(r, c)) = rw[p];
-        *reinterpret_cast<i32x4*>(xt + lds_at(r, c)) = rx[p];
+      for (int t = 0; t < IT; ++t) {
+        const int r = wi + (col >> 2 & 1) * (16 * IT) + 16 * t + (col >> 3) * 4 + (col & 3);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) fi[t][g] = part(it, r, inner_key(r), (g >> 1) * 4 + half * 2 + (g & 1));
       }
-      __syncthreads();
-      Fragment<WIDE> fi[4];
+      f32x4 si[IT][4];
+      if (WGRAD) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fi[i] = fragment<WIDE>(wt, wi + i * 16 + col, quad);
+        for (int t = 0; t < IT; ++t)
 #pragma unroll
-      for (int o = 0; o < 4; ++o) {
-        const Fragment<WIDE> fo = fragment<WIDE>(xt, wo + o * 16 + col, quad);
+          for (int j = 0; j < 4; ++j)
+            si[t][j] = *reinterpret_cast<const f32x4*>(scales + kOuterScaleWaves * 64 + wi + half * (16 * IT) + 16 * t + j * 4);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 d = mfma_block(fi[i], fo);
+      for (int o = 0; o < OT; ++o) {
+        const int r = wo + o * 32 + col;
+        i32x4 fo[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[o][i][j] += d[j] * sc[o];
+        for (int g = 0; g < 4; ++g) fo[g] = part(ot, r, r & 7, (g >> 1) * 4 + half * 2 + (g & 1));
+        const float sc = scales[r] * one;
+#pragma unroll
+        for (int t = 0; t < IT; ++t) {
+          f32x16 d;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) d[i] = 0.0f;
+          if (WIDE) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                d = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[g], h), d, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int g = 0; g < 4; g += 2)
+              d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                  __builtin_shufflevector(fi[t][g], fi[t][g + 1], 0, 1, 2, 3, 4, 5, 6, 7),
+                  __builtin_shufflevector(fo[g], fo[g + 1], 0, 1, 2, 3, 4, 5, 6, 7), d, 0, 0, 0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[o][t][i] += d[i] * (WGRAD ? sc * si[t][i >> 2][i & 3] : sc);
+        }
+      }
+    }
+    wait_loads<0>();                         // none may land in LDS that is no longer this workgroup's
+  }
+
+  // Half h of 16 8-bit values as 16-bit ones.
+  static __device__ __forceinline__ f16x8 half_of(i32x4 v, int h) {
+    const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h], 1.0f, false);
+    const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h], 1.0f, true);
+    const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + 1], 1.0f, false);
+    const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + 1], 1.0f, true);
+    return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+  }
+
+  // Stores the wave's values: row(r) is outer row r's first element in the
+  // output or -1, `left` the inner values from the tile's start on.
+  template <typename Row>
+  static __device__ __forceinline__ void store(const f32x16 (&acc)[OT][IT], void* out, int32_t dtype, int64_t width,
+                                               int64_t left, Row row) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    const int wi = wave % WI * (IT * 32) + half * (16 * IT), wo = wave / WI * (OT * 32);
+#pragma unroll
+    for (int o = 0; o < OT; ++o) {
+      const int64_t at = row(wo + o * 32 + col);
+      if (at < 0) continue;
+#pragma unroll
+      for (int t = 0; t < IT; ++t) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = acc[o][t][i];
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+          const int64_t n = wi + 16 * t + i;
+          if (n < left) store8(out, dtype, at + n, left - n < 8 ? (int)(left - n) : 8, width, v + i);
         }
       }
     }
   }
-  const bool vec = a.N % 4 == 0;
-#pragma unroll
-  for (int o = 0; o < 4; ++o) {
-    const int ro = wo + o * 16 + col;
-    if (ro >= t.rows) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = nb * kTile + wi + i * 16 + quad * 4;
-      store4(a.y, a.dtype, (int64_t)(t.row + ro) * a.N + n, a.N - n, vec, acc[o][i]);
-    }
+};
+
+template <int WI, int WO, int IT, int OT, int STAGES, bool WIDE>
+__global__ __launch_bounds__(WI* WO * 64) void expert_tile_kernel(MatmulArgs a, int32_t n_tiles) {
+  typedef TileKernel<WI, WO, IT, OT, STAGES, WIDE, false> K;
+  extern __shared__ __attribute__((aligned(16))) uint8_t tile_lds[];
+  __shared__ int32_t src[K::kOuter];
+  const int32_t total = count_tiles(a.offsets, a.G, a.R, K::kOuter, true) * n_tiles;
+  if ((int32_t)blockIdx.x >= total) return;
+  const int32_t id = die_order(blockIdx.x, total);
+  const Tile t = find_tile(a.offsets, a.G, a.R, K::kOuter, id / n_tiles, true);
+  if (t.g < 0) return;
+  const int64_t n0 = (int64_t)(id % n_tiles) * K::kInner;
+  for (int r = threadIdx.x; r < K::kOuter; r += K::kThreads)
+    src[r] = r < t.rows && t.g < a.G ? source_row(a, t.row + r) : -1;
+  __syncthreads();
+  f32x16 acc[OT][IT];
+  if (t.g < a.G && a.X > 0) {
+    TileJob job;
+    job.inner = a.w + ((int64_t)t.g * a.N + n0) * a.K;
+    job.inner_ld = a.K;
+    job.inner_rows = (int)(a.N - n0 < K::kInner ? a.N - n0 : K::kInner);
+    // the wave's n lie in one block of 128
+    const int64_t nb = (n0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WI * (IT * 32)) / kBlock;
+    job.inner_scale = a.w_scale + ((int64_t)t.g * a.NB + (nb < a.NB ? nb : a.NB - 1)) * a.KB;
+    job.inner_step = 0;
+    job.outer_step = 1;
+    job.block0 = 0;
+    job.blocks = a.KB;
+    job.K = a.K;
+    K::run(job, tile_lds, [&](int r) { return a.q + (int64_t)max(src[r], 0) * a.K; },
+           [&](int r) { return a.scale + (int64_t)max(src[r < K::kOuter ? r : 0], 0) * a.KB; }, acc);
+  }
+  K::store(acc, a.y, a.dtype, a.N, a.N - n0, [&](int r) -> int64_t {
+    return r < t.rows && src[r] >= 0 ? (int64_t)(t.row + r) * a.N + n0 : -1;
+  });
+  // rows of nothing are zero
+  for (int r = 0; r < t.rows; ++r) {
+    if (src[r] >= 0) continue;
+    for (int64_t n = threadIdx.x; n < K::kInner && n0 + n < a.N; n += K::kThreads)
+      store_float(a.y, a.dtype, (int64_t)(t.row + r) * a.N + n0 + n, 0.0f);
   }
 }
 
-template <bool WIDE>
-__global__ __launch_bounds__(kMmThreads) void expert_wgrad_kernel(WgradArgs a, int32_t ni, int32_t no) {
-  __shared__ __attribute__((aligned(16))) uint8_t it[kTile * kBlock];
-  __shared__ __attribute__((aligned(16))) uint8_t ot[kTile * kBlock];
-  const int g = (int)(blockIdx.x / (ni * no));
-  const int bo = (int)(blockIdx.x / ni % no), bi = (int)(blockIdx.x % ni);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int quad = lane >> 4, col = lane & 15;
-  const int wi = (wave & 1) * 64, wo = (wave >> 1) * 64;
+template <int WI, int WO, int IT, int OT, int STAGES, bool WIDE>
+__global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, int32_t ni, int32_t no) {
+  typedef TileKernel<WI, WO, IT, OT, STAGES, WIDE, true> K;
+  extern __shared__ __attribute__((aligned(16))) uint8_t tile_lds[];
+  const int32_t id = die_order(blockIdx.x, gridDim.x);
+  const int32_t g = id / (ni * no);
+  const int64_t i0 = (int64_t)(id % ni) * K::kInner, o0 = (int64_t)(id / ni % no) * K::kOuter;
   // the group's blocks of 128 rows
-  int64_t b0 = 0, b1 = 0;
-  for (int h = 0; h <= g; ++h) {
-    const int32_t lo = clamp_row(a.offsets[h], a.R), hi = clamp_row(a.offsets[h + 1], a.R);
-    b0 = b1;
-    b1 += hi > lo ? ((int64_t)hi - lo + kBlock - 1) / kBlock : 0;
+  const int32_t before = count_tiles(a.offsets, g, a.R, kBlock, false);
+  const int32_t lo = clamp_row(a.offsets[g], a.R), hi = clamp_row(a.offsets[g + 1], a.R);
+  TileJob job;
+  job.block0 = before;
+  job.blocks = hi > lo ? ((int64_t)hi - lo + kBlock - 1) / kBlock : 0;
+  if (job.block0 + job.blocks > a.Rp / kBlock) job.blocks = a.Rp / kBlock - job.block0;
+  job.inner = a.x + i0 * a.Rp;
+  job.inner_ld = a.Rp;
+  job.inner_rows = (int)(a.K - i0 < K::kInner ? a.K - i0 : K::kInner);
+  job.inner_scale = a.x_scale + i0;
+  job.inner_step = a.K;
+  job.outer_step = a.N;
+  job.K = a.Rp;
+  const int64_t last = a.N - 1 - o0;
+  f32x16 acc[OT][IT];
+  if (job.blocks > 0) {
+    K::run(job, tile_lds, [&](int r) { return a.dy + (o0 + (r < last ? r : last)) * a.Rp; },
+           [&](int r) { return a.dy_scale + o0 + (r < last ? r : last); }, acc);
+  } else {
+#pragma unroll
+    for (int o = 0; o < OT; ++o)
+#pragma unroll
+      for (int t = 0; t < IT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[o][t][i] = 0.0f;
   }
-  if (b1 > a.Rp / kBlock) b1 = a.Rp / kBlock;
-  f32x4 acc[4][4];
-#pragma unroll
-  for (int o = 0; o < 4; ++o)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[o][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t b = b0; b < b1; ++b) {
-    i32x4 ri[4], ro[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int r = (tid + p * kMmThreads) >> 3, c = tid & 7;
-      const int64_t i = (int64_t)bi * kTile + r, o = (int64_t)bo * kTile + r;
-      ri[p] = ro[p] = i32x4{0, 0, 0, 0};
-      if (i < a.K) ri[p] = *reinterpret_cast<const i32x4*>(a.x + i * a.Rp + b * kBlock + c * 16);
-      if (o < a.N) ro[p] = *reinterpret_cast<const i32x4*>(a.dy + o * a.Rp + b * kBlock + c * 16);
-    }
-    float so[4];
-    f32x4 si[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int64_t o = (int64_t)bo * kTile + wo + t * 16 + col;
-      so[t] = o < a.N ? a.dy_scale[b * a.N + o] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t i = (int64_t)bi * kTile + wi + t * 16 + quad * 4 + j;
-        si[t][j] = i < a.K ? a.x_scale[b * a.K + i] : 0.0f;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int r = (tid + p * kMmThreads) >> 3, c = tid & 7;
-      *reinterpret_cast<i32x4*>(it + lds_at(r, c)) = ri[p];
-      *reinterpret_cast<i32x4*>(ot + lds_at(r, c)) = ro[p];
-    }
-    __syncthreads();
-    Fragment<WIDE> fi[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) fi[i] = fragment<WIDE>(it, wi + i * 16 + col, quad);
-#pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      const Fragment<WIDE> fo = fragment<WIDE>(ot, wo + o * 16 + col, quad);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 d = mfma_block(fi[i], fo);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[o][i][j] += d[j] * (so[o] * si[i][j]);
-      }
-    }
-  }
-  const bool vec = a.K % 4 == 0;
-#pragma unroll
-  for (int o = 0; o < 4; ++o) {
-    const int64_t n = (int64_t)bo * kTile + wo + o * 16 + col;
-    if (n >= a.N) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t k = (int64_t)bi * kTile + wi + i * 16 + quad * 4;
-      const int64_t left = a.K - k;
-      store4(a.dw, a.dtype, ((int64_t)g * a.N + n) * a.K + k, left < 4 ? (int)left : 4, vec, acc[o][i]);
-    }
-  }
+  K::store(acc, a.dw, a.dtype, a.K, a.K - i0,
+           [&](int r) -> int64_t { return r <= last ? ((int64_t)g * a.N + o0 + r) * a.K + i0 : -1; });
 }
 
 // The form of a product: rows to a tile and n to a workgroup.
-enum MatmulForm { kStream16, kStream, kTiles };
+enum MatmulForm { kStream16, kStream, kSmallTiles, kLargeTiles };
 
 struct MatmulPlan {
   MatmulForm form;
   int rows, n;
+  bool wide;                 // 16-bit products
 };
 
-MatmulPlan plan_matmul(int64_t R, int32_t G) {
+MatmulPlan plan_matmul(int64_t R, int64_t N, int64_t K, int32_t G, int32_t dtype) {
   const int64_t average = ceil_div(R, G);
-  if (average <= 8) return {kStream16, 16, kStream16N};
+  if (average <= 8) return {kStream16, 16, kStream16N, true};
   // room for groups half as large again as the average, so that few need a second tile
-  if (average <= 64) return {kStream, average <= 42 ? 64 : 96, kStreamN};
-  return {kTiles, kTile, kTile};
+  if (average <= 64) return {kStream, average <= 42 ? 64 : 96, kStreamN, true};
+  const bool wide = dtype == kF32 || !matrix_bound(R, N, K, (double)R * K + (double)G * N * K + 2.0 * R * N);
+  if (wide) return {kSmallTiles, 64, 64, true};
+  return {kLargeTiles, 256, 256, false};
 }
 
 }  // namespace
 
-int64_t matmul_tiles(int64_t R, int64_t N, int32_t G) {
-  const MatmulPlan p = plan_matmul(R, G);
+int64_t matmul_tiles(int64_t R, int64_t N, int64_t K, int32_t G, int32_t dtype) {
+  const MatmulPlan p = plan_matmul(R, N, K, G, dtype);
   // every group adds at most one tile that is not full, and a tile has a row
   return (std::min(R, R / p.rows + G) + 2) * ceil_div(N, p.n);
 }
 
-int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G) { return G * ceil_div(N, kTile) * ceil_div(K, kTile); }
+int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G) { return G * ceil_div(N, 64) * ceil_div(K, 64); }
 
-hipError_t launch_expert_matmul(const MatmulArgs& args, hipStream_t stream) {
-  if (args.R == 0) return hipSuccess;
-  MatmulArgs a = args;
-  a.large = matrix_bound(a.R, a.N, a.K, (double)a.R * a.K + (double)a.G * a.N * a.K + 2.0 * a.R * a.N);
-  const MatmulPlan p = plan_matmul(a.R, a.G);
-  const dim3 grid((unsigned)matmul_tiles(a.R, a.N, a.G));
+hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
+  if (a.R == 0) return hipSuccess;
+  const MatmulPlan p = plan_matmul(a.R, a.N, a.K, a.G, a.dtype);
+  const dim3 grid((unsigned)matmul_tiles(a.R, a.N, a.K, a.G, a.dtype));
   const int32_t n_tiles = (int32_t)ceil_div(a.N, p.n);
   switch (p.form) {
     case kStream16:
@@ -530,20 +679,29 @@ hipError_t launch_expert_matmul(const MatmulArgs& args, hipStream_t stream) {
     case kStream:
       expert_stream_kernel<<<grid, dim3(kStreamThreads), (size_t)kStreamSplit * p.rows * 8 * 16, stream>>>(a, n_tiles, p.rows);
       break;
-    case kTiles:
-      if (a.dtype == kF32 || !a.large) expert_matmul_kernel<true><<<grid, dim3(kMmThreads), 0, stream>>>(a);
-      else expert_matmul_kernel<false><<<grid, dim3(kMmThreads), 0, stream>>>(a);
+    case kSmallTiles:
+      expert_tile_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), 4 * TileKernel<2, 2, 1, 1, 4, true, false>::kStageBytes,
+                                              stream>>>(a, n_tiles);
+      break;
+    case kLargeTiles:
+      expert_tile_kernel<4, 2, 2, 4, 2, false><<<grid, dim3(512), 2 * TileKernel<4, 2, 2, 4, 2, false, false>::kStageBytes,
+                                               stream>>>(a, n_tiles);
       break;
   }
   return hipGetLastError();
 }
 
 hipError_t launch_expert_wgrad(const WgradArgs& a, hipStream_t stream) {
-  const int32_t ni = (int32_t)ceil_div(a.K, kTile), no = (int32_t)ceil_div(a.N, kTile);
-  const dim3 grid((unsigned)wgrad_tiles(a.N, a.K, a.G));
-  const bool large = matrix_bound(a.N, a.K, a.R, (double)a.R * (a.N + a.K) + 2.0 * a.G * a.N * a.K);
-  if (a.dtype == kF32 || !large) expert_wgrad_kernel<true><<<grid, dim3(kMmThreads), 0, stream>>>(a, ni, no);
-  else expert_wgrad_kernel<false><<<grid, dim3(kMmThreads), 0, stream>>>(a, ni, no);
+  const bool large = (double)a.N * a.K * a.R >= 0x1p33;
+  const int ti = large ? 256 : 64, to = large ? 128 : 64;
+  const int32_t ni = (int32_t)ceil_div(a.K, ti), no = (int32_t)ceil_div(a.N, to);
+  const dim3 grid((unsigned)((int64_t)a.G * ni * no));
+  if (large)
+    expert_wgrad_kernel<4, 2, 2, 2, 3, true><<<grid, dim3(512), 3 * TileKernel<4, 2, 2, 2, 3, true, true>::kStageBytes,
+                                             stream>>>(a, ni, no);
+  else
+    expert_wgrad_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), 4 * TileKernel<2, 2, 1, 1, 4, true, true>::kStageBytes,
+                                             stream>>>(a, ni, no);
   return hipGetLastError();
 }
 

@@ -66,6 +66,31 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int32_t G, int
   return Tile{-1, 0, 0, 0, 0};
 }
 
+// Number of tiles of all groups and, with `rest`, of the rows of no group.
+__device__ __forceinline__ int32_t count_tiles(const int32_t* offsets, int32_t G, int32_t R, int32_t size, bool rest) {
+  const int lane = threadIdx.x & 63;
+  const int32_t n = rest ? G + 2 : G;
+  int32_t mine = 0;
+  for (int32_t g = lane; g < n; g += 64) {
+    int32_t lo = 0, hi = 0;
+    if (g < G) lo = clamp_row(offsets[g], R), hi = clamp_row(offsets[g + 1], R);
+    else if (g == G) lo = clamp_row(offsets[G], R), hi = R;
+    else hi = clamp_row(offsets[0], R);
+    if (hi > lo) mine += (int32_t)(((int64_t)hi - lo + size - 1) / size);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) mine += __shfl_xor(mine, d);
+  return __builtin_amdgcn_readfirstlane(mine);
+}
+
+// Workgroup `id` of `total` on a chip of 8 dies (workgroups go round the dies
+// in turn): each die gets a run of neighbouring tiles, which share operands in
+// its L2.
+__device__ __forceinline__ int32_t die_order(int32_t id, int32_t total) {
+  const int32_t per = total >> 3;
+  return id < per * 8 ? (id & 7) * per + (id >> 3) : id;
+}
+
 // Scale of a block whose largest magnitude is amax (NaN: the block holds an
 // infinity or a NaN) and the factor its elements are multiplied with.
 __device__ __forceinline__ float block_scale(float amax, float& factor) {

@@ -114,7 +114,6 @@ struct MatmulArgs {
   void* y;
   int64_t X;
   int32_t R, N, K, KB, NB, G, topk, dtype;
-  bool large;                // 16-bit outputs come from the 8-bit matrix instruction
   FastDiv fd_topk;
 };
 
@@ -129,7 +128,7 @@ struct WgradArgs {
   int32_t R, N, K, G, dtype;
 };
 
-int64_t matmul_tiles(int64_t R, int64_t N, int32_t G);
+int64_t matmul_tiles(int64_t R, int64_t N, int64_t K, int32_t G, int32_t dtype);
 int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G);
 hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_expert_wgrad(const WgradArgs& a, hipStream_t stream);
