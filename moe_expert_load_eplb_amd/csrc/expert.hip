@@ -378,10 +378,10 @@ struct TileJob {
   const uint8_t* inner;      // first inner row of the tile
   int64_t inner_ld;
   int inner_rows;            // rows inside (the others read the last one and are not stored)
-  const float* inner_scale;  // matmul: [blocks], one for the tile; weight gradient: [blocks][inner_step], at the tile
-  int64_t inner_step;
-  const float* outer_scale;  // matmul: of this lane's row, next block 1 on; weight gradient: [blocks][outer_step]
-  int64_t outer_step;
+  const float* inner_scale;  // scale i, block b at inner_scale[i * inner_scale_ld + b * inner_step]: matmul: a scale
+  int64_t inner_scale_ld, inner_step;        // for each 128 inner rows from the tile's first on; weight gradient: for each
+  int inner_scales, inner_first;             // inner_first: the tile's first inner row within its 128
+  int64_t outer_step;        // from one block's scale of an outer row to the next one's
   int64_t block0, blocks, K; // first block, number of blocks, elements of a row (matmul: past it zeros)
 };
 
@@ -390,7 +390,7 @@ struct TileKernel {
   static constexpr int kWaves = WI * WO, kThreads = kWaves * 64;
   static constexpr int kInner = WI * IT * 32, kOuter = WO * OT * 32;
   static constexpr int kInnerLoads = kInner / 8 / kWaves, kOuterLoads = kOuter / 8 / kWaves;   // of 8 rows, per wave
-  static constexpr int kOuterScaleWaves = (kOuter + 63) / 64, kInnerScaleWaves = WGRAD ? (kInner + 63) / 64 : 0;
+  static constexpr int kOuterScaleWaves = (kOuter + 63) / 64, kInnerScaleWaves = WGRAD ? (kInner + 63) / 64 : 1;
   static constexpr int kLoads = kInnerLoads + kOuterLoads + 1;
   static constexpr int kScaleWords = (kOuterScaleWaves + kInnerScaleWaves + 1) * 64;
   static constexpr int kStageBytes = (kInner + kOuter) * kBlock + kScaleWords * 4;
@@ -398,6 +398,14 @@ struct TileKernel {
   static_assert(kOuterScaleWaves + kInnerScaleWaves <= kWaves, "one load of scales per wave");
 
   static __device__ __forceinline__ int inner_key(int r) { return (r & 3) | ((r / (16 * IT) & 1) << 2); }
+
+  // The element of a block that this lane's load p starts at.
+  static __device__ __forceinline__ int inner_part(int p, int wave, int lane) {
+    return ((lane & 7) ^ inner_key((wave * kInnerLoads + p) * 8 + (lane >> 3))) * 16;
+  }
+  static __device__ __forceinline__ int outer_part(int p, int wave, int lane) {
+    return ((lane & 7) ^ (((wave * kOuterLoads + p) * 8 + (lane >> 3)) & 7)) * 16;
+  }
 
   // `outer_row(r)`: pointer to outer row r of the tile (any valid row where it has none).
   template <typename OuterRow, typename OuterScale>
@@ -414,27 +422,23 @@ struct TileKernel {
         for (int i = 0; i < 16; ++i) acc[o][t][i] = 0.0f;
 
     // what this lane loads of every block
-    const uint8_t *ip[kInnerLoads], *op[kOuterLoads];
-    int ik[kInnerLoads], ok[kOuterLoads];    // its element of the block
+    uint32_t ip[kInnerLoads];                // from the tile's start: below 2^32, as rows are of at most 2^24 bytes
+    const uint8_t* op[kOuterLoads];
 #pragma unroll
     for (int p = 0; p < kInnerLoads; ++p) {
       const int r = (wave * kInnerLoads + p) * 8 + (lane >> 3);
-      ik[p] = ((lane & 7) ^ inner_key(r)) * 16;
-      ip[p] = job.inner + (int64_t)min(r, job.inner_rows - 1) * job.inner_ld;
+      ip[p] = (uint32_t)min(r, job.inner_rows - 1) * (uint32_t)job.inner_ld + inner_part(p, wave, lane);
     }
 #pragma unroll
-    for (int p = 0; p < kOuterLoads; ++p) {
-      const int r = (wave * kOuterLoads + p) * 8 + (lane >> 3);
-      ok[p] = ((lane & 7) ^ (r & 7)) * 16;
-      op[p] = outer_row(r);
-    }
+    for (int p = 0; p < kOuterLoads; ++p)
+      op[p] = outer_row((wave * kOuterLoads + p) * 8 + (lane >> 3)) + outer_part(p, wave, lane);
     const float* sp;
     int64_t s_step = job.outer_step;
     int s_at = wave * 64;
     if (wave < kOuterScaleWaves) {
       sp = outer_scale(wave * 64 + lane);
-    } else if (WGRAD && wave < kOuterScaleWaves + kInnerScaleWaves) {
-      sp = job.inner_scale + min((wave - kOuterScaleWaves) * 64 + lane, job.inner_rows - 1);
+    } else if (wave < kOuterScaleWaves + kInnerScaleWaves) {
+      sp = job.inner_scale + min((wave - kOuterScaleWaves) * 64 + lane, job.inner_scales - 1) * job.inner_scale_ld;
       s_step = job.inner_step;
     } else {
       sp = outer_scale(0);                   // keeps the count of loads equal; its place is not read
@@ -445,18 +449,22 @@ struct TileKernel {
       uint8_t* stage = lds + (int)(b % STAGES) * kStageBytes;
       uint8_t* si = stage + wave * kInnerLoads * 1024;
       uint8_t* so = stage + kInner * kBlock + wave * kOuterLoads * 1024;
+      const uint8_t* inner = job.inner + blk * kBlock;
       if (WGRAD || (blk + 1) * kBlock <= job.K) {
 #pragma unroll
-        for (int p = 0; p < kInnerLoads; ++p) load_to_lds16(ip[p] + blk * kBlock + ik[p], si + p * 1024);
+        for (int p = 0; p < kInnerLoads; ++p) load_to_lds16(inner + ip[p], si + p * 1024);
 #pragma unroll
-        for (int p = 0; p < kOuterLoads; ++p) load_to_lds16(op[p] + blk * kBlock + ok[p], so + p * 1024);
-      } else {                               // the end of K: any inner part of the row against zeros
+        for (int p = 0; p < kOuterLoads; ++p) load_to_lds16(op[p] + blk * kBlock, so + p * 1024);
+      } else {                               // the end of K: the row's first inner part against zeros
+        const int left = (int)(job.K - blk * kBlock);
 #pragma unroll
-        for (int p = 0; p < kInnerLoads; ++p)
-          load_to_lds16(ip[p] + (blk * kBlock + ik[p] < job.K ? blk * kBlock + ik[p] : 0), si + p * 1024);
+        for (int p = 0; p < kInnerLoads; ++p) {
+          const int k = inner_part(p, wave, lane);
+          load_to_lds16(k < left ? inner + ip[p] : job.inner + (ip[p] - k), si + p * 1024);
+        }
 #pragma unroll
         for (int p = 0; p < kOuterLoads; ++p)
-          load_to_lds16(blk * kBlock + ok[p] < job.K ? op[p] + blk * kBlock + ok[p] : g_zeros, so + p * 1024);
+          load_to_lds16(outer_part(p, wave, lane) < left ? op[p] + blk * kBlock : g_zeros, so + p * 1024);
       }
       load_to_lds4(sp + blk * s_step, stage + (kInner + kOuter) * kBlock + s_at * 4);
     };
@@ -464,12 +472,14 @@ struct TileKernel {
     for (int p = 0; p < STAGES - 1; ++p) load(p);
     for (int64_t b = 0; b < job.blocks; ++b) {
       wait_loads<kLoads * (STAGES - 2)>();   // this block's have arrived, of this wave
-      __syncthreads();                       // of all waves; and all are done with the block before
+      // of all waves; and all are done with the block before (a barrier that
+      // does not wait for the later blocks' loads)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       load(b + STAGES - 1);
       const uint8_t* it = lds + (int)(b % STAGES) * kStageBytes;
       const uint8_t* ot = it + kInner * kBlock;
       const float* scales = reinterpret_cast<const float*>(ot + kOuter * kBlock);
-      const float one = WGRAD ? 1.0f : job.inner_scale[job.block0 + b];
+      const float one = WGRAD ? 1.0f : scales[kOuterScaleWaves * 64 + (job.inner_first + wi) / kBlock];
       auto part = [&](const uint8_t* tile, int row, int key, int g) {
         return *reinterpret_cast<const i32x4*>(tile + row * kBlock + ((g ^ key) << 4));
       };
@@ -489,35 +499,44 @@ struct TileKernel {
           for (int j = 0; j < 4; ++j)
             si[t][j] = *reinterpret_cast<const f32x4*>(scales + kOuterScaleWaves * 64 + wi + half * (16 * IT) + 16 * t + j * 4);
       }
+      // a tile's scales are applied while the next tile's products are in the
+      // matrix pipeline
+      f32x16 d[2];
+      float sc[2];
+      auto apply = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          acc[j / IT][j % IT][i] += d[j & 1][i] * (WGRAD ? sc[j / IT & 1] * si[j % IT][i >> 2][i & 3] : sc[j / IT & 1]);
+      };
 #pragma unroll
       for (int o = 0; o < OT; ++o) {
         const int r = wo + o * 32 + col;
         i32x4 fo[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) fo[g] = part(ot, r, r & 7, (g >> 1) * 4 + half * 2 + (g & 1));
-        const float sc = scales[r] * one;
+        sc[o & 1] = scales[r] * one;
 #pragma unroll
         for (int t = 0; t < IT; ++t) {
-          f32x16 d;
+          const int j = o * IT + t;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) d[i] = 0.0f;
+          for (int i = 0; i < 16; ++i) d[j & 1][i] = 0.0f;
           if (WIDE) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                d = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[g], h), d, 0, 0, 0);
+                d[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[g], h), d[j & 1], 0, 0, 0);
           } else {
 #pragma unroll
             for (int g = 0; g < 4; g += 2)
-              d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              d[j & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                   __builtin_shufflevector(fi[t][g], fi[t][g + 1], 0, 1, 2, 3, 4, 5, 6, 7),
-                  __builtin_shufflevector(fo[g], fo[g + 1], 0, 1, 2, 3, 4, 5, 6, 7), d, 0, 0, 0, 0, 0, 0);
+                  __builtin_shufflevector(fo[g], fo[g + 1], 0, 1, 2, 3, 4, 5, 6, 7), d[j & 1], 0, 0, 0, 0, 0, 0);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[o][t][i] += d[i] * (WGRAD ? sc * si[t][i >> 2][i & 3] : sc);
+          if (j > 0) apply(j - 1);
         }
       }
+      apply(OT * IT - 1);
     }
     wait_loads<0>();                         // none may land in LDS that is no longer this workgroup's
   }
@@ -578,11 +597,11 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_tile_kernel(MatmulArgs a, 
     job.inner = a.w + ((int64_t)t.g * a.N + n0) * a.K;
     job.inner_ld = a.K;
     job.inner_rows = (int)(a.N - n0 < K::kInner ? a.N - n0 : K::kInner);
-    // the wave's n lie in one block of 128
-    const int64_t nb = (n0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WI * (IT * 32)) / kBlock;
-    job.inner_scale = a.w_scale + ((int64_t)t.g * a.NB + (nb < a.NB ? nb : a.NB - 1)) * a.KB;
-    job.inner_step = 0;
-    job.outer_step = 1;
+    job.inner_scale = a.w_scale + ((int64_t)t.g * a.NB + n0 / kBlock) * a.KB;
+    job.inner_scale_ld = a.KB;
+    job.inner_step = job.outer_step = 1;
+    job.inner_scales = a.NB - (int)(n0 / kBlock);
+    job.inner_first = (int)(n0 % kBlock);
     job.block0 = 0;
     job.blocks = a.KB;
     job.K = a.K;
@@ -618,7 +637,10 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
   job.inner_ld = a.Rp;
   job.inner_rows = (int)(a.K - i0 < K::kInner ? a.K - i0 : K::kInner);
   job.inner_scale = a.x_scale + i0;
+  job.inner_scale_ld = 1;
   job.inner_step = a.K;
+  job.inner_scales = job.inner_rows;
+  job.inner_first = 0;
   job.outer_step = a.N;
   job.K = a.Rp;
   const int64_t last = a.N - 1 - o0;
