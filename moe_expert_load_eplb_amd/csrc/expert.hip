@@ -397,14 +397,16 @@ struct TileKernel {
   static_assert(kInner % (8 * kWaves) == 0 && kOuter % (8 * kWaves) == 0, "whole loads");
   static_assert(kOuterScaleWaves + kInnerScaleWaves <= kWaves, "one load of scales per wave");
 
-  static __device__ __forceinline__ int inner_key(int r) { return (r & 3) | ((r / (16 * IT) & 1) << 2); }
+  // How the parts of row r are permuted: by bits 1 to 3 of the row, as two
+  // rows make one turn of the banks.
+  static __device__ __forceinline__ int key(int r) { return r >> 1 & 7; }
 
   // The element of a block that this lane's load p starts at.
   static __device__ __forceinline__ int inner_part(int p, int wave, int lane) {
-    return ((lane & 7) ^ inner_key((wave * kInnerLoads + p) * 8 + (lane >> 3))) * 16;
+    return ((lane & 7) ^ key((wave * kInnerLoads + p) * 8 + (lane >> 3))) * 16;
   }
   static __device__ __forceinline__ int outer_part(int p, int wave, int lane) {
-    return ((lane & 7) ^ (((wave * kOuterLoads + p) * 8 + (lane >> 3)) & 7)) * 16;
+    return ((lane & 7) ^ key((wave * kOuterLoads + p) * 8 + (lane >> 3))) * 16;
   }
 
   // `outer_row(r)`: pointer to outer row r of the tile (any valid row where it has none).
@@ -480,8 +482,8 @@ struct TileKernel {
       const uint8_t* ot = it + kInner * kBlock;
       const float* scales = reinterpret_cast<const float*>(ot + kOuter * kBlock);
       const float one = WGRAD ? 1.0f : scales[kOuterScaleWaves * 64 + (job.inner_first + wi) / kBlock];
-      auto part = [&](const uint8_t* tile, int row, int key, int g) {
-        return *reinterpret_cast<const i32x4*>(tile + row * kBlock + ((g ^ key) << 4));
+      auto part = [&](const uint8_t* tile, int row, int g) {
+        return *reinterpret_cast<const i32x4*>(tile + row * kBlock + ((g ^ key(row)) << 4));
       };
       // part 2 s' + half * 2 ... : a lane's 64 of the block's 128 elements, the same of both operands
       i32x4 fi[IT][4];
@@ -489,7 +491,7 @@ struct TileKernel {
       for (int t = 0; t < IT; ++t) {
         const int r = wi + (col >> 2 & 1) * (16 * IT) + 16 * t + (col >> 3) * 4 + (col & 3);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) fi[t][g] = part(it, r, inner_key(r), (g >> 1) * 4 + half * 2 + (g & 1));
+        for (int g = 0; g < 4; ++g) fi[t][g] = part(it, r, (g >> 1) * 4 + half * 2 + (g & 1));
       }
       f32x4 si[IT][4];
       if (WGRAD) {
@@ -508,13 +510,16 @@ struct TileKernel {
         for (int i = 0; i < 16; ++i)
           acc[j / IT][j % IT][i] += d[j & 1][i] * (WGRAD ? sc[j / IT & 1] * si[j % IT][i >> 2][i & 3] : sc[j / IT & 1]);
       };
+      constexpr int kSets = OT < 4 ? 2 : 1;  // outer fragments ahead of the matrix instructions: as registers allow
+      i32x4 fo[kSets][4];
+      auto outer = [&](int o) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) fo[o % kSets][g] = part(ot, wo + o * 32 + col, (g >> 1) * 4 + half * 2 + (g & 1));
+        sc[o & 1] = scales[wo + o * 32 + col] * one;
+      };
+      outer(0);
 #pragma unroll
       for (int o = 0; o < OT; ++o) {
-        const int r = wo + o * 32 + col;
-        i32x4 fo[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) fo[g] = part(ot, r, r & 7, (g >> 1) * 4 + half * 2 + (g & 1));
-        sc[o & 1] = scales[r] * one;
 #pragma unroll
         for (int t = 0; t < IT; ++t) {
           const int j = o * IT + t;
@@ -525,15 +530,17 @@ struct TileKernel {
             for (int g = 0; g < 4; ++g)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                d[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[g], h), d[j & 1], 0, 0, 0);
+                d[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[o % kSets][g], h), d[j & 1], 0, 0, 0);
           } else {
 #pragma unroll
             for (int g = 0; g < 4; g += 2)
               d[j & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                   __builtin_shufflevector(fi[t][g], fi[t][g + 1], 0, 1, 2, 3, 4, 5, 6, 7),
-                  __builtin_shufflevector(fo[g], fo[g + 1], 0, 1, 2, 3, 4, 5, 6, 7), d[j & 1], 0, 0, 0, 0, 0, 0);
+                  __builtin_shufflevector(fo[o % kSets][g], fo[o % kSets][g + 1], 0, 1, 2, 3, 4, 5, 6, 7), d[j & 1], 0, 0, 0, 0, 0, 0);
           }
           if (j > 0) apply(j - 1);
+          // the tile before has had its scale by now
+          if (t == (kSets == 2 ? 0 : IT - 1) && o + 1 < OT) outer(o + 1);
         }
       }
       apply(OT * IT - 1);
@@ -551,10 +558,11 @@ struct TileKernel {
   }
 
   // Stores the wave's values: row(r) is outer row r's first element in the
-  // output or -1, `left` the inner values from the tile's start on.
-  template <typename Row>
+  // output or -1, some(r) whether it has values (else zeros), `left` the inner
+  // values from the tile's start on.
+  template <typename Row, typename Some>
   static __device__ __forceinline__ void store(const f32x16 (&acc)[OT][IT], void* out, int32_t dtype, int64_t width,
-                                               int64_t left, Row row) {
+                                               int64_t left, Row row, Some some) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, col = lane & 31;
     const int wi = wave % WI * (IT * 32) + half * (16 * IT), wo = wave / WI * (OT * 32);
@@ -562,11 +570,12 @@ struct TileKernel {
     for (int o = 0; o < OT; ++o) {
       const int64_t at = row(wo + o * 32 + col);
       if (at < 0) continue;
+      const bool in = some(wo + o * 32 + col);
 #pragma unroll
       for (int t = 0; t < IT; ++t) {
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = acc[o][t][i];
+        for (int i = 0; i < 16; ++i) v[i] = in ? acc[o][t][i] : 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; i += 8) {
           const int64_t n = wi + 16 * t + i;
@@ -608,15 +617,9 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_tile_kernel(MatmulArgs a, 
     K::run(job, tile_lds, [&](int r) { return a.q + (int64_t)max(src[r], 0) * a.K; },
            [&](int r) { return a.scale + (int64_t)max(src[r < K::kOuter ? r : 0], 0) * a.KB; }, acc);
   }
-  K::store(acc, a.y, a.dtype, a.N, a.N - n0, [&](int r) -> int64_t {
-    return r < t.rows && src[r] >= 0 ? (int64_t)(t.row + r) * a.N + n0 : -1;
-  });
-  // rows of nothing are zero
-  for (int r = 0; r < t.rows; ++r) {
-    if (src[r] >= 0) continue;
-    for (int64_t n = threadIdx.x; n < K::kInner && n0 + n < a.N; n += K::kThreads)
-      store_float(a.y, a.dtype, (int64_t)(t.row + r) * a.N + n0 + n, 0.0f);
-  }
+  K::store(acc, a.y, a.dtype, a.N, a.N - n0,
+           [&](int r) -> int64_t { return r < t.rows ? (int64_t)(t.row + r) * a.N + n0 : -1; },
+           [&](int r) { return src[r] >= 0; });
 }
 
 template <int WI, int WO, int IT, int OT, int STAGES, bool WIDE>
@@ -645,19 +648,13 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
   job.K = a.Rp;
   const int64_t last = a.N - 1 - o0;
   f32x16 acc[OT][IT];
-  if (job.blocks > 0) {
+  const bool some = job.blocks > 0;
+  if (some)
     K::run(job, tile_lds, [&](int r) { return a.dy + (o0 + (r < last ? r : last)) * a.Rp; },
            [&](int r) { return a.dy_scale + o0 + (r < last ? r : last); }, acc);
-  } else {
-#pragma unroll
-    for (int o = 0; o < OT; ++o)
-#pragma unroll
-      for (int t = 0; t < IT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[o][t][i] = 0.0f;
-  }
   K::store(acc, a.dw, a.dtype, a.K, a.K - i0,
-           [&](int r) -> int64_t { return r <= last ? ((int64_t)g * a.N + o0 + r) * a.K + i0 : -1; });
+           [&](int r) -> int64_t { return r <= last ? ((int64_t)g * a.N + o0 + r) * a.K + i0 : -1; },
+           [&](int) { return some; });
 }
 
 // The form of a product: rows to a tile and n to a workgroup.
