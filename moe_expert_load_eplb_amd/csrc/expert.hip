@@ -394,6 +394,7 @@ struct TileKernel {
   static constexpr int kLoads = kInnerLoads + kOuterLoads + 1;
   static constexpr int kScaleWords = (kOuterScaleWaves + kInnerScaleWaves + 1) * 64;
   static constexpr int kStageBytes = (kInner + kOuter) * kBlock + kScaleWords * 4;
+  static constexpr int kLdsBytes = STAGES * kStageBytes;
   static_assert(kInner % (8 * kWaves) == 0 && kOuter % (8 * kWaves) == 0, "whole loads");
   static_assert(kOuterScaleWaves + kInnerScaleWaves <= kWaves, "one load of scales per wave");
 
@@ -591,12 +592,13 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_tile_kernel(MatmulArgs a, 
   typedef TileKernel<WI, WO, IT, OT, STAGES, WIDE, false> K;
   extern __shared__ __attribute__((aligned(16))) uint8_t tile_lds[];
   __shared__ int32_t src[K::kOuter];
-  const int32_t total = count_tiles(a.offsets, a.G, a.R, K::kOuter, true) * n_tiles;
-  if ((int32_t)blockIdx.x >= total) return;
-  const int32_t id = die_order(blockIdx.x, total);
-  const Tile t = find_tile(a.offsets, a.G, a.R, K::kOuter, id / n_tiles, true);
+  const int32_t row_tiles = count_tiles(a.offsets, a.G, a.R, K::kOuter, true);
+  if ((int64_t)blockIdx.x >= (int64_t)row_tiles * n_tiles) return;
+  int32_t row, column;
+  band_order(die_order(blockIdx.x, row_tiles * n_tiles), row_tiles, n_tiles, row, column);
+  const Tile t = find_tile(a.offsets, a.G, a.R, K::kOuter, row, true);
   if (t.g < 0) return;
-  const int64_t n0 = (int64_t)(id % n_tiles) * K::kInner;
+  const int64_t n0 = (int64_t)column * K::kInner;
   for (int r = threadIdx.x; r < K::kOuter; r += K::kThreads)
     src[r] = r < t.rows && t.g < a.G ? source_row(a, t.row + r) : -1;
   __syncthreads();
@@ -628,7 +630,9 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
   extern __shared__ __attribute__((aligned(16))) uint8_t tile_lds[];
   const int32_t id = die_order(blockIdx.x, gridDim.x);
   const int32_t g = id / (ni * no);
-  const int64_t i0 = (int64_t)(id % ni) * K::kInner, o0 = (int64_t)(id / ni % no) * K::kOuter;
+  int32_t row, column;
+  band_order(id - g * (ni * no), no, ni, row, column);
+  const int64_t i0 = (int64_t)column * K::kInner, o0 = (int64_t)row * K::kOuter;
   // the group's blocks of 128 rows
   const int32_t before = count_tiles(a.offsets, g, a.R, kBlock, false);
   const int32_t lo = clamp_row(a.offsets[g], a.R), hi = clamp_row(a.offsets[g + 1], a.R);
@@ -699,11 +703,11 @@ hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
       expert_stream_kernel<<<grid, dim3(kStreamThreads), (size_t)kStreamSplit * p.rows * 8 * 16, stream>>>(a, n_tiles, p.rows);
       break;
     case kSmallTiles:
-      expert_tile_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), 4 * TileKernel<2, 2, 1, 1, 4, true, false>::kStageBytes,
+      expert_tile_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), TileKernel<2, 2, 1, 1, 4, true, false>::kLdsBytes,
                                               stream>>>(a, n_tiles);
       break;
     case kLargeTiles:
-      expert_tile_kernel<4, 2, 2, 4, 2, false><<<grid, dim3(512), 2 * TileKernel<4, 2, 2, 4, 2, false, false>::kStageBytes,
+      expert_tile_kernel<4, 2, 2, 4, 2, false><<<grid, dim3(512), TileKernel<4, 2, 2, 4, 2, false, false>::kLdsBytes,
                                                stream>>>(a, n_tiles);
       break;
   }
@@ -716,10 +720,10 @@ hipError_t launch_expert_wgrad(const WgradArgs& a, hipStream_t stream) {
   const int32_t ni = (int32_t)ceil_div(a.K, ti), no = (int32_t)ceil_div(a.N, to);
   const dim3 grid((unsigned)((int64_t)a.G * ni * no));
   if (large)
-    expert_wgrad_kernel<4, 2, 2, 2, 3, true><<<grid, dim3(512), 3 * TileKernel<4, 2, 2, 2, 3, true, true>::kStageBytes,
+    expert_wgrad_kernel<4, 2, 2, 2, 3, true><<<grid, dim3(512), TileKernel<4, 2, 2, 2, 3, true, true>::kLdsBytes,
                                              stream>>>(a, ni, no);
   else
-    expert_wgrad_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), 4 * TileKernel<2, 2, 1, 1, 4, true, true>::kStageBytes,
+    expert_wgrad_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), TileKernel<2, 2, 1, 1, 4, true, true>::kLdsBytes,
                                              stream>>>(a, ni, no);
   return hipGetLastError();
 }

@@ -91,6 +91,16 @@ __device__ __forceinline__ int32_t die_order(int32_t id, int32_t total) {
   return id < per * 8 ? (id & 7) * per + (id >> 3) : id;
 }
 
+// Tile `id` of rows x columns tiles taken in bands of four rows, column by
+// column: the 32 tiles that a die works on at once are 4 x 8, which read 12
+// different operand tiles (one row after the other: 18 of 2 x 16).
+__device__ __forceinline__ void band_order(int32_t id, int32_t rows, int32_t columns, int32_t& row, int32_t& column) {
+  const int32_t band = id / (4 * columns), at = id - band * 4 * columns;
+  const int32_t high = rows - band * 4 < 4 ? rows - band * 4 : 4;
+  column = at / high;
+  row = band * 4 + at - column * high;
+}
+
 // Scale of a block whose largest magnitude is amax (NaN: the block holds an
 // infinity or a NaN) and the factor its elements are multiplied with.
 __device__ __forceinline__ float block_scale(float amax, float& factor) {
