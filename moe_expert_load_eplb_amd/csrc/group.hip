@@ -80,11 +80,18 @@ __global__ __launch_bounds__(512) void group_place_kernel(const int32_t* __restr
     if (sp.segs == 1) {
       for (int w = 0; w < waves; ++w) total += lds[w * C + p];
     } else {
+      // 16 loads in flight; past the last segment its count again, not added
       const int32_t* col = ws + l * sp.segs * C + p;
-      for (int64_t j = 0; j < sp.segs; ++j) {
-        const int32_t c = col[j * C];
-        total += c;
-        before += j < s ? c : 0;
+      const int segs = (int)sp.segs, here = (int)s;
+      for (int j0 = 0; j0 < segs; j0 += 16) {
+        int32_t c[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) c[j] = col[(int64_t)min(j0 + j, segs - 1) * C];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          total += j0 + j < segs ? c[j] : 0;
+          before += j0 + j < here ? c[j] : 0;
+        }
       }
     }
     start[p] = sum;

@@ -91,15 +91,19 @@ __global__ __launch_bounds__(kQThreads) void quantize_rows_kernel(const void* __
   }
 }
 
-// One block of 128 rows and 64 columns per workgroup: a thread holds 16 rows
-// of 2 columns, whose 8-bit values are 16 consecutive bytes of the output.
+// One block of 128 rows and 128 columns per workgroup: a thread holds 8 rows
+// of 8 columns (16 bytes a load), whose 8-bit values are 8 consecutive bytes of
+// 8 rows of the output; they pass through LDS so that a store covers a whole
+// 128-byte run.
+template <bool VEC>
 __global__ __launch_bounds__(kQThreads) void quantize_columns_kernel(const void* __restrict__ x, int32_t dtype,
                                                                      int64_t ld, int64_t X, int64_t C,
                                                                      const int32_t* __restrict__ rows, int32_t R,
                                                                      FastDiv fd_k, const int32_t* __restrict__ offsets,
                                                                      int32_t G, int64_t Rp, uint8_t* __restrict__ q,
                                                                      float* __restrict__ scale, int32_t col_tiles) {
-  __shared__ float part[8][64];
+  __shared__ float part[16][kBlock + 4];
+  __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock][kBlock + 16];
   __shared__ int32_t src[kBlock];
   const int32_t b = (int32_t)(blockIdx.x / col_tiles);
   const Tile t = find_tile(offsets, G, R, kBlock, b, false);
@@ -117,36 +121,44 @@ __global__ __launch_bounds__(kQThreads) void quantize_columns_kernel(const void*
     src[threadIdx.x] = from;
   }
   __syncthreads();
-  const int pair = threadIdx.x & 31, band = threadIdx.x >> 5;
-  const int64_t c = (int64_t)(blockIdx.x % col_tiles) * 64 + pair * 2;
-  float v[2][16];
+  const int cx = threadIdx.x & 15, band = threadIdx.x >> 4;
+  const int64_t c0 = (int64_t)(blockIdx.x % col_tiles) * kBlock, c = c0 + cx * 8;
+  float v[8][8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int32_t from = src[band * 16 + i];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      v[j][i] = from >= 0 && c + j < C ? load_as_float(x, dtype, from * ld + c + j) : 0.0f;
+  for (int i = 0; i < 8; ++i) {
+    const int32_t from = src[band * 8 + i];
+    load8<VEC>(x, dtype, (int64_t)(from < 0 ? 0 : from) * ld + c, from < 0 ? 0 : C - c, v[i]);
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) part[band][pair * 2 + j] = magnitude(v[j]);
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (c + j >= C) break;
+  for (int j = 0; j < 8; ++j) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i][pair * 2 + j]);
-    float f;
-    const float sc = scale_of(m, f);
-    if (band == 0) scale[(int64_t)b * C + c + j] = sc;
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i][j]) <= 3.4028235e38f ? fabsf(v[i][j]) : INFINITY);
+    part[band][cx * 8 + j] = m;
+  }
+  __syncthreads();
+  float f[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[j][i] = scaled(v[j][i], f);
-    uint4 w;
-    w.x = pack_f8(v[j][0], v[j][1], v[j][2], v[j][3]);
-    w.y = pack_f8(v[j][4], v[j][5], v[j][6], v[j][7]);
-    w.z = pack_f8(v[j][8], v[j][9], v[j][10], v[j][11]);
-    w.w = pack_f8(v[j][12], v[j][13], v[j][14], v[j][15]);
-    *reinterpret_cast<uint4*>(q + (c + j) * Rp + (int64_t)b * kBlock + band * 16) = w;
+  for (int j = 0; j < 8; ++j) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, part[i][cx * 8 + j]);
+    const float sc = scale_of(m, f[j]);
+    if (band == 0 && c + j < C) scale[(int64_t)b * C + c + j] = sc;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i][j] = scaled(v[i][j], f[j]);
+    *reinterpret_cast<uint2*>(&turned[cx * 8 + j][band * 8]) =
+        make_uint2(pack_f8(v[0][j], v[1][j], v[2][j], v[3][j]), pack_f8(v[4][j], v[5][j], v[6][j], v[7][j]));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int i = threadIdx.x + p * kQThreads, r = i >> 3, at = (i & 7) * 16;
+    if (c0 + r < C)
+      *reinterpret_cast<uint4*>(q + (c0 + r) * Rp + (int64_t)b * kBlock + at) = *reinterpret_cast<const uint4*>(&turned[r][at]);
   }
 }
 
@@ -220,9 +232,16 @@ hipError_t launch_quantize_columns(const void* x, int32_t dtype, int64_t ld, int
                                    const int32_t* rows, int64_t R, int32_t K, const int32_t* offsets, int32_t G,
                                    int64_t Rp, uint8_t* q, float* scale, hipStream_t stream) {
   if (Rp == 0) return hipSuccess;
-  const int64_t col_tiles = ceil_div(C, 64);
-  quantize_columns_kernel<<<dim3((unsigned)(Rp / kBlock * col_tiles)), dim3(kQThreads), 0, stream>>>(
-      x, dtype, ld, X, C, rows, (int32_t)R, fastdiv_make((uint32_t)K), offsets, G, Rp, q, scale, (int32_t)col_tiles);
+  const int64_t col_tiles = ceil_div(C, kBlock);
+  const dim3 grid((unsigned)(Rp / kBlock * col_tiles));
+  const FastDiv fd = fastdiv_make((uint32_t)K);
+  const bool vec = aligned(x, 16) && ld * dtype_size(dtype) % 16 == 0;
+  if (vec)
+    quantize_columns_kernel<true><<<grid, dim3(kQThreads), 0, stream>>>(x, dtype, ld, X, C, rows, (int32_t)R, fd, offsets,
+                                                                        G, Rp, q, scale, (int32_t)col_tiles);
+  else
+    quantize_columns_kernel<false><<<grid, dim3(kQThreads), 0, stream>>>(x, dtype, ld, X, C, rows, (int32_t)R, fd, offsets,
+                                                                         G, Rp, q, scale, (int32_t)col_tiles);
   return hipGetLastError();
 }
 
