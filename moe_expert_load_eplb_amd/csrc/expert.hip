@@ -117,8 +117,7 @@ __device__ __forceinline__ void store4(void* p, int32_t dtype, int64_t at, int l
 // the end are clamped to the last ones and not used): a load that may or may
 // not have been issued makes every wait behind it wait for all of them.
 constexpr int kStreamThreads = 256;
-constexpr int kStream16N = 64;               // n of a workgroup: 16 of each wave
-constexpr int kStreamN = 32;                 // n of a workgroup, of each wave
+constexpr int kStream16N = 64;             // n of a workgroup: 16 of each wave
 
 // The two 16-byte parts of block kb that a lane of `quad` holds; at the end of
 // a row that has no such part, its first ones (the caller zeroes the other
@@ -212,116 +211,6 @@ __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulA
   if (col < t.rows) store4(a.y, a.dtype, (int64_t)(t.row + col) * a.N + n, a.N - n, a.N % 4 == 0, acc);
 }
 
-// Up to 96 rows of one group against 32 n: the workgroup's four waves take
-// every fourth block of K each, all operands straight from memory (the rows,
-// read by every workgroup of the group, from the caches), and add their sums
-// in LDS at the end, in order.  Without a barrier in the loop the waves run
-// free; a tile's next rows are loaded as soon as its last ones are used.
-constexpr int kStreamSplit = kStreamThreads / 64;          // waves that share a tile's K
-
-// The loop for NT tiles of 16 rows (all of them present).
-template <int NT>
-__device__ __forceinline__ void stream_tiles(const MatmulArgs& a, const Tile& t, int n0, int wave, f32x4* sums) {
-  constexpr int kAheadW = 2;                 // blocks of the weights in flight
-  const int lane = threadIdx.x & 63, quad = lane >> 4, col = lane & 15;
-  f32x4 acc[NT][2];
-#pragma unroll
-  for (int o = 0; o < NT; ++o) acc[o][0] = acc[o][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const uint8_t* w[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) w[u] = a.w + ((int64_t)t.g * a.N + min(n0 + u * 16 + col, a.N - 1)) * a.K;
-  i32x4 rw[kAheadW][2][2], rx[NT][2];
-  float sx[NT];
-  auto block = [&](int b) { return min(b * kStreamSplit + wave, a.KB - 1); };
-  auto load_w = [&](int slot, int b) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) load_parts(w[u], block(b), quad, a.K, rw[slot][u][0], rw[slot][u][1]);
-  };
-  int32_t from[NT];
-#pragma unroll
-  for (int o = 0; o < NT; ++o) from[o] = o * 16 + col < t.rows ? source_row(a, t.row + o * 16 + col) : -1;
-  ScaleRow ws(a.w_scale + ((int64_t)t.g * a.NB + n0 / kBlock) * a.KB, a.KB);
-  load_w(0, 0);
-  auto load_x = [&](int o, int b) {
-    const int64_t row = max(from[o], 0);
-    load_parts(a.q + row * a.K, block(b), quad, a.K, rx[o][0], rx[o][1]);
-    sx[o] = a.scale[row * a.KB + block(b)];
-  };
-#pragma unroll
-  for (int o = 0; o < NT; ++o) load_x(o, 0);
-#pragma unroll
-  for (int p = 1; p < kAheadW; ++p) load_w(p, p);
-  const int steps = (a.KB + kStreamSplit - 1) / kStreamSplit;
-  for (int b0 = 0; b0 < steps; b0 += kAheadW) {
-    ws.load_next((b0 + kAheadW) * kStreamSplit);
-#pragma unroll
-    for (int p = 0; p < kAheadW; ++p) {
-      const int b = b0 + p, kb = b * kStreamSplit + wave;
-      const i32x4 zero = {0, 0, 0, 0};
-      const bool lo = kb * kBlock + quad * 16 < a.K, hi = kb * kBlock + quad * 16 + 64 < a.K;
-      const bool in = kb < a.KB;             // past the end: not added
-      const float wk = ws.get(p * kStreamSplit + wave);
-      Fragment<true> fw[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) fw[u].set(rw[p][u][0], rw[p][u][1]);
-#pragma unroll
-      for (int o = 0; o < NT; ++o) {
-        Fragment<true> fx;
-        fx.set(lo ? rx[o][0] : zero, hi ? rx[o][1] : zero);
-        const float sc = sx[o] * wk;
-        load_x(o, b + 1);
-        f32x4 d[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) d[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[u].v[c], fx.v[c], d[u], 0, 0, 0);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[o][u][j] = in ? acc[o][u][j] + d[u][j] * sc : acc[o][u][j];
-      }
-      load_w(p, b + kAheadW);                // behind the rows' loads: loads return in order
-    }
-    ws.advance();
-  }
-#pragma unroll
-  for (int o = 0; o < NT; ++o)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) sums[(o * 2 + u) * 64 + lane] = from[o] >= 0 ? acc[o][u] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-}
-
-__global__ __launch_bounds__(kStreamThreads, 2) void expert_stream_kernel(MatmulArgs a, int32_t n_tiles, int32_t rows) {
-  extern __shared__ __attribute__((aligned(16))) f32x4 sums[];   // [wave][rows / 16][2][64]
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = (int)(blockIdx.x % n_tiles) * kStreamN;
-  const Tile t = find_tile(a.offsets, a.G, a.R, rows, (int32_t)(blockIdx.x / n_tiles), true);
-  if (t.g < 0) return;
-  const bool some = t.g < a.G && a.X > 0;
-  const int tiles = (t.rows + 15) >> 4, each = rows * 8;
-  if (some) {
-    // a loop of its own for every number of tiles: no load behind a branch
-    f32x4* mine = sums + wave * each;
-    switch (tiles) {
-      case 1: stream_tiles<1>(a, t, n0, wave, mine); break;
-      case 2: stream_tiles<2>(a, t, n0, wave, mine); break;
-      case 3: stream_tiles<3>(a, t, n0, wave, mine); break;
-      case 4: stream_tiles<4>(a, t, n0, wave, mine); break;
-      case 5: stream_tiles<5>(a, t, n0, wave, mine); break;
-      default: stream_tiles<6>(a, t, n0, wave, mine); break;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tiles * 128; i += kStreamThreads) {
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (some) {
-#pragma unroll
-      for (int k = 0; k < kStreamSplit; ++k) v += sums[k * each + i];
-    }
-    const int r = (i >> 7) * 16 + (i & 15), n = n0 + (i >> 6 & 1) * 16 + (i >> 4 & 3) * 4;
-    if (r < t.rows && n < a.N) store4(a.y, a.dtype, (int64_t)(t.row + r) * a.N + n, a.N - n, a.N % 4 == 0, v);
-  }
-}
-
 // ---------------------------------------------------------------- tiles
 // Tiles of the output, for many rows.  A workgroup of WI x WO waves computes
 // (WI IT 32) inner x (WO OT 32) outer values, a wave IT x OT tiles of 32 x 32
@@ -382,7 +271,8 @@ struct TileJob {
   int64_t inner_scale_ld, inner_step;        // for each 128 inner rows from the tile's first on; weight gradient: for each
   int inner_scales, inner_first;             // inner_first: the tile's first inner row within its 128
   int64_t outer_step;        // from one block's scale of an outer row to the next one's
-  int64_t block0, blocks, K; // first block, number of blocks, elements of a row (matmul: past it zeros)
+  int64_t K;                 // elements of a row (matmul: past it zeros)
+  int block0, blocks;        // first block, number of blocks
 };
 
 template <int WI, int WO, int IT, int OT, int STAGES, bool WIDE, bool WGRAD>
@@ -447,9 +337,10 @@ struct TileKernel {
       sp = outer_scale(0);                   // keeps the count of loads equal; its place is not read
       s_at = (kOuterScaleWaves + kInnerScaleWaves) * 64;
     }
-    auto load = [&](int64_t b) {             // block b of the job to its stage; past the end the last one again
-      const int64_t blk = job.block0 + (b < job.blocks ? b : job.blocks - 1);
-      uint8_t* stage = lds + (int)(b % STAGES) * kStageBytes;
+    // block b of the job to stage `slot`; past the end the last one again
+    auto load = [&](int b, int slot) {
+      const int64_t blk = job.block0 + min(b, job.blocks - 1);
+      uint8_t* stage = lds + slot * kStageBytes;
       uint8_t* si = stage + wave * kInnerLoads * 1024;
       uint8_t* so = stage + kInner * kBlock + wave * kOuterLoads * 1024;
       const uint8_t* inner = job.inner + blk * kBlock;
@@ -472,14 +363,16 @@ struct TileKernel {
       load_to_lds4(sp + blk * s_step, stage + (kInner + kOuter) * kBlock + s_at * 4);
     };
 #pragma unroll
-    for (int p = 0; p < STAGES - 1; ++p) load(p);
-    for (int64_t b = 0; b < job.blocks; ++b) {
+    for (int p = 0; p < STAGES - 1; ++p) load(p, p);
+    int slot = 0;
+    for (int b = 0; b < job.blocks; ++b) {
       wait_loads<kLoads * (STAGES - 2)>();   // this block's have arrived, of this wave
       // of all waves; and all are done with the block before (a barrier that
       // does not wait for the later blocks' loads)
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      load(b + STAGES - 1);
-      const uint8_t* it = lds + (int)(b % STAGES) * kStageBytes;
+      load(b + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+      const uint8_t* it = lds + slot * kStageBytes;
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
       const uint8_t* ot = it + kInner * kBlock;
       const float* scales = reinterpret_cast<const float*>(ot + kOuter * kBlock);
       const float one = WGRAD ? 1.0f : scales[kOuterScaleWaves * 64 + (job.inner_first + wi) / kBlock];
@@ -526,7 +419,17 @@ struct TileKernel {
           const int j = o * IT + t;
 #pragma unroll
           for (int i = 0; i < 16; ++i) d[j & 1][i] = 0.0f;
-          if (WIDE) {
+          if (WIDE && IT * OT == 1) {        // no other tile to fill the pipeline with: two sums side by side
+#pragma unroll
+            for (int i = 0; i < 16; ++i) d[1][i] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                d[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[o % kSets][g], h), d[h], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) d[0][i] += d[1][i];
+          } else if (WIDE) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -590,12 +493,15 @@ struct TileKernel {
 template <int WI, int WO, int IT, int OT, int STAGES, bool WIDE>
 __global__ __launch_bounds__(WI* WO * 64) void expert_tile_kernel(MatmulArgs a, int32_t n_tiles) {
   typedef TileKernel<WI, WO, IT, OT, STAGES, WIDE, false> K;
+  constexpr bool kOrdered = IT * OT > 1;     // few blocks of small tiles: counting them all would cost more than it gives
   extern __shared__ __attribute__((aligned(16))) uint8_t tile_lds[];
   __shared__ int32_t src[K::kOuter];
-  const int32_t row_tiles = count_tiles(a.offsets, a.G, a.R, K::kOuter, true);
-  if ((int64_t)blockIdx.x >= (int64_t)row_tiles * n_tiles) return;
-  int32_t row, column;
-  band_order(die_order(blockIdx.x, row_tiles * n_tiles), row_tiles, n_tiles, row, column);
+  int32_t row = blockIdx.x / n_tiles, column = blockIdx.x % n_tiles;
+  if (kOrdered) {
+    const int32_t row_tiles = count_tiles(a.offsets, a.G, a.R, K::kOuter, true);
+    if ((int64_t)blockIdx.x >= (int64_t)row_tiles * n_tiles) return;
+    band_order(die_order(blockIdx.x, row_tiles * n_tiles), row_tiles, n_tiles, row, column);
+  }
   const Tile t = find_tile(a.offsets, a.G, a.R, K::kOuter, row, true);
   if (t.g < 0) return;
   const int64_t n0 = (int64_t)column * K::kInner;
@@ -638,8 +544,8 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
   const int32_t lo = clamp_row(a.offsets[g], a.R), hi = clamp_row(a.offsets[g + 1], a.R);
   TileJob job;
   job.block0 = before;
-  job.blocks = hi > lo ? ((int64_t)hi - lo + kBlock - 1) / kBlock : 0;
-  if (job.block0 + job.blocks > a.Rp / kBlock) job.blocks = a.Rp / kBlock - job.block0;
+  job.blocks = hi > lo ? (int)(((int64_t)hi - lo + kBlock - 1) / kBlock) : 0;
+  if ((int64_t)job.block0 + job.blocks > a.Rp / kBlock) job.blocks = (int)(a.Rp / kBlock) - job.block0;
   job.inner = a.x + i0 * a.Rp;
   job.inner_ld = a.Rp;
   job.inner_rows = (int)(a.K - i0 < K::kInner ? a.K - i0 : K::kInner);
@@ -662,7 +568,7 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
 }
 
 // The form of a product: rows to a tile and n to a workgroup.
-enum MatmulForm { kStream16, kStream, kSmallTiles, kLargeTiles };
+enum MatmulForm { kStream16, kSmallTiles, kLargeTiles };
 
 struct MatmulPlan {
   MatmulForm form;
@@ -673,8 +579,6 @@ struct MatmulPlan {
 MatmulPlan plan_matmul(int64_t R, int64_t N, int64_t K, int32_t G, int32_t dtype) {
   const int64_t average = ceil_div(R, G);
   if (average <= 8) return {kStream16, 16, kStream16N, true};
-  // room for groups half as large again as the average, so that few need a second tile
-  if (average <= 64) return {kStream, average <= 42 ? 64 : 96, kStreamN, true};
   const bool wide = dtype == kF32 || !matrix_bound(R, N, K, (double)R * K + (double)G * N * K + 2.0 * R * N);
   if (wide) return {kSmallTiles, 64, 64, true};
   return {kLargeTiles, 256, 256, false};
@@ -698,9 +602,6 @@ hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
   switch (p.form) {
     case kStream16:
       expert_stream16_kernel<<<grid, dim3(kStreamThreads), 0, stream>>>(a, n_tiles);
-      break;
-    case kStream:
-      expert_stream_kernel<<<grid, dim3(kStreamThreads), (size_t)kStreamSplit * p.rows * 8 * 16, stream>>>(a, n_tiles, p.rows);
       break;
     case kSmallTiles:
       expert_tile_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), TileKernel<2, 2, 1, 1, 4, true, false>::kLdsBytes,
