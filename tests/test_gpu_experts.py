@@ -382,3 +382,53 @@ def test_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, held)), i
+
+
+def test_matmul_large_form():
+    """The 8-bit matrix instruction behind large 16-bit products.  Within each
+    8 consecutive k its products are aligned to the largest one and what lies
+    below 2^-13 of that is lost, at most 7 times; sums of the groups of 8 are
+    32-bit: the bound below, computed for a sample of rows and columns."""
+    counts, head, tail, N, C = [701, 0, 590], 3, 5, 1101, 6416
+    R = head + sum(counts) + tail
+    note("large form", counts, N, C)
+    off = torch.tensor(head + np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    x, w = rand((R, C), "bf16", 1), rand((3, N, C), "bf16", 2)
+    q, s = eplb.quantize_rows(x.to(DEV))
+    wq, ws = eplb.quantize_weights(w.to(DEV))
+    g = torch.Generator().manual_seed(5)
+    rows = torch.randperm(R, generator=g).to(torch.int32)
+    rows[50], rows[900] = -1, R
+    for t in (torch.bfloat16, torch.float16):
+        y = eplb.expert_matmul(q, s, wq, ws, off.to(DEV), rows=rows.to(DEV), dtype=t).double().cpu()
+        assert (y[:head] == 0).all() and (y[R - tail:] == 0).all() and (y[50] == 0).all() and (y[900] == 0).all()
+        for i, pick in ((0, [3, 4, 130, 258, 259, 300, 703]), (2, [704, 705, 831, 960, 1200, 1293])):
+            cols = torch.tensor([0, 1, 31, 32, 127, 128, 255, 256, 511, 700, 1023, 1024, 1099, 1100])
+            src = rows[torch.tensor(pick)].long()
+            xd = dequantized(q[src.to(DEV)], s[src.to(DEV)], 1, B)
+            wd = dequantized(wq[i], ws[i], B, B)[cols]
+            p = xd[:, None, :] * wd[None, :, :]
+            ref = p.sum(2)
+            lost = 7 * 2.0 ** -13 * p.abs().view(*ref.shape, C // 8, 8).amax(3).sum(2)
+            room = lost + (C + 16) * 2.0 ** -24 * p.abs().sum(2) + HALF_ULP[t] * (ref.abs() + lost)
+            got = y[torch.tensor(pick)][:, cols]
+            past = ref.abs() > torch.finfo(t).max * 0.99
+            assert ((got - ref).abs()[~past] <= room[~past]).all()
+
+
+def test_wgrad_large_form():
+    counts, N, C = [3000, 1, 4000], 1301, 1104
+    R = sum(counts)
+    note("large weight gradient", counts, N, C)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    x, dy = rand((R, C), "bf16", 1), rand((R, N), "bf16", 2)
+    xq, xs = eplb.quantize_columns(x.to(DEV), off.to(DEV))
+    dq, ds = eplb.quantize_columns(dy.to(DEV), off.to(DEV))
+    got = eplb.expert_wgrad(dq, ds, xq, xs, off.to(DEV))
+    xd, dd = dequantized(xq.t(), xs, B, 1).to(DEV), dequantized(dq.t(), ds, B, 1).to(DEV)
+    pad = 0
+    for i, n in enumerate(counts):
+        m = up(n) * B
+        a, b = dd[pad:pad + m], xd[pad:pad + m]
+        check(got[i], (a.t() @ b).cpu(), (a.abs().t() @ b.abs()).cpu(), m, i)
+        pad += m

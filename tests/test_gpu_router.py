@@ -345,3 +345,62 @@ def test_group_rows_workspace_and_shapes():
     assert all(torch.equal(x, y) for x, y in zip(a, b))
     with pytest.raises(eplb.EplbError):
         eplb.group_rows(ids, 40, workspace=torch.empty((need - 4,), dtype=torch.uint8, device=DEV))
+
+
+# ------------------------------------------------------------------ many rows: four to a wave
+@pytest.mark.parametrize("E,K,G,top,gtop,dtype", [
+    (16, 4, 1, 1, 1, "f32"), (60, 6, 1, 1, 1, "bf16"), (64, 16, 8, 4, 2, "f16"), (120, 8, 4, 2, 2, "bf16"),
+    (256, 8, 8, 4, 2, "f32"), (250, 7, 10, 3, 1, "bf16"), (512, 16, 16, 5, 2, "bf16"), (300, 9, 1, 1, 1, "f32"),
+    (256, 17, 8, 4, 2, "f32")])
+def test_choice_many_rows(E, K, G, top, gtop, dtype):
+    T = 2048 + 37
+    x, x64, rng = make(T, E, dtype, E * K, ties=True)
+    x64[rng.random((T, E)) < 0.05] = -np.inf
+    x64[5] = -np.inf
+    x64[7] = 1.0                                        # all keys equal but for the bias
+    x64[9, : E // 2] = np.nan
+    bias = rng.integers(-4, 5, size=E).astype(np.float32) * 0.25
+    if E == 300:
+        bias[:] = 0
+    mask = rng.random(T) > 0.1
+    x = torch.from_numpy(x64).to(TYPES[dtype])
+    note("many", E, K, G, top, gtop, dtype)
+    ids, w = eplb.gate(x.to(DEV), K, scoring="softmax", bias=torch.from_numpy(bias).to(DEV), G=G, top_groups=top,
+                       group_top=gtop, mask=torch.from_numpy(mask).to(DEV))
+    want = choose((x.float().numpy() + bias).astype(np.float32), K, G, top, gtop)
+    want[~mask] = -1
+    assert np.array_equal(ids.cpu().numpy(), want)
+    fine = ~np.isnan(x64).any(1)
+    ref = weights_of(scores(x.double().numpy(), "softmax"), want, True, 1.0)
+    np.testing.assert_allclose(w.cpu().numpy()[fine], ref[fine], rtol=2e-5, atol=1e-30)
+
+
+def test_equal_logits():
+    """A router that has learned nothing: the lowest experts, by rows of 64 lanes and of 16."""
+    for T in (3, 2100):
+        ids, w = eplb.gate(torch.zeros((T, 256), device=DEV), 8, G=8, top_groups=4, group_top=2)
+        assert (ids.cpu().numpy() == np.arange(8)).all() and (w == 0.125).all()
+
+
+@pytest.mark.parametrize("scoring,dtype", [("sigmoid", "f32"), ("softmax", "bf16")])
+def test_loss_and_gradient_many_rows(scoring, dtype):
+    T, E, K = 2500, 72, 5
+    x, x64, rng = make(T, E, dtype, 3)
+    seg = [0, 700, 700, 2100, 2490]
+    mask = rng.random(T) > 0.1
+    ids_d, w, loss, counts, prob, tokens = eplb.gate_loss(
+        x.to(DEV), K, torch.tensor(seg, dtype=torch.int32, device=DEV), 0.2, scoring=scoring,
+        mask=torch.from_numpy(mask).to(DEV))
+    ids = ids_d.cpu().numpy()
+    rl, rc, rp, rt = loss_of(scores(x64, scoring), scoring, ids, seg, mask, 0.2, E)
+    assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
+    np.testing.assert_allclose(prob.cpu().numpy(), rp, rtol=2e-5, atol=1e-30)
+    np.testing.assert_allclose(loss.cpu().numpy(), rl, rtol=4e-5)
+    ids[11] = ids[11, 0]                                # one expert named K times
+    gw, gl = rng.normal(size=(T, K)).astype(np.float32), rng.normal(size=4).astype(np.float32)
+    got = eplb.gate_backward(x.to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(gw).to(DEV), scoring=scoring,
+                             mask=torch.from_numpy(mask).to(DEV), seg=torch.tensor(seg, dtype=torch.int32, device=DEV),
+                             alpha=0.2, counts=counts, tokens=tokens, d_loss=torch.from_numpy(gl).to(DEV))
+    ref, big = gradient(x64, scoring, ids, mask, True, 1.0, gw, seg, 0.2, gl, rc, rt)
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert (err <= 4e-5 * big + HALF_ULP[dtype] * np.abs(ref) + 2.0 ** -25).all(), err.max()
