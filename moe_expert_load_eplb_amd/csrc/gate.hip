@@ -520,7 +520,12 @@ __global__ __launch_bounds__(kLossThreads) void gate_loss_kernel(GateArgs a, int
     for (int64_t t0 = r; t0 < end; t0 += kRows) {
       const int64_t t = t0 + sub;
       const bool real = t < end && (a.mask == nullptr || a.mask[t] != 0);
-      gate_row<LPR, VPL, true>(a, t < end ? t : a.T, real, lane, row, cnt, psum);
+      // the lane's number is not the same to the compiler in every turn: what
+      // it would keep for all of them (addresses, comparisons, the bias) takes
+      // more registers than there are
+      int turn_lane = lane;
+      asm volatile("" : "+v"(turn_lane));
+      gate_row<LPR, VPL, true>(a, t < end ? t : a.T, real, turn_lane, row, cnt, psum);
       mine += real;
     }
     if (lane == 0 && mine > 0) atomicAdd(&kept, mine);
@@ -633,16 +638,18 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
   extern __shared__ float grads[];           // [rows at once][E rounded up to 4], zero but for the row in work
   constexpr int kRows = kGateThreads / LPR;
   constexpr int kC = 1;                      // K <= LPR
-  const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+  const int first_lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   float* grad = grads + sub * ((a.E + 3) / 4 * 4 + 4);
 #pragma unroll
   for (int j = 0; j < VPL; ++j)
-    if (expert_of<LPR>(j, lane) < a.E) grad[expert_of<LPR>(j, lane)] = 0.0f;
+    if (expert_of<LPR>(j, first_lane) < a.E) grad[expert_of<LPR>(j, first_lane)] = 0.0f;
   int64_t seg_end = -1;                      // where the coefficients in registers stop to hold
   float coef[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) coef[j] = 0.0f;
   for (int i = 0; i < per_group; ++i) {
+    int lane = first_lane;                   // as in the loss: nothing is kept from turn to turn
+    asm volatile("" : "+v"(lane));
     const int64_t t = ((int64_t)blockIdx.x * per_group + i) * kRows + sub;
     const bool inside = t < a.T;
     const bool real = inside && (a.mask == nullptr || a.mask[t] != 0);
