@@ -37,7 +37,8 @@ extern "C" {
  * largest keys are chosen, in descending order; equal keys (and equal group
  * scores) go to the lowest index.  An expert whose logit or key is minus
  * infinity or NaN is never chosen: where fewer than K experts are left, the
- * remaining ids are -1 and their weights 0.  The weights are the scores, without the bias:
+ * remaining ids are -1 and their weights 0.  The weights are the scores,
+ * without the bias:
  *   w[t][k] = scale * s[t][ids[t][k]] / (sum over the chosen of s + 1e-20)
  * or, with normalize = 0, scale * s.  A row whose mask byte is 0 (padding)
  * gets ids -1 and weights 0.
@@ -86,9 +87,8 @@ int32_t eplb_gate(const void* logits, int32_t dtype, int64_t ld, int64_t T, int3
  *   prob       [S][E] float32    out
  *   tokens     [S] int32         out: n of each segment
  * Other arguments and errors: as for eplb_gate; S is 1 .. 2^20 and S * ceil(E
- * / 64) at most 2^21 (EPLB_E_LIMIT); EPLB_E_ARG
- * also for a workspace that is too small, misaligned, or shares a byte with
- * another array.
+ * / 64) at most 2^21 (EPLB_E_LIMIT); EPLB_E_ARG also for a workspace that is
+ * too small, misaligned, or shares a byte with another array.
  */
 int32_t eplb_gate_loss(const void* logits, int32_t dtype, int64_t ld, int64_t T, int32_t E, int32_t K,
                        int32_t scoring, const float* bias, int32_t G, int32_t top_groups, int32_t group_top,
@@ -189,7 +189,7 @@ int32_t eplb_quantize_rows(const void* x, int32_t dtype, int64_t ld, int64_t R, 
  *                                R, a group that ends before it starts is empty
  *   Rp                           columns of q: a multiple of 128, at least
  *                                R + 127 G rounded down to one
- *   q          [C][Rp] 8-bit     out: columns below pad[G]
+ *   q          [C][Rp] 8-bit     out: columns below pad[G]; 16-byte aligned
  *   scale      [Rp / 128][C] float32  out: blocks below pad[G] / 128
  */
 int32_t eplb_quantize_columns(const void* x, int32_t dtype, int64_t ld, int64_t X, int64_t C, const int32_t* rows,
@@ -215,10 +215,12 @@ int32_t eplb_quantize_weights(const void* w, int32_t dtype, int32_t G, int64_t N
  *   y[r][n] = sum over blocks b of scale[x(r)][b] * w_scale[g][n / 128][b]
  *             * (sum over k in b of q[x(r)][k] * w[g][n][k])
  * where g is the group of row r and x(r) = rows[r] / topk, or r without rows.
- * The sum over blocks is held in 32 bits.  With a 32-bit output the sums
- * within a block keep 32 bits too; with a 16-bit one they come from the 8-bit
- * matrix instruction, whose sums keep fewer (about 5e-5 relative at worst,
- * far below the output's rounding).  Rows of no group, and rows whose x(r) is
+ * The sum over blocks is held in 32 bits, and so are the sums within a block,
+ * but for large products with a 16-bit output that the matrix cores' rate
+ * bounds: there they come from the 8-bit matrix instruction, which drops of
+ * each 8 consecutive products what lies below 2^-13 of the largest of them
+ * (about 5e-5 of a typical sum at worst, far below the output's rounding).
+ * Equal inputs give equal bits.  Rows of no group, and rows whose x(r) is
  * outside [0, X), get zeros.
  *
  *   q          [X][K] 8-bit      and scale [X][ceil(K / 128)] float32, as
@@ -250,7 +252,7 @@ int32_t eplb_expert_matmul(const uint8_t* q, const float* scale, int64_t X, cons
  *                                x_scale [Rp / 128][K]: eplb_quantize_columns'
  *                                outputs for the same offsets and Rp
  *   dw         [G][N][K] dtype   out: zeros for a group without rows
- * dy, x and dw are 16-byte aligned.  The sums are as for eplb_expert_matmul.
+ * dy, x and dw are 16-byte aligned.  All sums are held in 32 bits.
  * Errors: as for eplb_expert_matmul.
  */
 int32_t eplb_expert_wgrad(const uint8_t* dy, const float* dy_scale, const uint8_t* x, const float* x_scale,

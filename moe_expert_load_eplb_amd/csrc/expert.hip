@@ -4,85 +4,45 @@
 // Both products have the same shape: out[o][i] = sum over blocks b of 128 of
 // so[o][b] * si[i][b] * (sum over j in b of O[o][j] * I[i][j]), with the
 // inner index i contiguous in the output (matmul: o = row, i = n, j = k;
-// weight gradient: o = n, i = k, j = row).  One matrix instruction takes a
-// 16 x 16 tile through a whole block (128 products per element), so its
-// result is what the block's scales multiply; the sum over blocks is kept in
-// 32-bit registers.  The inner operand is the instruction's first, which
-// leaves four consecutive i of one o in each lane.
+// weight gradient: o = n, i = k, j = row).  The sum within a block is what its
+// scales multiply; the sum over blocks is kept in 32-bit registers.  The inner
+// operand is the matrix instruction's first, which leaves consecutive i of one
+// o in each lane.
+//
+// Sums within a block.  The 8-bit matrix instruction aligns each 8 consecutive
+// products to the largest of them and drops what lies below 2^-13 of it
+// (measured: 5e-5 of a typical sum of values spread over the format's whole
+// range, 1.6e-5 of normally distributed ones; between the eights its sums keep
+// 32 bits).  The 16-bit matrix instruction keeps 32 bits (measured: 7e-8); the
+// 8-bit values become 16-bit ones exactly on the way from LDS, two per vector
+// instruction.  It has half the rate, so the 8-bit instruction is taken only
+// where its rate is what counts and the output is rounded to 16 bits anyway
+// (the 2^-13 is 32 times below a bfloat16's rounding).
 #include "experts_device.h"
 
 namespace eplb {
 
 namespace {
 
-
-// Whether the matrix cores' rate bounds a product, rather than its bytes or
-// the launch: then 16-bit outputs come from the 8-bit matrix instruction.
-// out rows x in columns over a contraction of `inner`, and the bytes of its
-// operands and output.
-bool matrix_bound(double out, double in, double inner, double bytes) {
-  const double ops = 2.0 * out * in * inner;
-  return ops >= 0x1p34 && ops >= 256.0 * bytes;
-}
-
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// 16 x 16 sums over a block of 128.  The 8-bit matrix instruction adds its
-// products with less than 32 bits (measured: 5e-5 of a typical sum of values
-// spread over the format's whole range, 1.6e-5 of normally distributed ones),
-// far below the rounding of a 16-bit output.  For 32-bit outputs the values
-// become 16-bit ones, exactly, and go through the 16-bit matrix instruction,
-// whose sums keep 32 bits (measured: 7e-8), at half the rate or less.
-template <bool WIDE>
-struct Fragment;
-
-template <>
-struct Fragment<false> {
-  i32x8 v;
-  __device__ __forceinline__ void set(i32x4 lo, i32x4 hi) {
-    v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-};
-
-template <>
-struct Fragment<true> {
-  f16x8 v[4];
-  __device__ __forceinline__ void set(i32x4 lo, i32x4 hi) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int a = s < 2 ? lo[2 * s] : hi[2 * s - 4], b = s < 2 ? lo[2 * s + 1] : hi[2 * s - 3];
-      const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
-      const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
-      const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
-      const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
-      v[s] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-    }
-  }
-};
-
-__device__ __forceinline__ f32x4 mfma_block(const Fragment<false>& a, const Fragment<false>& b) {
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, zero, 0, 0, 0, 0, 0, 0);
+// Half h of 16 8-bit values as 16-bit ones.
+__device__ __forceinline__ f16x8 half_of(i32x4 v, int h) {
+  const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h], 1.0f, false);
+  const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h], 1.0f, true);
+  const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + 1], 1.0f, false);
+  const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + 1], 1.0f, true);
+  return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-__device__ __forceinline__ f32x4 mfma_block(const Fragment<true>& a, const Fragment<true>& b) {
+// 16 x 16 sums over 128: a lane's 32 values of each operand, in two parts.
+__device__ __forceinline__ f32x4 mfma_block(const i32x4 (&a)[2], const i32x4 (&b)[2]) {
   f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int s = 0; s < 4; ++s) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[s], b.v[s], d, 0, 0, 0);
+  for (int s = 0; s < 4; ++s)
+    d = __builtin_amdgcn_mfma_f32_16x16x32_f16(half_of(a[s >> 1], s & 1), half_of(b[s >> 1], s & 1), d, 0, 0, 0);
   return d;
-}
-
-// 16 bytes `c` of row `r` of a staged tile: rows of 128 bytes, their 16-byte
-// parts permuted by the row so that 8 rows at one c cover all banks.
-__device__ __forceinline__ int lds_at(int r, int c) { return r * kBlock + ((c ^ (r & 7)) << 4); }
-
-template <bool WIDE>
-__device__ __forceinline__ Fragment<WIDE> fragment(const uint8_t* tile, int row, int quad) {
-  Fragment<WIDE> f;
-  f.set(*reinterpret_cast<const i32x4*>(tile + lds_at(row, quad)),
-        *reinterpret_cast<const i32x4*>(tile + lds_at(row, quad + 4)));
-  return f;
 }
 
 // Four consecutive values of one output row; `left` of them are inside.
@@ -109,11 +69,11 @@ __device__ __forceinline__ void store4(void* p, int32_t dtype, int64_t at, int l
 }
 
 // ---------------------------------------------------------------- few rows
-// Streaming forms, for groups of few rows: the weights are read once, from
+// The streaming form, for groups of few rows: the weights are read once, from
 // memory to registers, and bound the time.  A wave takes 16 n of one group
-// through K; the fragments of several blocks of 128 are in flight at once
-// (2 KiB each).  With the memory as the bound, 16-bit products cost nothing
-// and keep 32-bit sums.  No load stands behind a branch (rows and blocks past
+// through K; both operands of eight blocks of 128 are in flight at once (2 KiB
+// each).  With the memory as the bound, 16-bit products cost nothing and keep
+// 32-bit sums.  No load stands behind a branch (rows and blocks past
 // the end are clamped to the last ones and not used): a load that may or may
 // not have been issued makes every wait behind it wait for all of them.
 constexpr int kStreamThreads = 256;
@@ -155,8 +115,7 @@ struct ScaleRow {
   }
 };
 
-// 16 rows: both operands go straight to registers.
-constexpr int kAhead16 = 8;
+constexpr int kAhead16 = 8;                // blocks in flight
 
 __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulArgs a, int32_t n_tiles) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quad = lane >> 4, col = lane & 15;
@@ -189,9 +148,8 @@ __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulA
         const int i = kb0 + p;               // past the end: not added
         const i32x4 zero = {0, 0, 0, 0};
         const int k = i * kBlock + quad * 16;
-        Fragment<true> fw, fx;
-        fw.set(rw[p][0], rw[p][1]);
-        fx.set(k < a.K ? rx[p][0] : zero, k + 64 < a.K ? rx[p][1] : zero);
+        const i32x4 fw[2] = {rw[p][0], rw[p][1]};
+        const i32x4 fx[2] = {k < a.K ? rx[p][0] : zero, k + 64 < a.K ? rx[p][1] : zero};
         const float sc = ws.get(p) * sx[p];
         const int next = min(i + kAhead16, a.KB - 1);
         load_parts(w, next, quad, a.K, rw[p][0], rw[p][1]);
@@ -267,9 +225,11 @@ struct TileJob {
   const uint8_t* inner;      // first inner row of the tile
   int64_t inner_ld;
   int inner_rows;            // rows inside (the others read the last one and are not stored)
-  const float* inner_scale;  // scale i, block b at inner_scale[i * inner_scale_ld + b * inner_step]: matmul: a scale
-  int64_t inner_scale_ld, inner_step;        // for each 128 inner rows from the tile's first on; weight gradient: for each
-  int inner_scales, inner_first;             // inner_first: the tile's first inner row within its 128
+  // scale i of block b: inner_scale[i * inner_scale_ld + b * inner_step], i < inner_scales.  Matmul: one for each 128
+  // inner rows, the tile's first row being row inner_first of its 128; weight gradient: one for each row
+  const float* inner_scale;
+  int64_t inner_scale_ld, inner_step;
+  int inner_scales, inner_first;
   int64_t outer_step;        // from one block's scale of an outer row to the next one's
   int64_t K;                 // elements of a row (matmul: past it zeros)
   int block0, blocks;        // first block, number of blocks
@@ -379,7 +339,7 @@ struct TileKernel {
       auto part = [&](const uint8_t* tile, int row, int g) {
         return *reinterpret_cast<const i32x4*>(tile + row * kBlock + ((g ^ key(row)) << 4));
       };
-      // part 2 s' + half * 2 ... : a lane's 64 of the block's 128 elements, the same of both operands
+      // a lane's 64 of the block's 128 elements, the same of both operands
       i32x4 fi[IT][4];
 #pragma unroll
       for (int t = 0; t < IT; ++t) {
@@ -452,15 +412,6 @@ struct TileKernel {
     wait_loads<0>();                         // none may land in LDS that is no longer this workgroup's
   }
 
-  // Half h of 16 8-bit values as 16-bit ones.
-  static __device__ __forceinline__ f16x8 half_of(i32x4 v, int h) {
-    const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h], 1.0f, false);
-    const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h], 1.0f, true);
-    const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + 1], 1.0f, false);
-    const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + 1], 1.0f, true);
-    return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-  }
-
   // Stores the wave's values: row(r) is outer row r's first element in the
   // output or -1, some(r) whether it has values (else zeros), `left` the inner
   // values from the tile's start on.
@@ -493,7 +444,9 @@ struct TileKernel {
 template <int WI, int WO, int IT, int OT, int STAGES, bool WIDE>
 __global__ __launch_bounds__(WI* WO * 64) void expert_tile_kernel(MatmulArgs a, int32_t n_tiles) {
   typedef TileKernel<WI, WO, IT, OT, STAGES, WIDE, false> K;
-  constexpr bool kOrdered = IT * OT > 1;     // few blocks of small tiles: counting them all would cost more than it gives
+  // Large tiles: the workgroups of one die take neighbouring tiles, which share operands in its cache.  Small tiles
+  // run where the weights are read once or few, and are found without counting them all first.
+  constexpr bool kOrdered = IT * OT > 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t tile_lds[];
   __shared__ int32_t src[K::kOuter];
   int32_t row = blockIdx.x / n_tiles, column = blockIdx.x % n_tiles;
@@ -567,21 +520,51 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
            [&](int) { return some; });
 }
 
-// The form of a product: rows to a tile and n to a workgroup.
-enum MatmulForm { kStream16, kSmallTiles, kLargeTiles };
+// The form of a product, with its rows to a tile and n to a workgroup.
+//
+// kStream16: one row to a group at most, and too few tiles for their loads in
+// flight to cover the memory's latency (a streaming workgroup has 64 KiB in
+// flight, a small tile's 24).  Weights of 8-bit values not in any cache, 8 rows
+// of 64 groups, N = 2048, K = 4096 (256 tiles): 19.9 us, 23.2 with small tiles;
+// 1 row, N = 4096, K = 2048: 10.1 and 12.5.  Twice the tiles: 20.4 and 19.4.
+// Two rows to a group (32 rows, 16 groups, 2048 x 2048): 23.4 and 20.6.  K =
+// 512: 7.8 and 5.9.
+//
+// kSmallTiles (64 x 64, four workgroups to a compute unit) against kWideTiles
+// (128 x 256, half the bytes through LDS per product): the wide ones win where
+// there are more of them than half the compute units and the groups fill them.
+// G = 1, K = 4096, N = 4096, 2048 rows (256 wide tiles): 76.5 us against 119.3;
+// 1024 rows (128): 122 at K = 8192 against 114; 8 groups of 1024 rows, 2048 x
+// 2048: 105 against 128; 32 groups of 128, 2048 x 2048: 78 against 88; 32
+// groups of 64: 215 against 210 (4096 x 4096).  At K = 128 they are equal, at K
+// = 256 wide tiles take 309 us of 361 (16384 x 8192, 32-bit output).
+//
+// kLargeTiles (256 x 256, the 8-bit matrix instruction) for 16-bit outputs
+// bound by the matrix cores, with tiles for a good part of the compute units:
+// 16384 x 4096 x 4096 in 8 groups 364 us (1.5 PFLOP/s) against 586 with wide
+// tiles; 8 groups of 512 rows, 2048 x 2048: 44 against 71; at 217 operations to
+// a byte (32 groups of 128 rows, 2048 x 2048) 78 and 78; 64 tiles (2048 x 2048
+// x 8192) 122 and 120.
+enum MatmulForm { kStream16, kSmallTiles, kWideTiles, kLargeTiles };
 
 struct MatmulPlan {
   MatmulForm form;
   int rows, n;
-  bool wide;                 // 16-bit products
 };
 
+// Tiles of R rows and N columns, every second group with one that is not full.
+int64_t about_tiles(int64_t R, int64_t N, int32_t G, int rows, int n) {
+  return (R / rows + G / 2) * ceil_div(N, n);
+}
+
 MatmulPlan plan_matmul(int64_t R, int64_t N, int64_t K, int32_t G, int32_t dtype) {
-  const int64_t average = ceil_div(R, G);
-  if (average <= 8) return {kStream16, 16, kStream16N, true};
-  const bool wide = dtype == kF32 || !matrix_bound(R, N, K, (double)R * K + (double)G * N * K + 2.0 * R * N);
-  if (wide) return {kSmallTiles, 64, 64, true};
-  return {kLargeTiles, 256, 256, false};
+  if (R <= G && K >= 1024 && R * ceil_div(N, 64) <= 256) return {kStream16, 16, kStream16N};
+  if (dtype != kF32 && about_tiles(R, N, G, 256, 256) >= 96) {
+    const double ops = 2.0 * R * N * K, bytes = (double)R * K + (double)G * N * K + 2.0 * R * N;
+    if (ops >= 0x1p34 && ops >= 256.0 * bytes) return {kLargeTiles, 256, 256};
+  }
+  if (R >= 128 * (int64_t)G && K >= 256 && about_tiles(R, N, G, 128, 256) > 128) return {kWideTiles, 128, 256};
+  return {kSmallTiles, 64, 64};
 }
 
 }  // namespace
@@ -607,6 +590,10 @@ hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
       expert_tile_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), TileKernel<2, 2, 1, 1, 4, true, false>::kLdsBytes,
                                               stream>>>(a, n_tiles);
       break;
+    case kWideTiles:
+      expert_tile_kernel<4, 2, 2, 2, 3, true><<<grid, dim3(512), TileKernel<4, 2, 2, 2, 3, true, false>::kLdsBytes,
+                                              stream>>>(a, n_tiles);
+      break;
     case kLargeTiles:
       expert_tile_kernel<4, 2, 2, 4, 2, false><<<grid, dim3(512), TileKernel<4, 2, 2, 4, 2, false, false>::kLdsBytes,
                                                stream>>>(a, n_tiles);
@@ -616,7 +603,12 @@ hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_expert_wgrad(const WgradArgs& a, hipStream_t stream) {
-  const bool large = (double)a.N * a.K * a.R >= 0x1p33;
+  // Large tiles take half the bytes through LDS per product, but there have to
+  // be enough of them: G = 8, 1024 x 1024 (256 large tiles), 4096 rows: 18.0 us
+  // against 26.0 (16-bit output); 8 groups of 8 rows, 32-bit output: 18.2
+  // against 23.0; 700 x 600, G = 9 (162): 13.2 and 13.1; 2048 x 2048, G = 1
+  // (128): 39.3 and 38.8; 1024 x 1024, G = 1 (32), 8192 rows: 112 and 45.
+  const bool large = a.G * ceil_div(a.N, 128) * ceil_div(a.K, 256) >= 160;
   const int ti = large ? 256 : 64, to = large ? 128 : 64;
   const int32_t ni = (int32_t)ceil_div(a.K, ti), no = (int32_t)ceil_div(a.N, to);
   const dim3 grid((unsigned)((int64_t)a.G * ni * no));

@@ -24,7 +24,6 @@ constexpr int kGateThreads = 256;
 constexpr int kLossThreads = 512;
 constexpr int kLossBlocks = 512;             // workgroups of the loss, at most
 constexpr int kV = 4;                        // consecutive experts of a lane
-constexpr int64_t kManyRows = 2048;          // rows from which 16 lanes take one
 constexpr int kParts = 16;                   // parts of a row whose maxima bound the choice
 
 // LDS between lanes of one wave: its own operations stay in order, the
@@ -456,7 +455,7 @@ if (a.vec) {
 
 template <int LPR, int VPL>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a, int32_t row_words) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];             // [rows at once][row_words]
+  extern __shared__ __attribute__((aligned(16))) float lds[];     // [rows at once][row_words]
   constexpr int kRows = kGateThreads / LPR;
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const int64_t t = (int64_t)blockIdx.x * kRows + sub;
@@ -485,18 +484,30 @@ __device__ __forceinline__ int64_t piece_end(const int32_t* seg, int64_t S, int6
 // Floats of one partial sum: E sums of shares, E counts, the rows counted.
 __host__ __device__ inline int64_t part_stride(int32_t E) { return (2 * (int64_t)E + 1 + 3) / 4 * 4; }
 
+// Whether 16 lanes take a row (else 64): four rows then share every butterfly
+// and every step of the selection, but a lane holds four times the experts, so
+// the rows have to fill the chip with a quarter of the waves.  Kernel times of
+// the choice, 16 lanes and 64, 8 of E (6 of 64): E = 64, 2048 rows: 3.4 and 3.8
+// us; E = 128, 2048: 4.2 and 3.9, 4096: 4.3 and 4.7; E = 256, 4096: 5.7 and
+// 4.7, 8192: 6.5 and 6.9, 16384: 9.1 and 11.1.  With the loss the same turn
+// (E = 256, 4096 rows: 14.6 and 17.0, 2048: 14.4 and 12.4).  Past 256 experts
+// 16 lanes gain nothing (E = 512, K = 16, 16384 rows: 40.9 and 38.2).
+__host__ __device__ inline bool narrow_rows(int64_t T, int32_t E) { return E <= 256 && T >= 32 * (int64_t)E; }
+
 // Rows of one workgroup of the loss: one row to a lane group where there are
 // few, else as many as make kLossBlocks workgroups (and partial sums).
-int32_t loss_chunk(int64_t T) {
-  const int64_t least = kLossThreads / (T >= kManyRows ? 16 : 64);
+int32_t loss_chunk(int64_t T, int32_t E) {
+  const int64_t least = kLossThreads / (narrow_rows(T, E) ? 16 : 64);
   return (int32_t)std::max<int64_t>(least, ceil_div(ceil_div(T, kLossBlocks), least) * least);
 }
 
-// Workgroup c takes rows c * chunk on, piece by piece where a segment ends.  The piece of segment s goes to partial sum c + s: two pieces never
-// share one, as each next piece has a larger c or a larger s.
+// Workgroup c takes rows c * chunk on, piece by piece where a segment ends.
+// The piece of segment s goes to partial sum c + s: two pieces never share one,
+// as each next piece has a larger c or a larger s.
 template <int LPR, int VPL>
 __global__ __launch_bounds__(kLossThreads) void gate_loss_kernel(GateArgs a, int32_t row_words, int32_t chunk) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];             // [rows at once][row_words]: the choice's, then shares; [E] counts
+  // [rows at once][row_words]: the choice's, then shares; [E] counts
+  extern __shared__ __attribute__((aligned(16))) float lds[];
   constexpr int kRows = kLossThreads / LPR;
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   float* row = lds + sub * row_words;
@@ -635,7 +646,8 @@ __global__ __launch_bounds__(kReduceThreads) void gate_loss_reduce_kernel(GateAr
 // logits, written and read).
 template <int LPR, int VPL>
 __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwardArgs a, int32_t per_group) {
-  extern __shared__ float grads[];           // [rows at once][E rounded up to 4], zero but for the row in work
+  // [rows at once][E rounded up to 4], zero but for the row in work
+  extern __shared__ __attribute__((aligned(16))) float grads[];
   constexpr int kRows = kGateThreads / LPR;
   constexpr int kC = 1;                      // K <= LPR
   const int first_lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
@@ -780,17 +792,15 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
 }
 
 // Calls f with the lanes per row and the values per lane that cover E experts:
-// 16 lanes for E <= 512 and K <= 16 where there are rows enough to fill the
-// chip with four to a wave, else 64.
+// 16 lanes for many rows (narrow_rows) and K <= 16, else 64.
 template <typename F>
 hipError_t by_width(int64_t T, int32_t E, int32_t K, F f) {
   typedef std::integral_constant<int, 16> L16;
   typedef std::integral_constant<int, 64> L64;
-  if (E <= 512 && K <= 16 && T >= kManyRows) {
+  if (narrow_rows(T, E) && K <= 16) {
     if (E <= 64) return f(L16(), std::integral_constant<int, 4>());
     if (E <= 128) return f(L16(), std::integral_constant<int, 8>());
-    if (E <= 256) return f(L16(), std::integral_constant<int, 16>());
-    return f(L16(), std::integral_constant<int, 32>());
+    return f(L16(), std::integral_constant<int, 16>());
   }
   if (E <= 256) return f(L64(), std::integral_constant<int, 4>());
   if (E <= 512) return f(L64(), std::integral_constant<int, 8>());
@@ -815,7 +825,7 @@ bool aligned4(const void* p, int32_t dtype, int64_t ld, int32_t E) {
 }  // namespace
 
 int64_t gate_loss_part_bytes(int64_t T, int32_t E, int64_t S) {
-  return ((ceil_div(T, loss_chunk(T)) + S) * part_stride(E) + S * (loss_parts(E) + 1)) * 4;
+  return ((ceil_div(T, loss_chunk(T, E)) + S) * part_stride(E) + S * (loss_parts(E) + 1)) * 4;
 }
 
 hipError_t launch_gate(const GateArgs& args, hipStream_t stream) {
@@ -835,19 +845,19 @@ hipError_t launch_gate_loss(const GateArgs& args, hipStream_t stream) {
   GateArgs a = args;
   a.vec = aligned4(a.logits, a.dtype, a.ld, a.E) && aligned4(a.bias, kF32, a.E, a.E);
   const int64_t parts = loss_parts(a.E);
-  a.terms = a.part + (ceil_div(a.T, loss_chunk(a.T)) + a.S) * part_stride(a.E);
+  a.terms = a.part + (ceil_div(a.T, loss_chunk(a.T, a.E)) + a.S) * part_stride(a.E);
   a.ticket = reinterpret_cast<int32_t*>(a.terms + a.S * parts);
   const hipError_t err = by_width(a.T, a.E, a.K, [&](auto lpr, auto vpl) {
     constexpr int LPR = decltype(lpr)::value, VPL = decltype(vpl)::value, kRows = kLossThreads / LPR;
     const int32_t words = choice_words(LPR, a.E, true);      // the shares' sums pass through the same place
-    const unsigned grid = (unsigned)std::max<int64_t>(1, ceil_div(a.T, loss_chunk(a.T)));
+    const unsigned grid = (unsigned)std::max<int64_t>(1, ceil_div(a.T, loss_chunk(a.T, a.E)));
     gate_loss_kernel<LPR, VPL><<<dim3(grid), dim3(kLossThreads), ((size_t)kRows * words + a.E) * 4, stream>>>(
-        a, words, loss_chunk(a.T));
+        a, words, loss_chunk(a.T, a.E));
     return hipGetLastError();
   });
   if (err != hipSuccess) return err;
   gate_loss_reduce_kernel<<<dim3((unsigned)(a.S * parts)), dim3(kReduceThreads), 0, stream>>>(a, (int32_t)parts,
-                                                                                              loss_chunk(a.T));
+                                                                                              loss_chunk(a.T, a.E));
   return hipGetLastError();
 }
 

@@ -432,3 +432,59 @@ def test_wgrad_large_form():
         a, b = dd[pad:pad + m], xd[pad:pad + m]
         check(got[i], (a.t() @ b).cpu(), (a.abs().t() @ b.abs()).cpu(), m, i)
         pad += m
+
+
+@pytest.mark.parametrize("counts", [[1] * 7, [0, 0, 5, 0, 2, 0, 0], [0] * 20 + [19, 0, 1], [0, 1, 0]])
+@pytest.mark.parametrize("N,C", [(70, 1024), (200, 2064)])
+def test_matmul_few_rows_of_many_groups(counts, N, C):
+    """As one token's choices make them, also where they fall on one group."""
+    product_case(counts, 0, 0, sum(counts), 1, N, C, "f32", N, rows=False)
+    product_case(counts, 0, 0, sum(counts), 1, N, C, "bf16", N + 1, rows=False)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_wide_tiles(out):
+    """Many rows and 32-bit sums: the tolerance of 32-bit sums, over tiles that
+    groups, N and K leave unfilled."""
+    product_case([701, 0, 2500], 3, 5, 3300, 1, 1101, 416, out, 7)
+
+
+def test_matmul_large_tiles():
+    """test_matmul_large_form's bound at a size of more tiles."""
+    counts, N, C = [1201, 0, 1399], 2310, 1440
+    R = sum(counts)
+    note("large tiles", counts, N, C)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    x, w = rand((R, C), "bf16", 1), rand((3, N, C), "bf16", 2)
+    q, s = eplb.quantize_rows(x.to(DEV))
+    wq, ws = eplb.quantize_weights(w.to(DEV))
+    t = torch.bfloat16
+    y = eplb.expert_matmul(q, s, wq, ws, off.to(DEV), dtype=t).double().cpu()
+    for i, pick in ((0, [0, 31, 32, 255, 256, 1023, 1200]), (2, [1201, 1456, 1457, 2224, 2225, 2599])):
+        cols = torch.tensor([0, 1, 31, 32, 127, 128, 255, 256, 1000, 2047, 2048, 2303, 2304, 2309])
+        src = torch.tensor(pick)
+        xd = dequantized(q[src.to(DEV)], s[src.to(DEV)], 1, B)
+        wd = dequantized(wq[i], ws[i], B, B)[cols]
+        p = xd[:, None, :] * wd[None, :, :]
+        ref = p.sum(2)
+        lost = 7 * 2.0 ** -13 * p.abs().view(*ref.shape, C // 8, 8).amax(3).sum(2)
+        room = lost + (C + 16) * 2.0 ** -24 * p.abs().sum(2) + HALF_ULP[t] * (ref.abs() + lost)
+        assert ((y[src][:, cols] - ref).abs() <= room).all()
+
+
+def test_wgrad_few_rows_of_large_outputs():
+    """Large tiles with one block, none, and groups that end inside it."""
+    counts, N, C = [0, 1, 130, 0, 64], 1030, 1300
+    R = sum(counts)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    x, dy = rand((R, C), "bf16", 1), rand((R, N), "bf16", 2)
+    xq, xs = eplb.quantize_columns(x.to(DEV), off.to(DEV))
+    dq, ds = eplb.quantize_columns(dy.to(DEV), off.to(DEV))
+    got = eplb.expert_wgrad(dq, ds, xq, xs, off.to(DEV))
+    xd, dd = dequantized(xq.t(), xs, B, 1), dequantized(dq.t(), ds, B, 1)
+    pad = 0
+    for i, n in enumerate(counts):
+        m = up(n) * B
+        a, b = dd[pad:pad + m], xd[pad:pad + m]
+        check(got[i], a.t() @ b, a.abs().t() @ b.abs(), m, (counts, i))
+        pad += m

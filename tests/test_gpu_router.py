@@ -404,3 +404,39 @@ def test_loss_and_gradient_many_rows(scoring, dtype):
     ref, big = gradient(x64, scoring, ids, mask, True, 1.0, gw, seg, 0.2, gl, rc, rt)
     err = np.abs(got.double().cpu().numpy() - ref)
     assert (err <= 4e-5 * big + HALF_ULP[dtype] * np.abs(ref) + 2.0 ** -25).all(), err.max()
+
+
+@pytest.mark.parametrize("E,K,G,top,gtop,dtype", [
+    (120, 8, 4, 2, 2, "bf16"), (128, 16, 1, 1, 1, "f32"), (250, 7, 10, 3, 1, "bf16"), (256, 8, 8, 4, 2, "f32"),
+    (256, 16, 1, 1, 1, "f16")])
+def test_rows_of_a_long_call_are_those_of_short_ones(E, K, G, top, gtop, dtype):
+    """Rows by 16 lanes against rows by 64: the same choices, and weights and
+    gradients within the rounding of E 32-bit operations in another order."""
+    T, step = 32 * E + 37, 1000
+    x, x64, rng = make(T, E, dtype, E + K, ties=True)
+    x64[rng.random((T, E)) < 0.05] = -np.inf
+    x64[5] = -np.inf
+    x64[7] = 1.0
+    x = torch.from_numpy(x64).to(TYPES[dtype]).to(DEV)
+    bias = torch.from_numpy(rng.integers(-4, 5, size=E).astype(np.float32) * 0.25).to(DEV)
+    note("long", E, K, G, top, gtop, dtype)
+    gw = torch.from_numpy(rng.normal(size=(T, K)).astype(np.float32)).to(DEV)
+    for scoring in ("sigmoid", "softmax"):
+        kw = dict(scoring=scoring, bias=bias, G=G, top_groups=top, group_top=gtop)
+        ids, w = eplb.gate(x, K, **kw)
+        d = eplb.gate_backward(x, ids, gw, scoring=scoring)
+        for t in range(0, T, step):
+            a, b = eplb.gate(x[t:t + step], K, **kw)
+            assert torch.equal(a, ids[t:t + step])
+            torch.testing.assert_close(b, w[t:t + step], rtol=2e-5, atol=1e-30, equal_nan=True)
+            e = eplb.gate_backward(x[t:t + step], a, gw[t:t + step].contiguous(), scoring=scoring)
+            room = 4e-5 * (gw[t:t + step].abs().sum(1, keepdim=True) + 1) + 2 * HALF_ULP[dtype] * e.float().abs()
+            assert ((e.float() - d[t:t + step].float()).abs() <= room)[~e.isnan()].all()
+            assert torch.equal(e.isnan(), d[t:t + step].isnan())
+
+
+def test_group_rows_few_layers():
+    """Segments shorter than a long layer's."""
+    rng = np.random.default_rng(1)
+    for L, n, P in ((1, 2050, 30), (16, 4000, 8), (3, 32768, 288), (17, 2500, 40), (2, 32769, 5), (1, 8192, 8192)):
+        check_group(rng.integers(-1, P + 1, size=(L, n)).astype(np.int32), 0, P)
