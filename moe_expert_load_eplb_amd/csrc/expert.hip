@@ -183,17 +183,19 @@ __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulA
 // all banks.  The inner rows of a wave are taken in an order that leaves a
 // lane with 16 IT consecutive inner values of one outer row.
 //
-// Measured.  Small tiles, weights not in any cache: 8 rows on 8 of 32 experts,
-// 4096 x 2048 (67 MB): 20.4 us, 3.3 TB/s; 512 rows on 9, 2048 x 4096 (80 MB):
-// 33 us, 2.4 TB/s (a group of more than 64 rows reads its weights twice, once
-// from the die's cache).  Large tiles, 16384 rows on 9, 4096 x 4096: 404 us,
-// 1.36 POPS of the 4.4 that the instruction reaches without loads: per block of
-// 128 the vector unit takes as long for the scales (16 products and sums a
-// tile, which the matrix unit's output has to pass through) as the matrix unit
-// for the products, and both wait for LDS.  Weight gradient, 16384 rows on 9,
-// 2048 x 4096, 32-bit output: 437 us, 0.63 POPS: the conversions to 16 bits and
-// the two scales of each product are vector instructions that the matrix
-// unit's time does not cover, and about 75 us of it are the stores of 302 MB.
+// Measured, weights not in any cache.  Low tiles, 8 rows on 8 of 32 experts,
+// 4096 x 2048 (67 MB): 18.7 us, 3.6 TB/s.  Small tiles, 512 rows on 9, 2048 x
+// 4096 (80 MB): 33 us, 2.4 TB/s: a block takes a workgroup half a microsecond,
+// the latency of its loads, and 1.1 workgroups to a compute unit leave most of
+// the units waiting for those that got two.  Large tiles, 16384 rows on 9, 4096
+// x 4096: 404 us, 1.36 POPS of the 4.4 that the instruction reaches without
+// loads: per block of 128 the vector unit takes as long for the scales (16
+// multiply-adds a lane and tile, which the matrix unit's output has to pass
+// through) as the matrix unit for the products, and both wait for LDS.  Weight
+// gradient, 16384 rows on 9, 2048 x 4096, 32-bit output: 437 us, 0.63 POPS: the
+// conversions to 16 bits and the two scales of each product are vector
+// instructions that the matrix unit's time does not cover, and about 75 us of
+// it are the stores of 302 MB.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __attribute__((aligned(16))) uint8_t g_zeros[16];   // read in place of what lies past the end of K
@@ -365,7 +367,8 @@ struct TileKernel {
         for (int t = 0; t < IT; ++t)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            si[t][j] = *reinterpret_cast<const f32x4*>(scales + kOuterScaleWaves * 64 + wi + half * (16 * IT) + 16 * t + j * 4);
+            si[t][j] = *reinterpret_cast<const f32x4*>(scales + kOuterScaleWaves * 64 + wi + half * (16 * IT) + 16 * t +
+                                                       j * 4);
       }
       // a tile's scales are applied while the next tile's products are in the
       // matrix pipeline
@@ -398,7 +401,8 @@ struct TileKernel {
             for (int g = 0; g < 4; ++g)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                d[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[o % kSets][g], h), d[h], 0, 0, 0);
+                d[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[o % kSets][g], h), d[h],
+                                                            0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) d[0][i] += d[1][i];
           } else if (WIDE) {
@@ -406,13 +410,15 @@ struct TileKernel {
             for (int g = 0; g < 4; ++g)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                d[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h), half_of(fo[o % kSets][g], h), d[j & 1], 0, 0, 0);
+                d[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(half_of(fi[t][g], h),
+                                                              half_of(fo[o % kSets][g], h), d[j & 1], 0, 0, 0);
           } else {
 #pragma unroll
             for (int g = 0; g < 4; g += 2)
               d[j & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                   __builtin_shufflevector(fi[t][g], fi[t][g + 1], 0, 1, 2, 3, 4, 5, 6, 7),
-                  __builtin_shufflevector(fo[o % kSets][g], fo[o % kSets][g + 1], 0, 1, 2, 3, 4, 5, 6, 7), d[j & 1], 0, 0, 0, 0, 0, 0);
+                  __builtin_shufflevector(fo[o % kSets][g], fo[o % kSets][g + 1], 0, 1, 2, 3, 4, 5, 6, 7), d[j & 1], 0, 0, 0,
+                  0, 0, 0);
           }
           if (j > 0) apply(j - 1);
           // the tile before has had its scale by now
@@ -537,10 +543,16 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
 // kStream16: one row to a group at most, and too few tiles for their loads in
 // flight to cover the memory's latency (a streaming workgroup has 64 KiB in
 // flight, a small tile's 24).  Weights of 8-bit values not in any cache, 8 rows
-// of 64 groups, N = 2048, K = 4096 (256 tiles): 19.9 us, 23.2 with small tiles;
-// 1 row, N = 4096, K = 2048: 10.1 and 12.5.  Twice the tiles: 20.4 and 19.4.
-// Two rows to a group (32 rows, 16 groups, 2048 x 2048): 23.4 and 20.6.  K =
-// 512: 7.8 and 5.9.
+// of 64 groups, N = 2048, K = 4096 (256 tiles): 17.9 us, 21.9 with low tiles;
+// 1 row, N = 4096, K = 2048: 10.1 and 12.6.  Twice the tiles: 20.5 and 18.7.
+// 16 groups of about one row, 2048 x 2048: 22.5 and 19.0.  K = 512: 7.8 and 6.0.
+//
+// kLowTiles (32 x 64, two waves) against kSmallTiles, up to 16 rows to a group:
+// half the rows' bytes and products beside the same weights.  72 rows of 9
+// groups, 4096 x 2048: 22.9 us, 28.4 with small tiles; 16, 64, 128 and 192 rows
+// of 16, 2048 x 2048: 19.0, 19.2, 19.1 and 19.4, small 20.7, 20.8, 20.2 and
+// 20.3; 128 of 32, 1024 x 4096: 37.3 and 36.7.  512 of 9, 2048 x 4096: 36.8 and
+// 35.0, as most groups then take two.
 //
 // kSmallTiles (64 x 64, four workgroups to a compute unit) against kWideTiles
 // (128 x 256, half the bytes through LDS per product): the wide ones win where
@@ -557,7 +569,7 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
 // tiles; 8 groups of 512 rows, 2048 x 2048: 44 against 71; at 217 operations to
 // a byte (32 groups of 128 rows, 2048 x 2048) 78 and 78; 64 tiles (2048 x 2048
 // x 8192) 122 and 120.
-enum MatmulForm { kStream16, kSmallTiles, kWideTiles, kLargeTiles };
+enum MatmulForm { kStream16, kLowTiles, kSmallTiles, kWideTiles, kLargeTiles };
 
 struct MatmulPlan {
   MatmulForm form;
@@ -571,6 +583,7 @@ int64_t about_tiles(int64_t R, int64_t N, int32_t G, int rows, int n) {
 
 MatmulPlan plan_matmul(int64_t R, int64_t N, int64_t K, int32_t G, int32_t dtype) {
   if (R <= G && K >= 1024 && R * ceil_div(N, 64) <= 256) return {kStream16, 16, kStream16N};
+  if (R <= 16 * (int64_t)G) return {kLowTiles, 32, 64};
   if (dtype != kF32 && about_tiles(R, N, G, 256, 256) >= 96) {
     const double ops = 2.0 * R * N * K, bytes = (double)R * K + (double)G * N * K + 2.0 * R * N;
     if (ops >= 0x1p34 && ops >= 256.0 * bytes) return {kLargeTiles, 256, 256};
@@ -597,6 +610,10 @@ hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
   switch (p.form) {
     case kStream16:
       expert_stream16_kernel<<<grid, dim3(kStreamThreads), 0, stream>>>(a, n_tiles);
+      break;
+    case kLowTiles:
+      expert_tile_kernel<2, 1, 1, 1, 4, true><<<grid, dim3(128), TileKernel<2, 1, 1, 1, 4, true, false>::kLdsBytes,
+                                              stream>>>(a, n_tiles);
       break;
     case kSmallTiles:
       expert_tile_kernel<2, 2, 1, 1, 4, true><<<grid, dim3(256), TileKernel<2, 2, 1, 1, 4, true, false>::kLdsBytes,
