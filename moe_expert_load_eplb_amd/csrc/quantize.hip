@@ -35,6 +35,50 @@ __device__ __forceinline__ void load8(const void* p, int32_t dtype, int64_t i, i
   for (int j = 0; j < 8; ++j) v[j] = j < left ? load_as_float(p, dtype, i + j) : 0.0f;
 }
 
+// How a thread loads eight elements of a block of rows: one by one, or as 16 or
+// 32 bytes of a type known at compile time.  Then all rows' loads are in flight
+// at once: nothing stands between them, rows and columns past the end read the
+// first ones and are zeroed afterwards.
+constexpr int kScalar = -1;                  // else EPLB_DTYPE_*
+
+template <int M>
+struct Raw8 {
+  i32x4 v[M == kF32 ? 2 : 1];
+};
+
+template <int M>
+__device__ __forceinline__ Raw8<M> fetch8(const void* p, int64_t i) {
+  Raw8<M> r;
+  const i32x4* from = reinterpret_cast<const i32x4*>(static_cast<const uint8_t*>(p) + i * (M == kF32 ? 4 : 2));
+  r.v[0] = from[0];
+  if constexpr (M == kF32) r.v[1] = from[1];
+  return r;
+}
+
+template <int M>
+__device__ __forceinline__ void unpack8(const Raw8<M>& r, bool in, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (M == kF32) {
+      v[j] = in ? __int_as_float(r.v[0][j]) : 0.0f;
+      v[4 + j] = in ? __int_as_float(r.v[1][j]) : 0.0f;
+    } else {
+      const uint32_t w = in ? (uint32_t)r.v[0][j] : 0;
+      v[2 * j] = M == kBf16 ? bf16_to_float((u16)w) : f16_to_float((u16)w);
+      v[2 * j + 1] = M == kBf16 ? bf16_to_float((u16)(w >> 16)) : f16_to_float((u16)(w >> 16));
+    }
+  }
+}
+
+// Calls f with the way to load.
+template <typename F>
+hipError_t by_load(bool vec, int32_t dtype, F f) {
+  if (!vec) return f(std::integral_constant<int, kScalar>());
+  if (dtype == kF32) return f(std::integral_constant<int, kF32>());
+  if (dtype == kBf16) return f(std::integral_constant<int, kBf16>());
+  return f(std::integral_constant<int, kF16>());
+}
+
 // Largest magnitude; a NaN or an infinity among the values gives infinity.
 template <int N>
 __device__ __forceinline__ float magnitude(const float (&v)[N]) {
@@ -97,10 +141,11 @@ __global__ __launch_bounds__(kQThreads) void quantize_rows_kernel(const void* __
 // of 8 columns (16 bytes a load), whose 8-bit values are 8 consecutive bytes of
 // 8 rows of the output; they pass through LDS so that a store covers a whole
 // 128-byte run.  The gathers of `rows` are whole 256-byte runs of a 16-bit
-// type.  16384 rows of 4096 bfloat16 columns, each source row read twice: 80 us
-// (201 MB, 2.5 TB/s); 2048 columns: 45 us.  The runs of 128 bytes that it
-// writes, Rp apart, are what keeps it below the other two.
-template <bool VEC>
+// type.  16384 rows of 4096 bfloat16 columns, each source row read twice: 62 us
+// (201 MB, 3.2 TB/s; 80 us with each row's load behind a choice of its type);
+// 2048 columns: 35 us.  The runs of 128 bytes that it writes, Rp apart, are
+// what keeps it below the other two.
+template <int M>
 __global__ __launch_bounds__(kQThreads) void quantize_columns_kernel(const void* __restrict__ x, int32_t dtype,
                                                                      int64_t ld, int64_t X, int64_t C,
                                                                      const int32_t* __restrict__ rows, int32_t R,
@@ -129,10 +174,22 @@ __global__ __launch_bounds__(kQThreads) void quantize_columns_kernel(const void*
   const int cx = threadIdx.x & 15, band = threadIdx.x >> 4;
   const int64_t c0 = (int64_t)(blockIdx.x % col_tiles) * kBlock, c = c0 + cx * 8;
   float v[8][8];
+  if constexpr (M == kScalar) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int32_t from = src[band * 8 + i];
-    load8<VEC>(x, dtype, (int64_t)(from < 0 ? 0 : from) * ld + c, from < 0 ? 0 : C - c, v[i]);
+    for (int i = 0; i < 8; ++i) {
+      const int32_t from = src[band * 8 + i];
+      load8<false>(x, dtype, (int64_t)(from < 0 ? 0 : from) * ld + c, from < 0 ? 0 : C - c, v[i]);
+    }
+  } else {                                   // X > 0, C % 8 == 0
+    const bool in = c < C;
+    int32_t from[8];
+    Raw8<M> raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) from[i] = src[band * 8 + i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = fetch8<M>(x, (int64_t)(from[i] < 0 ? 0 : from[i]) * ld + (in ? c : 0));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpack8<M>(raw[i], in && from[i] >= 0, v[i]);
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -169,8 +226,8 @@ __global__ __launch_bounds__(kQThreads) void quantize_columns_kernel(const void*
 
 // One 128 x 128 block per workgroup: a thread holds 8 rows of 8 columns, so
 // that it has 8 consecutive bytes of both layouts.  9 x 2048 x 4096 bfloat16
-// with both outputs: 73 us (302 MB, 4.1 TB/s, 0.87 of a large copy).
-template <bool VEC>
+// with both outputs: 61 us (302 MB, 4.9 TB/s, as a large copy).
+template <int M>
 __global__ __launch_bounds__(kQThreads) void quantize_weights_kernel(const void* __restrict__ w, int32_t dtype, int64_t N,
                                                                      int64_t K, int32_t nn, int32_t nk,
                                                                      uint8_t* __restrict__ q, float* __restrict__ scale,
@@ -182,13 +239,21 @@ __global__ __launch_bounds__(kQThreads) void quantize_weights_kernel(const void*
   const int32_t bn = (int32_t)(blockIdx.x % per / nk), bk = (int32_t)(blockIdx.x % nk);
   const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
   const int64_t n0 = (int64_t)bn * kBlock + ry * 8, k0 = (int64_t)bk * kBlock + cx * 8;
+  constexpr bool VEC = M != kScalar;
   float v[8][8];
   float m = 0.0f;
+  if constexpr (M == kScalar) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    load8<VEC>(w, dtype, (g * N + n0 + i) * K + k0, n0 + i < N ? K - k0 : 0, v[i]);
-    m = fmaxf(m, magnitude(v[i]));
+    for (int i = 0; i < 8; ++i) load8<false>(w, dtype, (g * N + n0 + i) * K + k0, n0 + i < N ? K - k0 : 0, v[i]);
+  } else {                                   // K % 8 == 0
+    Raw8<M> raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = fetch8<M>(w, (g * N + (n0 + i < N ? n0 + i : 0)) * K + (k0 < K ? k0 : 0));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpack8<M>(raw[i], n0 + i < N && k0 < K, v[i]);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, magnitude(v[i]));
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
   if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = m;
@@ -241,14 +306,12 @@ hipError_t launch_quantize_columns(const void* x, int32_t dtype, int64_t ld, int
   const int64_t col_tiles = ceil_div(C, kBlock);
   const dim3 grid((unsigned)(Rp / kBlock * col_tiles));
   const FastDiv fd = fastdiv_make((uint32_t)K);
-  const bool vec = aligned(x, 16) && ld * dtype_size(dtype) % 16 == 0;
-  if (vec)
-    quantize_columns_kernel<true><<<grid, dim3(kQThreads), 0, stream>>>(x, dtype, ld, X, C, rows, (int32_t)R, fd, offsets,
-                                                                        G, Rp, q, scale, (int32_t)col_tiles);
-  else
-    quantize_columns_kernel<false><<<grid, dim3(kQThreads), 0, stream>>>(x, dtype, ld, X, C, rows, (int32_t)R, fd, offsets,
-                                                                         G, Rp, q, scale, (int32_t)col_tiles);
-  return hipGetLastError();
+  const bool vec = X > 0 && aligned(x, 16) && ld * dtype_size(dtype) % 16 == 0 && C % 8 == 0;
+  return by_load(vec, dtype, [&](auto mode) {
+    quantize_columns_kernel<decltype(mode)::value><<<grid, dim3(kQThreads), 0, stream>>>(
+        x, dtype, ld, X, C, rows, (int32_t)R, fd, offsets, G, Rp, q, scale, (int32_t)col_tiles);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_quantize_weights(const void* w, int32_t dtype, int32_t G, int64_t N, int64_t K, uint8_t* q,
@@ -256,13 +319,11 @@ hipError_t launch_quantize_weights(const void* w, int32_t dtype, int32_t G, int6
   const int64_t nn = ceil_div(N, kBlock), nk = ceil_div(K, kBlock);
   const dim3 grid((unsigned)(G * nn * nk));
   const bool vec = aligned(w, 16) && K % 8 == 0 && aligned(q, 8) && aligned(qt, 8);
-  if (vec)
-    quantize_weights_kernel<true><<<grid, dim3(kQThreads), 0, stream>>>(w, dtype, N, K, (int32_t)nn, (int32_t)nk, q,
-                                                                        scale, qt, scale_t);
-  else
-    quantize_weights_kernel<false><<<grid, dim3(kQThreads), 0, stream>>>(w, dtype, N, K, (int32_t)nn, (int32_t)nk, q,
-                                                                         scale, qt, scale_t);
-  return hipGetLastError();
+  return by_load(vec, dtype, [&](auto mode) {
+    quantize_weights_kernel<decltype(mode)::value><<<grid, dim3(kQThreads), 0, stream>>>(w, dtype, N, K, (int32_t)nn,
+                                                                                         (int32_t)nk, q, scale, qt, scale_t);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace eplb
