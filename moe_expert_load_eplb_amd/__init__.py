@@ -558,7 +558,7 @@ def _f8(t: torch.Tensor, name: str) -> int:
 def _optional(t, dtype: torch.dtype, shape: tuple, name: str) -> int | None:
     if t is None:
         return None
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return _dev(t, dtype, name)
 
@@ -584,7 +584,10 @@ def _workspace(workspace, need: int, device) -> torch.Tensor:
 
 
 def _shapes(out: tuple, shapes: tuple, what: str) -> None:
-    if len(out) != len(shapes) or any(tuple(t.shape) != s for t, s in zip(out, shapes)):
+    same = len(out) == len(shapes)
+    for t, s in zip(out, shapes):
+        same = same and t.shape == s
+    if not same:
         raise ValueError(f"{what} must have the shapes {[list(s) for s in shapes]}")
 
 
