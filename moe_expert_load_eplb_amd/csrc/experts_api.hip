@@ -232,7 +232,7 @@ int32_t eplb_expert_matmul(const uint8_t* q, const float* scale, int64_t X, cons
                            int64_t K, int32_t dtype, void* y, void* stream) {
   if (X < 0 || G < 1 || R < 0 || topk < 1 || N < 1 || K < 1 || K % 16 != 0 || !known_dtype(dtype)) return EPLB_E_ARG;
   if (N > kMaxDim || K > kMaxDim || R > kMaxRows || X > kMaxRows || G > kMaxSlots) return EPLB_E_LIMIT;
-  if (matmul_tiles(R, N, K, G, dtype) > kMaxTiles) return EPLB_E_LIMIT;
+  if (matmul_tiles(R, N, K, G) > kMaxTiles) return EPLB_E_LIMIT;
   if (R == 0) return EPLB_OK;
   if (w == nullptr || w_scale == nullptr || offsets == nullptr || y == nullptr) return EPLB_E_ARG;
   if (X > 0 && (q == nullptr || scale == nullptr)) return EPLB_E_ARG;

@@ -22,7 +22,6 @@ constexpr int64_t kMaxDim = int64_t(1) << 24;       // columns of an operand
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
 typedef unsigned short u16;
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 inline int64_t dtype_size(int32_t dtype) { return dtype == kF32 ? 4 : 2; }
@@ -128,7 +127,7 @@ struct WgradArgs {
   int32_t R, N, K, G, dtype;
 };
 
-int64_t matmul_tiles(int64_t R, int64_t N, int64_t K, int32_t G, int32_t dtype);
+int64_t matmul_tiles(int64_t R, int64_t N, int64_t K, int32_t G);
 int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G);
 hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_expert_wgrad(const WgradArgs& a, hipStream_t stream);
