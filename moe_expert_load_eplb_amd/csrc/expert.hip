@@ -287,12 +287,16 @@ struct TileKernel {
         for (int i = 0; i < 16; ++i) acc[o][t][i] = 0.0f;
 
     // what this lane loads of every block
-    uint32_t ip[kInnerLoads];                // from the tile's start: below 2^32, as rows are of at most 2^24 bytes
+    // from the tile's start: matmul below 2^32, as there are at most 256 rows of at most 2^24 bytes; a row of padded
+    // rows may be longer
+    typedef typename std::conditional<WGRAD, int64_t, uint32_t>::type Offset;
+    static_assert(kInner <= 256, "inner offsets in 32 bits");
+    Offset ip[kInnerLoads];
     const uint8_t* op[kOuterLoads];
 #pragma unroll
     for (int p = 0; p < kInnerLoads; ++p) {
       const int r = (wave * kInnerLoads + p) * 8 + (lane >> 3);
-      ip[p] = (uint32_t)min(r, job.inner_rows - 1) * (uint32_t)job.inner_ld + inner_part(p, wave, lane);
+      ip[p] = (Offset)min(r, job.inner_rows - 1) * (Offset)job.inner_ld + (Offset)inner_part(p, wave, lane);
     }
 #pragma unroll
     for (int p = 0; p < kOuterLoads; ++p)
