@@ -169,8 +169,10 @@ int64_t eplb_group_rows_workspace_bytes(int64_t L, int64_t n, int32_t P);
  *   scale      [R][ceil(C / 128)] float32  out
  *
  * Errors of the three calls: EPLB_E_ARG (a size < 1 where one is needed, ld
- * < C, an unknown dtype, a NULL array, outputs sharing a byte), EPLB_E_LIMIT
- * (C or N or K > 2^24, R > 2^31 - 1, G > 8192), EPLB_E_HIP.
+ * < C, an unknown dtype, a NULL array, a pointer not aligned, an output sharing
+ * a byte with an input or another output, Rp not as below), EPLB_E_LIMIT (C or N
+ * or K > 2^24, R or X > 2^31 - 1, Rp > 2^32, G > 8192, or more than 2^23 - 1
+ * blocks of 128 x 128 of columns or weights), EPLB_E_HIP.
  */
 int32_t eplb_quantize_rows(const void* x, int32_t dtype, int64_t ld, int64_t R, int64_t C, uint8_t* q, float* scale,
                            void* stream);
@@ -249,7 +251,7 @@ int32_t eplb_expert_matmul(const uint8_t* q, const float* scale, int64_t X, cons
  *                                outputs for the same offsets and Rp
  *   dw         [G][N][K] dtype   out: zeros for a group without rows
  * dy, x and dw are 16-byte aligned.  All sums are held in 32 bits.
- * Errors: as for eplb_expert_matmul.
+ * Errors: as for eplb_expert_matmul; Rp as for eplb_quantize_columns.
  */
 int32_t eplb_expert_wgrad(const uint8_t* dy, const float* dy_scale, const uint8_t* x, const float* x_scale,
                           const int32_t* offsets, int32_t G, int64_t R, int64_t Rp, int64_t N, int64_t K,

@@ -575,6 +575,23 @@ MatmulPlan plan_matmul(int64_t R, int64_t N, int64_t K, int32_t G) {
   return {kSmallTiles, 64, 64};
 }
 
+// The form of a weight gradient.
+struct WgradPlan {
+  bool large;
+  int32_t ni, no;            // tiles along K and N
+};
+
+// Large tiles (128 x 256 against 64 x 64) take half the bytes through LDS per
+// product, but there have to be enough of them: G = 8, 1024 x 1024 (256 large
+// tiles), 4096 rows: 18.0 us against 26.0 (16-bit output); 8 groups of 8 rows,
+// 32-bit output: 18.2 against 23.0; 700 x 600, G = 9 (162): 13.2 and 13.1; 2048
+// x 2048, G = 1 (128): 39.3 and 38.8; 1024 x 1024, G = 1 (32), 8192 rows: 112
+// and 45.
+WgradPlan plan_wgrad(int64_t N, int64_t K, int32_t G) {
+  const bool large = G * ceil_div(N, 128) * ceil_div(K, 256) >= 160;
+  return {large, (int32_t)ceil_div(K, large ? 256 : 64), (int32_t)ceil_div(N, large ? 128 : 64)};
+}
+
 }  // namespace
 
 int64_t matmul_tiles(int64_t R, int64_t N, int64_t K, int32_t G) {
@@ -583,7 +600,10 @@ int64_t matmul_tiles(int64_t R, int64_t N, int64_t K, int32_t G) {
   return (std::min(R, R / p.rows + G) + 2) * ceil_div(N, p.n);
 }
 
-int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G) { return G * ceil_div(N, 64) * ceil_div(K, 64); }
+int64_t wgrad_tiles(int64_t N, int64_t K, int32_t G) {
+  const WgradPlan p = plan_wgrad(N, K, G);
+  return (int64_t)G * p.ni * p.no;
+}
 
 hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
@@ -611,21 +631,14 @@ hipError_t launch_expert_matmul(const MatmulArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_expert_wgrad(const WgradArgs& a, hipStream_t stream) {
-  // Large tiles take half the bytes through LDS per product, but there have to
-  // be enough of them: G = 8, 1024 x 1024 (256 large tiles), 4096 rows: 18.0 us
-  // against 26.0 (16-bit output); 8 groups of 8 rows, 32-bit output: 18.2
-  // against 23.0; 700 x 600, G = 9 (162): 13.2 and 13.1; 2048 x 2048, G = 1
-  // (128): 39.3 and 38.8; 1024 x 1024, G = 1 (32), 8192 rows: 112 and 45.
-  const bool large = a.G * ceil_div(a.N, 128) * ceil_div(a.K, 256) >= 160;
-  const int ti = large ? 256 : 64, to = large ? 128 : 64;
-  const int32_t ni = (int32_t)ceil_div(a.K, ti), no = (int32_t)ceil_div(a.N, to);
-  const dim3 grid((unsigned)((int64_t)a.G * ni * no));
-  if (large)
+  const WgradPlan p = plan_wgrad(a.N, a.K, a.G);
+  const dim3 grid((unsigned)wgrad_tiles(a.N, a.K, a.G));
+  if (p.large)
     expert_wgrad_kernel<4, 2, 2, 2, 3><<<grid, dim3(512), TileKernel<4, 2, 2, 2, 3, true>::kLdsBytes, stream>>>(
-        a, ni, no);
+        a, p.ni, p.no);
   else
     expert_wgrad_kernel<2, 2, 1, 1, 4><<<grid, dim3(256), TileKernel<2, 2, 1, 1, 4, true>::kLdsBytes, stream>>>(
-        a, ni, no);
+        a, p.ni, p.no);
   return hipGetLastError();
 }
 

@@ -193,10 +193,10 @@ int32_t eplb_quantize_columns(const void* x, int32_t dtype, int64_t ld, int64_t 
                               int64_t R, int32_t K, const int32_t* offsets, int32_t G, int64_t Rp, uint8_t* q,
                               float* scale, void* stream) {
   if (X < 0 || C < 1 || ld < C || R < 0 || K < 1 || G < 1 || !known_dtype(dtype)) return EPLB_E_ARG;
-  if (C > kMaxDim || X > kMaxRows || R > kMaxRows || G > kMaxSlots || ld > INT64_MAX / 8 / (X + 1))
+  if (C > kMaxDim || X > kMaxRows || R > kMaxRows || G > kMaxSlots || Rp > kMaxPadded || ld > INT64_MAX / 8 / (X + 1))
     return EPLB_E_LIMIT;
   if (Rp % kBlock != 0 || Rp < (R + (kBlock - 1) * (int64_t)G) / kBlock * kBlock) return EPLB_E_ARG;
-  if (Rp / kBlock * ceil_div(C, 64) > kMaxTiles) return EPLB_E_LIMIT;
+  if (Rp / kBlock * ceil_div(C, kBlock) > kMaxTiles) return EPLB_E_LIMIT;
   if (R == 0) return EPLB_OK;
   if (offsets == nullptr || (X > 0 && x == nullptr) || q == nullptr || scale == nullptr) return EPLB_E_ARG;
   if (!aligned(x, dtype_size(dtype)) || !aligned(q, 16)) return EPLB_E_ARG;
@@ -254,7 +254,7 @@ int32_t eplb_expert_wgrad(const uint8_t* dy, const float* dy_scale, const uint8_
                           const int32_t* offsets, int32_t G, int64_t R, int64_t Rp, int64_t N, int64_t K,
                           int32_t dtype, void* dw, void* stream) {
   if (G < 1 || R < 0 || N < 1 || K < 1 || !known_dtype(dtype)) return EPLB_E_ARG;
-  if (N > kMaxDim || K > kMaxDim || R > kMaxRows || G > kMaxSlots) return EPLB_E_LIMIT;
+  if (N > kMaxDim || K > kMaxDim || R > kMaxRows || G > kMaxSlots || Rp > kMaxPadded) return EPLB_E_LIMIT;
   if (Rp % kBlock != 0 || Rp < (R + (kBlock - 1) * (int64_t)G) / kBlock * kBlock) return EPLB_E_ARG;
   if (wgrad_tiles(N, K, G) > kMaxTiles) return EPLB_E_LIMIT;
   if (offsets == nullptr || dw == nullptr || !aligned(dw, 16)) return EPLB_E_ARG;

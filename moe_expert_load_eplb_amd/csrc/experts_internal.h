@@ -20,6 +20,7 @@ constexpr int kBlock = 128;                         // elements a scale covers a
 constexpr int kMaxSlots = 8192;                     // slots of a grouping, groups of a product
 constexpr int64_t kMaxDim = int64_t(1) << 24;       // columns of an operand
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxPadded = int64_t(1) << 32;    // grouped rows, every group rounded up to 128
 
 typedef unsigned short u16;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
