@@ -187,8 +187,12 @@ int32_t eplb_quantize_rows(const void* x, int32_t dtype, int64_t ld, int64_t R, 
  *                                K of x (eplb_group_rows' order); without it
  *                                row r reads row r
  *   X                            rows that x has: a row outside [0, X) is zero
- *   offsets    [G + 1] int32     eplb_group_rows'; values are clamped to 0 ..
- *                                R, a group that ends before it starts is empty
+ *   offsets    [G + 1] int32     eplb_group_rows': non-decreasing.  Values are
+ *                                clamped to 0 .. R, a group that ends before it
+ *                                starts is empty.  Offsets that decrease make
+ *                                groups that share rows: nothing outside the
+ *                                arrays is reached, but what the outputs hold
+ *                                for such groups and rows is not defined
  *   Rp                           columns of q: a multiple of 128, at least
  *                                R + 127 G rounded down to one
  *   q          [C][Rp] 8-bit     out: columns below pad[G]; 16-byte aligned

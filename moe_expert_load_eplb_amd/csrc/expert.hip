@@ -464,8 +464,9 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_tile_kernel(MatmulArgs a, 
   int32_t row = blockIdx.x / n_tiles, column = blockIdx.x % n_tiles;
   if (kOrdered) {
     const int32_t row_tiles = count_tiles(a.offsets, a.G, a.R, K::kOuter, true);
-    if ((int64_t)blockIdx.x >= (int64_t)row_tiles * n_tiles) return;
-    band_order(die_order(blockIdx.x, row_tiles * n_tiles), row_tiles, n_tiles, row, column);
+    const int64_t tiles = min((int64_t)row_tiles * n_tiles, (int64_t)gridDim.x);    // less where offsets decrease
+    if (blockIdx.x >= tiles) return;
+    band_order(die_order(blockIdx.x, (int32_t)tiles), row_tiles, n_tiles, row, column);
   }
   const Tile t = find_tile(a.offsets, a.G, a.R, K::kOuter, row, true);
   if (t.g < 0) return;
@@ -506,10 +507,9 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
   const int64_t i0 = (int64_t)column * K::kInner, o0 = (int64_t)row * K::kOuter;
   // the group's blocks of 128 rows
   const int32_t before = count_tiles(a.offsets, g, a.R, kBlock, false);
-  const int32_t lo = clamp_row(a.offsets[g], a.R), hi = clamp_row(a.offsets[g + 1], a.R);
   TileJob job;
   job.block0 = before;
-  job.blocks = hi > lo ? (int)(((int64_t)hi - lo + kBlock - 1) / kBlock) : 0;
+  job.blocks = tiles_of(group_span(a.offsets, g, a.G, a.R), kBlock);
   if ((int64_t)job.block0 + job.blocks > a.Rp / kBlock) job.blocks = (int)(a.Rp / kBlock) - job.block0;
   job.inner = a.x + i0 * a.Rp;
   job.inner_ld = a.Rp;

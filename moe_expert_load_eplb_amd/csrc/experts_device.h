@@ -13,7 +13,30 @@ struct Tile {
   int32_t before;            // tiles of all groups before this group's
 };
 
-__device__ __forceinline__ int32_t clamp_row(int32_t v, int32_t R) { return v < 0 ? 0 : v > R ? R : v; }
+__host__ __device__ __forceinline__ int32_t clamp_row(int32_t v, int32_t R) { return v < 0 ? 0 : v > R ? R : v; }
+
+// Rows lo .. hi - 1.
+struct Span {
+  int32_t lo, hi;
+};
+
+// Rows of group g; G: those behind the last group, G + 1: those before the first.
+__host__ __device__ __forceinline__ Span group_span(const int32_t* offsets, int32_t g, int32_t G, int32_t R) {
+  if (g < G) return {clamp_row(offsets[g], R), clamp_row(offsets[g + 1], R)};
+  if (g == G) return {clamp_row(offsets[G], R), R};
+  return {0, clamp_row(offsets[0], R)};
+}
+
+__host__ __device__ __forceinline__ int32_t tiles_of(Span s, int32_t size) {
+  return s.hi > s.lo ? (int32_t)(((int64_t)s.hi - s.lo + size - 1) / size) : 0;
+}
+
+// Sum of two tile counts, at most 2^31 - 1: groups of decreasing offsets
+// overlap, and together may have more tiles than that.
+__host__ __device__ __forceinline__ int32_t add_tiles(int32_t a, int32_t b) {
+  const uint32_t sum = (uint32_t)a + (uint32_t)b;
+  return sum > 0x7FFFFFFFu ? 0x7FFFFFFF : (int32_t)sum;
+}
 
 // Tile `want` when every group's rows are cut into tiles of `size` rows, in
 // the order of the groups; with `rest`, the rows behind the last group and
@@ -26,25 +49,16 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int32_t G, int
   int32_t carry = 0;
   for (int32_t g0 = 0; g0 < n; g0 += 64) {
     const int32_t g = g0 + lane;
-    int32_t lo = 0, hi = 0;
-    if (g < G) {
-      lo = clamp_row(offsets[g], R);
-      hi = clamp_row(offsets[g + 1], R);
-    } else if (g == G && rest) {
-      lo = clamp_row(offsets[G], R);
-      hi = R;
-    } else if (g == G + 1 && rest) {
-      hi = clamp_row(offsets[0], R);
-    }
-    const int32_t tiles = hi > lo ? (int32_t)(((int64_t)hi - lo + size - 1) / size) : 0;
+    const Span rows = g < n ? group_span(offsets, g, G, R) : Span{0, 0};
+    const int32_t lo = rows.lo, hi = rows.hi, tiles = tiles_of(rows, size);
     int32_t incl = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int32_t v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
+      if (lane >= d) incl = add_tiles(incl, v);
     }
-    const int32_t before = carry + incl - tiles;
-    const u64 here = __ballot(want >= before && want < before + tiles);
+    const int32_t before = add_tiles(carry, incl - tiles);
+    const u64 here = __ballot(want >= before && want - before < tiles);
     if (here != 0) {
       const int src = __ffsll((unsigned long long)here) - 1;
       Tile t;
@@ -61,7 +75,7 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int32_t G, int
       t.rows = __builtin_amdgcn_readfirstlane(t.rows);
       return t;
     }
-    carry = __builtin_amdgcn_readfirstlane(__shfl(carry + incl, 63));
+    carry = __builtin_amdgcn_readfirstlane(__shfl(add_tiles(carry, incl), 63));
   }
   return Tile{-1, 0, 0, 0, 0};
 }
@@ -71,15 +85,9 @@ __device__ __forceinline__ int32_t count_tiles(const int32_t* offsets, int32_t G
   const int lane = threadIdx.x & 63;
   const int32_t n = rest ? G + 2 : G;
   int32_t mine = 0;
-  for (int32_t g = lane; g < n; g += 64) {
-    int32_t lo = 0, hi = 0;
-    if (g < G) lo = clamp_row(offsets[g], R), hi = clamp_row(offsets[g + 1], R);
-    else if (g == G) lo = clamp_row(offsets[G], R), hi = R;
-    else hi = clamp_row(offsets[0], R);
-    if (hi > lo) mine += (int32_t)(((int64_t)hi - lo + size - 1) / size);
-  }
+  for (int32_t g = lane; g < n; g += 64) mine = add_tiles(mine, tiles_of(group_span(offsets, g, G, R), size));
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) mine += __shfl_xor(mine, d);
+  for (int d = 32; d > 0; d >>= 1) mine = add_tiles(mine, __shfl_xor(mine, d));
   return __builtin_amdgcn_readfirstlane(mine);
 }
 
