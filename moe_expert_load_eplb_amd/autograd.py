@@ -3,7 +3,8 @@
 Thin wrappers: forward and backward are the calls of the package, chained as a
 training step chains them.  ``route`` carries gradients through the weights and
 the balance loss to the logits; ``expert_linear`` through the product to the
-rows and to the weights.
+rows and to the weights.  Neither has a second derivative: asking for one raises
+RuntimeError.
 """
 from __future__ import annotations
 
@@ -11,6 +12,23 @@ import torch
 
 from . import (expert_matmul, expert_wgrad, gate_backward, gate_loss, quantize_columns, quantize_rows,
                quantize_weights)
+
+
+class _Final(torch.autograd.Function):
+    """A gradient that depends on `through`: the same values, but differentiating them fails."""
+
+    @staticmethod
+    def forward(ctx, grad, *through):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("route and expert_linear have no second derivative")
+
+
+def _final(grad, *through):
+    # under create_graph the gradient would come back as a constant, and its share of a second derivative as zero
+    return _Final.apply(grad, *through) if grad is not None and torch.is_grad_enabled() else grad
 
 
 class _Route(torch.autograd.Function):
@@ -33,7 +51,7 @@ class _Route(torch.autograd.Function):
         dx = gate_backward(logits, ids, None if d_weights is None else d_weights.contiguous(), mask=mask, seg=seg,
                            alpha=ctx.alpha, counts=counts, tokens=tokens,
                            d_loss=None if d_loss is None else d_loss.contiguous(), **ctx.how)
-        return dx, None, None, None, None
+        return _final(dx, logits, d_weights, d_loss), None, None, None, None
 
 
 def route(logits: torch.Tensor, K: int, seg: torch.Tensor, alpha: float, **options):
@@ -49,7 +67,7 @@ class _ExpertLinear(torch.autograd.Function):
         wq, ws, wqt, wst = quantize_weights(w, transpose=True)
         y = expert_matmul(*quantize_rows(x), wq, ws, offsets, rows=rows, K=K, dtype=x.dtype)
         ctx.save_for_backward(x, wqt, wst, offsets, rows, place)
-        ctx.K, ctx.w_dtype = K, w.dtype
+        ctx.K, ctx.w = K, w              # w itself is not read again, only named to a second derivative
         return y
 
     @staticmethod
@@ -63,8 +81,8 @@ class _ExpertLinear(torch.autograd.Function):
                 dx = dx[place.long()].view(x.shape[0], ctx.K, x.shape[1]).float().sum(1).to(x.dtype)
         if ctx.needs_input_grad[1]:
             dw = expert_wgrad(*quantize_columns(dy, offsets), *quantize_columns(x, offsets, rows=rows, K=ctx.K), offsets,
-                              dtype=ctx.w_dtype)
-        return dx, dw, None, None, None, None
+                              dtype=ctx.w.dtype)
+        return _final(dx, dy, ctx.w), _final(dw, dy, x), None, None, None, None
 
 
 def expert_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
