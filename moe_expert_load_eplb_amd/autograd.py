@@ -90,9 +90,16 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows:
     """Every grouped row times the transposed weights of its expert, in 8-bit
     blocks, differentiable in x and w.
 
-    x [T, C], w [G, N, C] (C and N multiples of 16); offsets, rows and place:
-    one layer of group_rows' outputs (offsets, order, place), rows and place
-    together.  Without them x is in grouped order itself.  Returns [R, N]."""
+    x [T, C], w [G, N, C], C a multiple of 16, and N too where x needs a
+    gradient; offsets, rows and place: one layer of group_rows' outputs (offsets,
+    order, place), rows and place together.  Without them x is in grouped order
+    itself.  Returns [R, N]."""
+    if x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1]:
+        raise ValueError("x [T, C] and w [G, N, C] expected")
+    if x.shape[1] % 16 != 0:
+        raise ValueError(f"C must be a multiple of 16, got {x.shape[1]}")
+    if w.shape[1] % 16 != 0 and x.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"N must be a multiple of 16 for the gradient of x, got {w.shape[1]}")
     if (rows is None) != (place is None):
         raise ValueError("rows and place go together")
     if rows is not None and rows.shape[0] != x.shape[0] * K:

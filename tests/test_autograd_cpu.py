@@ -116,3 +116,28 @@ def test_second_derivatives_are_refused(plain):
             assert torch.equal(same, 2 * first)
     d, = torch.autograd.grad(y, x, torch.ones_like(y))      # without a graph: as ever
     assert not d.requires_grad
+
+
+def test_widths_that_the_products_refuse(plain):
+    """The contraction of a product is a multiple of 16: C of the forward pass, N
+    of the gradient of x.  What cannot be done is said before anything is done,
+    and what can be is done."""
+    x, w, off = operands(N=32, C=40)
+    with pytest.raises(ValueError, match="multiple of 16"):
+        plain.expert_linear(x, w, off)
+    x, w, off = operands(N=100, C=48)
+    with pytest.raises(ValueError, match="multiple of 16"):
+        plain.expert_linear(x, w, off)
+    assert plain.calls == []
+    with torch.no_grad():
+        assert plain.expert_linear(x, w, off).shape == (20, 100)
+    assert plain.expert_linear(x.detach(), w.detach(), off).shape == (20, 100)
+    dw, = torch.autograd.grad(plain.expert_linear(x.detach(), w, off).sum(), w)
+    assert dw.shape == w.shape
+
+
+def test_operands_that_do_not_match(plain):
+    x, w, off = operands()
+    for bad in ((x[0], w, off), (x, w[0], off), (x, w[:, :, :32], off), (x.view(40, 24), w, off)):
+        with pytest.raises(ValueError, match=r"x \[T, C\] and w \[G, N, C\]"):
+            plain.expert_linear(*bad)
