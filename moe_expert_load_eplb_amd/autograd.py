@@ -63,8 +63,9 @@ def route(logits: torch.Tensor, K: int, seg: torch.Tensor, alpha: float, **optio
 
 class _ExpertLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets, rows, place, K):
-        wq, ws, wqt, wst = quantize_weights(w, transpose=True)
+    def forward(ctx, x, w, offsets, rows, place, K, x_grad):
+        # the transposed weights are the operand of the gradient of x only
+        wq, ws, wqt, wst = quantize_weights(w, transpose=True) if x_grad else (*quantize_weights(w), None, None)
         y = expert_matmul(*quantize_rows(x), wq, ws, offsets, rows=rows, K=K, dtype=x.dtype)
         ctx.save_for_backward(x, wqt, wst, offsets, rows, place)
         ctx.K, ctx.w = K, w              # w itself is not read again, only named to a second derivative
@@ -82,7 +83,7 @@ class _ExpertLinear(torch.autograd.Function):
         if ctx.needs_input_grad[1]:
             dw = expert_wgrad(*quantize_columns(dy, offsets), *quantize_columns(x, offsets, rows=rows, K=ctx.K), offsets,
                               dtype=ctx.w.dtype)
-        return _final(dx, dy, ctx.w), _final(dw, dy, x), None, None, None, None
+        return _final(dx, dy, ctx.w), _final(dw, dy, x), None, None, None, None, None
 
 
 def expert_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
@@ -98,10 +99,11 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows:
         raise ValueError("x [T, C] and w [G, N, C] expected")
     if x.shape[1] % 16 != 0:
         raise ValueError(f"C must be a multiple of 16, got {x.shape[1]}")
-    if w.shape[1] % 16 != 0 and x.requires_grad and torch.is_grad_enabled():
+    x_grad = x.requires_grad and torch.is_grad_enabled()
+    if w.shape[1] % 16 != 0 and x_grad:
         raise ValueError(f"N must be a multiple of 16 for the gradient of x, got {w.shape[1]}")
     if (rows is None) != (place is None):
         raise ValueError("rows and place go together")
     if rows is not None and rows.shape[0] != x.shape[0] * K:
         raise ValueError(f"rows must be [{x.shape[0] * K}]")
-    return _ExpertLinear.apply(x, w, offsets, rows, place, K)
+    return _ExpertLinear.apply(x, w, offsets, rows, place, K, x_grad)

@@ -141,3 +141,21 @@ def test_operands_that_do_not_match(plain):
     for bad in ((x[0], w, off), (x, w[0], off), (x, w[:, :, :32], off), (x.view(40, 24), w, off)):
         with pytest.raises(ValueError, match=r"x \[T, C\] and w \[G, N, C\]"):
             plain.expert_linear(*bad)
+
+
+def test_transposed_weights_only_for_the_gradient_of_x(plain):
+    """They are as large as the weights: made and kept where that gradient is taken."""
+    for x_grad, w_grad, grad_mode, want in ((True, True, True, "transposed"), (True, False, True, "transposed"),
+                                            (False, True, True, "weights"), (False, False, True, "weights"),
+                                            (True, True, False, "weights")):
+        x, w, off = operands(x_grad=x_grad, w_grad=w_grad)
+        plain.calls.clear()
+        with torch.set_grad_enabled(grad_mode):
+            y = plain.expert_linear(x, w, off)
+        assert plain.calls == [want, "matmul"], (x_grad, w_grad, grad_mode)
+        assert y.requires_grad == (grad_mode and (x_grad or w_grad))
+        if y.requires_grad:
+            used = [t for t in (x, w) if t.requires_grad]
+            got = torch.autograd.grad(y, used, torch.ones_like(y))
+            assert [g.shape for g in got] == [t.shape for t in used]
+            assert plain.calls[2:] == ["matmul"] * x_grad + ["wgrad"] * w_grad
