@@ -77,9 +77,10 @@ class _ExpertLinear(torch.autograd.Function):
         dy = dy.contiguous()
         dx = dw = None
         if ctx.needs_input_grad[0]:
-            dx = expert_matmul(*quantize_rows(dy), wqt, wst, offsets, dtype=x.dtype)
-            if rows is not None:         # a token's rows, in the order of its choices
-                dx = dx[place.long()].view(x.shape[0], ctx.K, x.shape[1]).float().sum(1).to(x.dtype)
+            # a token's rows are summed in 32 bits, in the order of its choices, and rounded once
+            dx = expert_matmul(*quantize_rows(dy), wqt, wst, offsets, dtype=x.dtype if rows is None else torch.float32)
+            if rows is not None:
+                dx = dx[place.long()].view(x.shape[0], ctx.K, x.shape[1]).sum(1).to(x.dtype)
         if ctx.needs_input_grad[1]:
             dw = expert_wgrad(*quantize_columns(dy, offsets), *quantize_columns(x, offsets, rows=rows, K=ctx.K), offsets,
                               dtype=ctx.w.dtype)
