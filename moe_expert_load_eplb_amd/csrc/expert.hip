@@ -182,18 +182,18 @@ __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulA
 // lane with 16 IT consecutive inner values of one outer row.
 //
 // Measured, weights not in any cache.  Low tiles, 8 rows on 8 of 32 experts,
-// 4096 x 2048 (67 MB): 18.7 us, 3.6 TB/s.  Small tiles, 512 rows on 9, 2048 x
-// 4096 (80 MB): 33 us, 2.4 TB/s: a block takes a workgroup half a microsecond,
-// the latency of its loads, and 1.1 workgroups to a compute unit leave most of
-// the units waiting for those that got two.  Wide tiles, 16384 rows on 9, 4096 x
+// 4096 x 2048 (67 MB): 18.7 us, 3.6 TB/s.  Small tiles, 56 rows to a group, 2048 x
+// 4096: a block takes a workgroup 0.7 us, the latency of its loads, as long as
+// each has a compute unit to itself (64 workgroups 22.3 us, 256 23.4); a second
+// workgroup on a unit adds half of that again (512: 38.8 us, 3.5 TB/s), also where
+// few units have two (288, which is 9 groups: 34.6 us, 2.2 TB/s).  Wide tiles, 16384 rows on 9, 4096 x
 // 4096, bfloat16 output: 597 us with the rows' quantisation in the call, 0.92
 // PFLOP/s: the conversions to 16 bits and the scales (16 multiply-adds a lane and
 // tile, which the matrix unit's output has to pass through) are vector
 // instructions beside the matrix unit's.  Weight
 // gradient, 16384 rows on 9, 2048 x 4096, 32-bit output: 437 us, 0.63 POPS: the
 // conversions to 16 bits and the two scales of each product are vector
-// instructions that the matrix unit's time does not cover, and about 75 us of
-// it are the stores of 302 MB.
+// instructions that the matrix unit's time does not cover, and it stores 302 MB.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __attribute__((aligned(16))) uint8_t g_zeros[16];   // read in place of what lies past the end of K
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(WI* WO * 64) void expert_wgrad_kernel(WgradArgs a, 
 // 20.3; 128 of 32, 1024 x 4096: 37.3 and 36.7.  512 of 9, 2048 x 4096: 36.8 and
 // 35.0, as most groups then take two.
 //
-// kSmallTiles (64 x 64, four workgroups to a compute unit) against kWideTiles
+// kSmallTiles (64 x 64, two workgroups to a compute unit) against kWideTiles
 // (128 x 256, half the bytes through LDS per product): the wide ones win where
 // there are more of them than half the compute units and the groups fill them.
 // G = 1, K = 4096, N = 4096, 2048 rows (256 wide tiles): 76.5 us against 119.3;

@@ -8,9 +8,7 @@ namespace eplb {
 // A run of rows of one group that a workgroup works on.
 struct Tile {
   int32_t g;                 // group; G and G + 1: rows of no group; -1: none
-  int32_t index;             // which of the group's tiles
   int32_t row, rows;         // its rows
-  int32_t before;            // tiles of all groups before this group's
 };
 
 __host__ __device__ __forceinline__ int32_t clamp_row(int32_t v, int32_t R) { return v < 0 ? 0 : v > R ? R : v; }
@@ -63,21 +61,17 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int32_t G, int
       const int src = __ffsll((unsigned long long)here) - 1;
       Tile t;
       t.g = __shfl(g, src);
-      t.before = __shfl(before, src);
-      t.index = want - t.before;
-      t.row = __shfl(lo, src) + t.index * size;
+      t.row = __shfl(lo, src) + (want - __shfl(before, src)) * size;
       const int32_t left = __shfl(hi, src) - t.row;
       t.rows = left < size ? left : size;
       t.g = __builtin_amdgcn_readfirstlane(t.g);
-      t.before = __builtin_amdgcn_readfirstlane(t.before);
-      t.index = __builtin_amdgcn_readfirstlane(t.index);
       t.row = __builtin_amdgcn_readfirstlane(t.row);
       t.rows = __builtin_amdgcn_readfirstlane(t.rows);
       return t;
     }
     carry = __builtin_amdgcn_readfirstlane(__shfl(add_tiles(carry, incl), 63));
   }
-  return Tile{-1, 0, 0, 0, 0};
+  return Tile{-1, 0, 0};
 }
 
 // Number of tiles of all groups and, with `rest`, of the rows of no group.
@@ -101,7 +95,10 @@ __device__ __forceinline__ int32_t die_order(int32_t id, int32_t total) {
 
 // Tile `id` of rows x columns tiles taken in bands of four rows, column by
 // column: the 32 tiles that a die works on at once are 4 x 8, which read 12
-// different operand tiles (one row after the other: 18 of 2 x 16).
+// different operand tiles (one row after the other: 18 of 2 x 16).  Bands of
+// one, two, four and eight rows, 16384 x 8192 x 2048: 635, 600, 589 and 590 us;
+// 16384 rows on 9, 4096 x 4096: 682, 686, 676, 672; weight gradient of 16384 rows
+// on 9, 2048 x 4096: 364, 364, 350, 368.
 __device__ __forceinline__ void band_order(int32_t id, int32_t rows, int32_t columns, int32_t& row, int32_t& column) {
   const int32_t band = id / (4 * columns), at = id - band * 4 * columns;
   const int32_t high = rows - band * 4 < 4 ? rows - band * 4 : 4;

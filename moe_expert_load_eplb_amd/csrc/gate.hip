@@ -100,8 +100,8 @@ __device__ __forceinline__ int row_last(int v) {
 // 1 / d correctly rounded, for 1 <= d <= 2^126: the hardware's approximation,
 // one Newton step, and Markstein's correction by the remainder, which rounds
 // correctly where no intermediate is denormal (compared with the division for
-// every such d).  Half the instructions of the general division, and the same
-// bits.
+// every 32-bit d of that range).  Half the instructions of the general division,
+// and the same bits.
 __device__ __forceinline__ float reciprocal(float d) {
   float r = __builtin_amdgcn_rcpf(d);
   r = fmaf(fmaf(-d, r, 1.0f), r, r);
@@ -406,7 +406,7 @@ __device__ __forceinline__ void gate_row(const GateArgs& a, int64_t t, bool real
 #pragma unroll
   for (int j = 0; j < VPL; ++j) key[j] = 0.0f;
   if (a.bias != nullptr) {
-if (a.vec) {
+    if (a.vec) {
 #pragma unroll
       for (int j = 0; j < VPL; j += kV) {
         const f32x4 b = *reinterpret_cast<const f32x4*>(a.bias + min(expert_of<LPR>(j, lane), a.E - kV));
@@ -874,7 +874,10 @@ hipError_t launch_gate_backward(const GateBackwardArgs& args, hipStream_t stream
   return by_width(a.T, a.E, a.K, [&](auto lpr, auto vpl) {
     constexpr int LPR = decltype(lpr)::value, VPL = decltype(vpl)::value, kRows = kGateThreads / LPR;
     const size_t lds = (size_t)kRows * ((a.E + 3) / 4 * 4 + 4) * 4;
-    // a few rows per lane group where there are many, so that a segment's counts are read once for them
+    // A few rows per lane group where there are many, so that a segment's counts are read once for them.  1, 2, 4 and 8
+    // rows: 16384 x 256 (here 2) 15.8, 15.1, 20.7 and 35.1 us; 4096 x 256 (1) 9.0, 9.0, 10.4, 16.8; 262144 x 256 bfloat16
+    // (8) 165, 129, 116, 113; in between the rule is past the best: 65536 x 256 bfloat16 (8) 46.2, 37.2, 36.4, 43.0; 16384
+    // x 512 (8) 27.1, 23.8, 22.6, 27.8.
     const int32_t per_group = (int32_t)std::min<int64_t>(8, std::max<int64_t>(1, a.T / (kRows * 512)));
     gate_backward_kernel<LPR, VPL><<<dim3((unsigned)ceil_div(a.T, (int64_t)kRows * per_group)), dim3(kGateThreads),
                                      lds, stream>>>(a, per_group);
