@@ -44,8 +44,8 @@ extern "C" {
  * gets ids -1 and weights 0.
  *
  *   logits     [T][E] dtype      router logits, rows `ld` elements apart
- *                                (ld >= E); a softmax row with an infinite or
- *                                NaN logit has the formula's NaN scores
+ *                                (ld >= E); a softmax row with a logit of plus
+ *                                infinity or NaN has the formula's NaN scores
  *   dtype                        EPLB_DTYPE_* of logits
  *   T, E, K                      tokens (0 .. 2^25), experts (1 .. 4096),
  *                                choices (1 .. 64, at most E)

@@ -851,8 +851,8 @@ def expert_matmul(q: torch.Tensor, scale: torch.Tensor, w: torch.Tensor, w_scale
     q [X, C], scale: quantize_rows' outputs; w [G, N, C], w_scale:
     quantize_weights'; offsets [G + 1] int32: rows offsets[g] .. offsets[g + 1]
     - 1 belong to expert g.  Grouped row r reads row rows[r] // K of q
-    (group_rows' order), or row r without rows.  Returns [R, N] in ``dtype``;
-    rows of no expert are 0.  offsets = [0, R] is the plain product.
+    (group_rows' order), or row r without rows.  Returns [R, N] in ``dtype``
+    (out's own type where out is given); rows of no expert are 0.  offsets = [0, R] is the plain product.
     """
     if q.dim() != 2 or w.dim() != 3 or w.shape[2] != q.shape[1]:
         raise ValueError("q [X, C] and w [G, N, C] expected")

@@ -183,17 +183,19 @@ __global__ __launch_bounds__(kStreamThreads) void expert_stream16_kernel(MatmulA
 //
 // Measured, weights not in any cache.  Low tiles, 8 rows on 8 of 32 experts,
 // 4096 x 2048 (67 MB): 18.7 us, 3.6 TB/s.  Small tiles, 56 rows to a group, 2048 x
-// 4096: a block takes a workgroup 0.7 us, the latency of its loads, as long as
-// each has a compute unit to itself (64 workgroups 22.3 us, 256 23.4); a second
-// workgroup on a unit adds half of that again (512: 38.8 us, 3.5 TB/s), also where
-// few units have two (288, which is 9 groups: 34.6 us, 2.2 TB/s).  Wide tiles, 16384 rows on 9, 4096 x
-// 4096, bfloat16 output: 597 us with the rows' quantisation in the call, 0.92
-// PFLOP/s: the conversions to 16 bits and the scales (16 multiply-adds a lane and
-// tile, which the matrix unit's output has to pass through) are vector
-// instructions beside the matrix unit's.  Weight
-// gradient, 16384 rows on 9, 2048 x 4096, 32-bit output: 437 us, 0.63 POPS: the
-// conversions to 16 bits and the two scales of each product are vector
-// instructions that the matrix unit's time does not cover, and it stores 302 MB.
+// 4096: a block takes a workgroup 0.7 us as long as each has a compute unit to
+// itself (64 workgroups 22.3 us, 256 23.4): a wave, alone on its SIMD, issues
+// about 160 vector and 8 matrix instructions for two thirds of it and waits for
+// loads and LDS the rest.  So a second workgroup on a unit adds half of the first
+// one's time and more (512: 38.8 us, 3.5 TB/s), also where few units have two (288,
+// which is 9 groups: 34.6 us, 2.2 TB/s).  Wide tiles, 16384 rows on 9, 4096 x 4096,
+// bfloat16 output: 622 to 654 us, 0.84 to 0.88 PFLOP/s: the matrix units are busy
+// for 47 % of the time and the vector units for 44 %, with 7.6 instructions to a
+// matrix instruction (conversions to 16 bits, and 16 multiply-adds a lane and tile
+// for the scales, which the matrix unit's output has to pass through); two waves
+// to a SIMD overlap little of the two.  Weight gradient, 16384 rows on 9, 2048 x
+// 4096, 32-bit output: 375 to 402 us, 0.68 to 0.73 PFLOP/s, with two scales to each
+// product: 37 % and 46 %; it stores 302 MB.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __attribute__((aligned(16))) uint8_t g_zeros[16];   // read in place of what lies past the end of K

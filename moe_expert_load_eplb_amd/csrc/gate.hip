@@ -7,18 +7,20 @@
 // LPR lanes.  16 lanes to a row for many rows (four rows share the cost of
 // every butterfly), 64 for few (shorter chains).
 //
-// What bounds the choice is arithmetic, not memory: an exponential and a
-// division per logit (about 20 instructions), and the selection, so all of it
-// is free of branches that differ between lanes.  For the K largest of a row:
+// What bounds the choice is arithmetic, not memory: 76 vector instructions per
+// logit (the vector units are busy for 79 % of the kernel's time), of which an
+// exponential and a division are about 20 and the group limit and the selection
+// the rest, so all of it is free of branches that differ between lanes.  For the K largest of a row:
 // the largest keys of 16 parts of it go to LDS; the K-th largest of those
 // bounds the K-th largest key from below, so that only a few more than K keys
 // (11 of 256 for K = 8) can be among the K largest.  They are compacted into
 // LDS and ranked by counting.
 //
 // Measured, 16384 tokens, 256 experts in 8 groups (4 taken), 8 chosen,
-// sigmoid: the choice 14.6 us from bfloat16 logits (9.5 MB: 0.65 TB/s); with
-// the loss 24.1 + 7.4 us from 32-bit ones, the gradient 17.0 us (35 MB: 2.0
-// TB/s).  One token: 3.6 us, the chain of its butterflies.
+// sigmoid: the choice 14.9 us from bfloat16 logits (9.5 MB: 0.63 TB/s); with
+// the loss 24.3 + 7.3 us from 32-bit ones, the gradient 17.0 us (34 MB: 2.0
+// TB/s; vector units busy for 39 %, its two waves to a SIMD wait for 62 % of their
+// time).  One token: 3.4 us, the chain of its butterflies.
 #include "experts_internal.h"
 
 namespace eplb {

@@ -9,8 +9,8 @@
 //
 // Bound by latency: of the launches, of the chain of 64-id steps in a wave
 // (ballots, one LDS round trip each), and of the sums over segments.  512 ids,
-// 320 slots: 4.7 us; 131,072 ids, 288 slots: 3.3 + 11.4 us (1.6 MB, whose copy
-// would take 0.4).
+// 320 slots: 4.5 us; 131,072 ids, 288 slots: 3.4 + 11.3 us (1.6 MB, whose copy
+// would take 0.3; the waves wait for two thirds of the second launch).
 #include "experts_internal.h"
 
 namespace eplb {

@@ -1,8 +1,8 @@
 // Blocks of 128 in 8-bit floating point: along rows (activations), down the
 // rows of a group (operands of a weight gradient), 128 x 128 (weights).
 //
-// All three read 2 or 4 bytes and write 1 per element and are bound by HBM.
-// Elements stay in registers between the block's maximum and the rounding.
+// All three read 2 or 4 bytes and write 1 per element.  Elements stay in
+// registers between the block's maximum and the rounding.
 #include "experts_device.h"
 
 namespace eplb {
@@ -113,8 +113,8 @@ __device__ __forceinline__ void store8(uint8_t* p, int64_t i, int64_t left, uint
 }
 
 // A block is 16 lanes of 8 elements, 16 bytes of a 16-bit type a lane; a
-// workgroup takes 16 blocks.  8192 x 4096 bfloat16: 25 us (102 MB, 4.1 TB/s,
-// 0.86 of a large copy).
+// workgroup takes 16 blocks.  8192 x 4096 bfloat16: 25 us (102 MB, 4.1 TB/s, two
+// thirds of a copy's rate): the vector units are busy for 90 % of it.
 template <bool VEC>
 __global__ __launch_bounds__(kQThreads) void quantize_rows_kernel(const void* __restrict__ x, int32_t dtype, int64_t ld,
                                                                   int64_t R, int64_t C, int64_t nb,
@@ -141,10 +141,10 @@ __global__ __launch_bounds__(kQThreads) void quantize_rows_kernel(const void* __
 // of 8 columns (16 bytes a load), whose 8-bit values are 8 consecutive bytes of
 // 8 rows of the output; they pass through LDS so that a store covers a whole
 // 128-byte run.  The gathers of `rows` are whole 256-byte runs of a 16-bit
-// type.  16384 rows of 4096 bfloat16 columns, each source row read twice: 62 us
-// (201 MB, 3.2 TB/s; 80 us with each row's load behind a choice of its type);
-// 2048 columns: 35 us.  The runs of 128 bytes that it writes, Rp apart, are
-// what keeps it below the other two.
+// type.  16384 rows of 4096 bfloat16 columns, each source row read twice: 58 us
+// (201 MB, 3.5 TB/s; 80 us with each row's load behind a choice of its type);
+// 2048 columns: 34 us.  LDS bounds it, busy for 86 % of the time, three quarters
+// of that with bank conflicts (the turned block's stores).
 template <int M>
 __global__ __launch_bounds__(kQThreads) void quantize_columns_kernel(const void* __restrict__ x, int32_t dtype,
                                                                      int64_t ld, int64_t X, int64_t C,
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kQThreads) void quantize_columns_kernel(const void*
 
 // One 128 x 128 block per workgroup: a thread holds 8 rows of 8 columns, so
 // that it has 8 consecutive bytes of both layouts.  9 x 2048 x 4096 bfloat16
-// with both outputs: 61 us (302 MB, 4.9 TB/s, as a large copy).
+// with both outputs: 60 us (302 MB, 5.1 TB/s, 0.8 of a copy's rate).
 template <int M>
 __global__ __launch_bounds__(kQThreads) void quantize_weights_kernel(const void* __restrict__ w, int32_t dtype, int64_t N,
                                                                      int64_t K, int32_t nn, int32_t nk,
