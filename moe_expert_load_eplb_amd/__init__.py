@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the path runs in the HIP kernels of
 ``libeplb.so``; this module checks dtypes, devices and contiguity, passes raw
 device pointers and the current HIP stream through the C ABI declared in
-``include/eplb.h`` and ``include/eplb_experts.h``, and raises :class:`EplbError` on a non-zero return code.
+``include/eplb.h``, ``include/eplb_experts.h`` and ``include/eplb_layer.h``, and raises :class:`EplbError` on a non-zero
+return code.
 PyTorch supplies device memory and streams.
 
 Importing this package loads the library; if it has not been built
@@ -43,7 +44,9 @@ EXPORTS = ("eplb_load_hist", "eplb_rebalance", "eplb_redirect", "eplb_hist_redir
            "eplb_rebalance_lds_bytes", "eplb_rebalance_max_count", "eplb_lp_redirect_noalloc",
            "eplb_gate", "eplb_gate_loss", "eplb_gate_loss_workspace_bytes", "eplb_balance_loss", "eplb_gate_backward",
            "eplb_group_rows", "eplb_group_rows_workspace_bytes", "eplb_quantize_rows", "eplb_quantize_columns",
-           "eplb_quantize_weights", "eplb_expert_matmul", "eplb_expert_wgrad")
+           "eplb_quantize_weights", "eplb_expert_matmul", "eplb_expert_wgrad",
+           "eplb_expert_matmul16", "eplb_expert_wgrad16", "eplb_quantize_weights4", "eplb_expert_matmul4",
+           "eplb_combine_rows", "eplb_combine_rows_backward")
 
 
 def _load() -> ctypes.CDLL:
@@ -113,6 +116,18 @@ def _load() -> ctypes.CDLL:
     lib.eplb_expert_matmul.restype = i32
     lib.eplb_expert_wgrad.argtypes = [p, p, p, p, p, i32, i64, i64, i64, i64, i32, p, p]
     lib.eplb_expert_wgrad.restype = i32
+    lib.eplb_expert_matmul16.argtypes = [p, i32, i64, i64, p, p, i32, p, i64, i32, i64, i64, i32, i32, p, p]
+    lib.eplb_expert_matmul16.restype = i32
+    lib.eplb_expert_wgrad16.argtypes = [p, i32, i64, i64, p, i64, i64, p, i32, p, i32, i64, i64, i32, p, p]
+    lib.eplb_expert_wgrad16.restype = i32
+    lib.eplb_quantize_weights4.argtypes = [p, i32, i32, i64, i64, p, p, p]
+    lib.eplb_quantize_weights4.restype = i32
+    lib.eplb_expert_matmul4.argtypes = [p, i32, i64, i64, p, p, p, i32, p, i64, i32, i64, i64, i32, p, p]
+    lib.eplb_expert_matmul4.restype = i32
+    lib.eplb_combine_rows.argtypes = [p, i32, i64, i64, p, p, i64, i32, i32, p, p]
+    lib.eplb_combine_rows.restype = i32
+    lib.eplb_combine_rows_backward.argtypes = [p, i32, p, i32, i64, p, p, p, i64, i32, p, p, p]
+    lib.eplb_combine_rows_backward.restype = i32
     return lib
 
 
@@ -894,4 +909,199 @@ def expert_wgrad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x_sc
                                _dev(x_scale, torch.float32, "x_scale"), _dev(offsets, torch.int32, "offsets"), G, R,
                                Rp, N, C, _dtype(out.dtype, "out"), _dev(out, out.dtype, "out"), _stream(dy.device))
     _check(rc, "eplb_expert_wgrad")
+    return out
+
+
+# ---------------------------------------------------------------- 16-bit and 4-bit products, rows joined to tokens
+SCALE_GROUP = 32             # 4-bit elements a scale covers along a row
+
+
+def _launch(name: str, dev: torch.device, *args) -> None:
+    """Calls the entry point on dev's current stream, with dev the current device."""
+    fn = getattr(lib, name)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    _check(rc, name)
+
+
+def _together(*tensors) -> torch.device:
+    """The one device of the tensors that are given."""
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return dev
+
+
+def _short(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """_rows of a bfloat16 or float16 tensor."""
+    if isinstance(t, torch.Tensor) and t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return _rows(t, name)
+
+
+def expert_matmul16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                    K: int = 1, transpose: bool = False, dtype: torch.dtype | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Every grouped row times the transposed weights of its expert, both in 16
+    bits; with transpose, times the weights as they are.
+
+    x [X, C] bfloat16 or float16 (rows may be strided by multiples of 8); w [G,
+    N, C] of the same type; offsets [G + 1] int32: rows offsets[g] .. offsets[g
+    + 1] - 1 belong to expert g.  Grouped row r reads row rows[r] // K of x
+    (group_rows' order), or row r without rows.  Returns [R, N] in ``dtype``
+    (out's own type where out is given, else x's); rows of no expert are 0.
+    With transpose x is [X, N] and the result [R, C]: the gradient of the rows
+    from that of the product.  C is a multiple of 8, with transpose N too.
+    """
+    ptr, code, ld = _short(x, "x")
+    if w.dim() != 3 or x.shape[1] != w.shape[1 if transpose else 2]:
+        raise ValueError("x [X, N] and w [G, N, C] expected" if transpose else "x [X, C] and w [G, N, C] expected")
+    X = x.shape[0]
+    G, N, C = w.shape
+    g, R = _grouping(offsets, rows, None if out is None else out.shape[0], X, K)
+    if g != G:
+        raise ValueError(f"offsets must be [{G + 1}]")
+    dev = _together(x, w, offsets, rows, out)
+    width = C if transpose else N
+    if out is None:
+        out = torch.empty((R, width), dtype=x.dtype if dtype is None else dtype, device=dev)
+    else:
+        _shapes((out,), ((R, width),), "out")
+    _launch("eplb_expert_matmul16", dev, ptr, code, ld, X, _dev(w, x.dtype, "w"), _dev(offsets, torch.int32, "offsets"),
+            G, _optional(rows, torch.int32, (R,), "rows"), R, K, N, C, int(transpose), _dtype(out.dtype, "out"),
+            _dev(out, out.dtype, "out"))
+    return out
+
+
+def expert_wgrad16(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                   K: int = 1, dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of expert_matmul16 with respect to the weights: [G, N, C] in
+    ``dtype`` (out's own type where out is given, else x's).
+
+    dy [R, N]: the gradient of the product; x [X, C], offsets, rows and K: its
+    arguments.  N and C are multiples of 8; rows may be strided by multiples of
+    8.  An expert without rows gets zeros."""
+    dptr, code, dy_ld = _short(dy, "dy")
+    ptr, xcode, ld = _short(x, "x")
+    if code != xcode:
+        raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
+    X, C = x.shape
+    N = dy.shape[1]
+    G, R = _grouping(offsets, rows, None, X, K)
+    if dy.shape[0] != R:
+        raise ValueError(f"dy must be [{R}, N]")
+    dev = _together(x, dy, offsets, rows, out)
+    if out is None:
+        out = torch.empty((G, N, C), dtype=x.dtype if dtype is None else dtype, device=dev)
+    else:
+        _shapes((out,), ((G, N, C),), "out")
+    _launch("eplb_expert_wgrad16", dev, dptr, code, dy_ld, R, ptr, ld, X, _dev(offsets, torch.int32, "offsets"), G,
+            _optional(rows, torch.int32, (R,), "rows"), K, N, C, _dtype(out.dtype, "out"), _dev(out, out.dtype, "out"))
+    return out
+
+
+def quantize_weights4(w: torch.Tensor, out: tuple | None = None):
+    """w [G, N, C] as 4-bit floating point (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6)
+    with a power of two for each 32 elements of a row: (q [G, N, C / 2] uint8,
+    two codes to a byte, the even element in the low half; scale [G, N, C / 32]
+    uint8, 2^(scale - 127), 255: NaN).  C is a multiple of 32."""
+    if w.dim() != 3:
+        raise ValueError("w must be [G, N, C]")
+    G, N, C = w.shape
+    shapes = ((G, N, C // 2), (G, N, C // SCALE_GROUP))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.uint8, device=w.device) for s in shapes)
+    _shapes(out, shapes, "out")
+    dev = _together(w, *out)
+    _launch("eplb_quantize_weights4", dev, _dev(w, w.dtype, "w"), _dtype(w.dtype, "w"), G, N, C,
+            _dev(out[0], torch.uint8, "q"), _dev(out[1], torch.uint8, "scale"))
+    return out
+
+
+def expert_matmul4(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, offsets: torch.Tensor,
+                   rows: torch.Tensor | None = None, K: int = 1, dtype: torch.dtype | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """expert_matmul16 with 4-bit weights: x [X, C] bfloat16 or float16; w [G, N, C
+    / 2], w_scale [G, N, C / 32]: quantize_weights4's outputs."""
+    ptr, code, ld = _short(x, "x")
+    X, C = x.shape
+    if w.dim() != 3 or 2 * w.shape[2] != C:
+        raise ValueError("x [X, C] and w [G, N, C / 2] expected")
+    G, N, _ = w.shape
+    g, R = _grouping(offsets, rows, None if out is None else out.shape[0], X, K)
+    if g != G:
+        raise ValueError(f"offsets must be [{G + 1}]")
+    dev = _together(x, w, w_scale, offsets, rows, out)
+    if out is None:
+        out = torch.empty((R, N), dtype=x.dtype if dtype is None else dtype, device=dev)
+    _shapes((w_scale, out), ((G, N, C // SCALE_GROUP), (R, N)), "w_scale, out")
+    _launch("eplb_expert_matmul4", dev, ptr, code, ld, X, _dev(w, torch.uint8, "w"),
+            _dev(w_scale, torch.uint8, "w_scale"), _dev(offsets, torch.int32, "offsets"), G,
+            _optional(rows, torch.int32, (R,), "rows"), R, K, N, C, _dtype(out.dtype, "out"), _dev(out, out.dtype, "out"))
+    return out
+
+
+def _choices(place: torch.Tensor, weights: torch.Tensor | None) -> tuple[int, int]:
+    """(tokens, choices of a token) of a grouping's place and the router's weights."""
+    shaped = place if weights is None else weights
+    if shaped.dim() != 2:
+        raise ValueError("weights must be [T, K]" if weights is not None else "place must be [T, K] without weights")
+    T, K = shaped.shape
+    if place.numel() != T * K or place.dim() > 2:
+        raise ValueError(f"place must have {T * K} elements")
+    return T, K
+
+
+def combine_rows(y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor | None,
+                 dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The experts' rows joined to tokens: out[t] = sum over k of weights[t, k] *
+    y[place[t, k]], in 32 bits, rounded once.
+
+    y [R, C] float32, bfloat16 or float16; place [T, K] (or [T * K]) int32:
+    group_rows' place, outside [0, R): nothing is added; weights [T, K] float32
+    (the router's), or None: ones, place being [T, K].  Returns [T, C] in
+    ``dtype`` (out's own type where out is given, else y's)."""
+    T, K = _choices(place, weights)
+    if y.dim() != 2:
+        raise ValueError("y must be [R, C]")
+    R, C = y.shape
+    dev = _together(y, place, weights, out)
+    if out is None:
+        out = torch.empty((T, C), dtype=y.dtype if dtype is None else dtype, device=dev)
+    else:
+        _shapes((out,), ((T, C),), "out")
+    _launch("eplb_combine_rows", dev, _dev(y, y.dtype, "y"), _dtype(y.dtype, "y"), R, C,
+            _dev(place, torch.int32, "place"), _optional(weights, torch.float32, (T, K), "weights"), T, K,
+            _dtype(out.dtype, "out"), _dev(out, out.dtype, "out"))
+    return out
+
+
+def combine_rows_backward(d_out: torch.Tensor, y: torch.Tensor, place: torch.Tensor, order: torch.Tensor,
+                          weights: torch.Tensor | None, out: tuple | None = None):
+    """Gradients of combine_rows: (d_y [T * K, C] in y's type, d_weights [T, K]
+    float32).
+
+    d_out [T, C]; y [T * K, C]; place and order: group_rows', each the inverse of
+    the other.  A choice whose place is outside y gets d_weights 0, a row that is
+    not the place of its own order gets zeros."""
+    T, K = _choices(place, weights)
+    if d_out.dim() != 2 or d_out.shape[0] != T:
+        raise ValueError(f"d_out must be [{T}, C]")
+    C = d_out.shape[1]
+    _shapes((y,), ((T * K, C),), "y")
+    if order.numel() != T * K:
+        raise ValueError(f"order must have {T * K} elements")
+    dev = _together(d_out, y, place, order, weights, *(out or ()))
+    if out is None:
+        out = (torch.empty((T * K, C), dtype=y.dtype, device=dev), torch.empty((T, K), dtype=torch.float32, device=dev))
+    else:
+        _shapes(out, ((T * K, C), (T, K)), "out")
+    _launch("eplb_combine_rows_backward", dev, _dev(d_out, d_out.dtype, "d_out"), _dtype(d_out.dtype, "d_out"),
+            _dev(y, y.dtype, "y"), _dtype(y.dtype, "y"), C, _dev(place, torch.int32, "place"),
+            _dev(order, torch.int32, "order"), _optional(weights, torch.float32, (T, K), "weights"), T, K,
+            _dev(out[0], y.dtype, "d_y"), _dev(out[1], torch.float32, "d_weights"))
     return out

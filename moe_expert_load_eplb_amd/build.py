@@ -26,7 +26,8 @@ REF_SOURCES = [os.path.join("ref", "stream_ref.hip")]
 ARCH = "gfx950"
 
 SOURCES = ["api.hip", "hist.hip", "rebalance.hip", "redirect.hip", "fused.hip", "quality.hip", "rearrange.hip", "lp.hip",
-           "lp_noalloc.hip", "experts_api.hip", "gate.hip", "group.hip", "quantize.hip", "expert.hip"]
+           "lp_noalloc.hip", "experts_api.hip", "gate.hip", "group.hip", "quantize.hip", "expert.hip",
+           "layer_api.hip", "linear16.hip", "linear4.hip", "quantize4.hip", "combine.hip"]
 
 
 def hipcc() -> str:
