@@ -135,25 +135,22 @@ struct Along {
   int part;                                // its first k within a block
   int at[4];                               // where the four steps' parts of this lane's row lie in LDS
 
-  // start(r): where row r of the tile begins (any valid row for one that is not stored), or NULL: zeros
+  // start(r): where row r of the tile begins (any valid row for one that is not stored)
   template <typename Start>
   __device__ __forceinline__ void init(int lane, int wave, int first, Start start) {
     part = ((lane & 7) ^ ((wave * 8 + (lane >> 3)) >> 1 & 7)) * 8;
 #pragma unroll
     for (int p = 0; p < kLoads; ++p) {
-      row[p] = start((p * W + wave) * 8 + (lane >> 3));
-      if (row[p] != nullptr) row[p] += part * 2;
+      row[p] = start((p * W + wave) * 8 + (lane >> 3)) + part * 2;
     }
     const int r = tile_row<T, INNER>(lane & 31, 0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) at[s] = (first + r) * 128 + (((s * 2 + (lane >> 5)) ^ (r >> 1 & 7)) << 4);
   }
-  // block blk, of K elements in all, to LDS
-  __device__ __forceinline__ void load(int blk, int K, int wave, uint32_t lds) const {
+  // load p of block blk, of K elements in all, to LDS
+  __device__ __forceinline__ void load(int p, int blk, int K, int wave, uint32_t lds) const {
     const bool in = blk * kTileK + part < K;
-#pragma unroll
-    for (int p = 0; p < kLoads; ++p)
-      part_to_lds(in && row[p] != nullptr ? row[p] + (int64_t)blk * 128 : g_zero_part, lds + (p * W + wave) * 1024);
+    part_to_lds(in ? row[p] + (int64_t)blk * 128 : g_zero_part, lds + (p * W + wave) * 1024);
   }
   __device__ __forceinline__ i32x4 fragment(const uint8_t* lds, int t, int s) const {
     return *reinterpret_cast<const i32x4*>(lds + at[s] + (INNER ? 16 : 32) * 128 * t);
@@ -161,7 +158,7 @@ struct Along {
 };
 
 // Memory rows are k; rows of the operand are columns there.
-template <int ROWS, int W, int T, bool INNER, bool GATHER>
+template <int ROWS, int W, int T, bool INNER>
 struct Across {
   static constexpr bool kThroughRegisters = false;
   static constexpr int kParts = ROWS / 8;            // 16-byte parts of a memory row
@@ -169,33 +166,28 @@ struct Across {
   static constexpr int kLoads = kTileK / kEach / W;
   static constexpr int kBytes = ROWS * 128;
   static_assert(kParts <= 64 && kParts >= 16 && kTileK % (kEach * W) == 0, "whole loads");
+  static_assert(kEach * W % 4 == 0, "k & 3 is the same for every load of a lane");
 
   const uint8_t* base;                     // this lane's column of memory row 0 (one it has, if its own is outside)
   int64_t ld;                              // bytes between memory rows
-  const int32_t* rows;                     // GATHER: memory row of each k
-  int X, first;                            // GATHER: memory rows that there are; the first k's place in rows
-  FastDiv fd;
-  bool self;
-  int own[kLoads];                         // k within a block of this lane's loads
+  int first;                               // k within a block of this lane's first load; the next ones are kEach W on
   bool inside;
   int at[T];
-  int next[kLoads];                        // GATHER: memory rows of the block that is loaded next
 
   // How the parts of memory row k are permuted: four consecutive k reach different banks.  The inner order reads parts
   // {0, 1} and {2 T, 2 T + 1} from a tile's start at once, the outer order {0 .. 3}.
   static __device__ __forceinline__ int key(int k) {
     return !INNER ? (k & 3) << 2 : T == 4 ? (k & 3) << 1 : (k & 1) << 1 | (k & 2) << 2;
   }
+  __device__ __forceinline__ uint32_t k_of(int p, int blk) const {
+    return (uint32_t)blk * kTileK + first + p * (kEach * W);
+  }
 
   // `columns` of the tile's columns are inside
   __device__ __forceinline__ void init(int lane, int wave, int first_row, const uint8_t* start, int64_t ld_bytes,
                                        int columns) {
-    const int pos = lane % kParts;
-#pragma unroll
-    for (int p = 0; p < kLoads; ++p) own[p] = (p * W + wave) * kEach + lane / kParts;
-    // k & 3 is the same for every load, as a round of the waves' loads is a multiple of 4 rows
-    static_assert(kEach * W % 4 == 0, "one key to a lane");
-    const int part = pos ^ key(own[0]);
+    first = wave * kEach + lane / kParts;
+    const int part = lane % kParts ^ key(first);
     inside = part * 8 < columns;
     base = start + (inside ? part * 16 : 0);
     ld = ld_bytes;
@@ -206,35 +198,13 @@ struct Across {
       at[t] = (half * 8 + kr) * (ROWS * 2) + (((r >> 3) ^ key(kr)) << 4) + (r >> 2 & 1) * 8;
     }
   }
-  // itself: memory row `first + k` is read, where rows names a row inside
-  __device__ __forceinline__ void gather(const int32_t* rows_, int first_, int X_, FastDiv fd_, int K, bool itself) {
-    rows = rows_;
-    first = first_;
-    X = X_;
-    fd = fd_;
-    self = itself;
-    fetch(0, K);
+  // load p of a block: memory row `row`, -1: zeros
+  __device__ __forceinline__ void load_row(int p, int row, int wave, uint32_t lds) const {
+    part_to_lds(inside && row >= 0 ? base + row * ld : g_zero_part, lds + (p * W + wave) * 1024);
   }
-  // GATHER: memory rows of block blk
-  __device__ __forceinline__ void fetch(int blk, int K) {
-#pragma unroll
-    for (int p = 0; p < kLoads; ++p) {
-      const int k = blk * kTileK + own[p];
-      int v = k < K ? first + k : -1;
-      if (rows != nullptr && k < K) {
-        v = rows[first + k];
-        v = v < 0 ? -1 : (int32_t)fastdiv_apply((uint32_t)v, fd);
-      }
-      next[p] = v < 0 || v >= X ? -1 : self ? first + k : v;
-    }
-  }
-  __device__ __forceinline__ void load(int blk, int K, int wave, uint32_t lds) const {
-#pragma unroll
-    for (int p = 0; p < kLoads; ++p) {
-      const int k = blk * kTileK + own[p];
-      const int from = GATHER ? next[p] : k < K ? k : -1;
-      part_to_lds(inside && from >= 0 ? base + from * ld : g_zero_part, lds + (p * W + wave) * 1024);
-    }
+  __device__ __forceinline__ void load(int p, int blk, int K, int wave, uint32_t lds) const {
+    const uint32_t k = k_of(p, blk);
+    load_row(p, k < (uint32_t)K ? (int)k : -1, wave, lds);
   }
   __device__ __forceinline__ i32x4 fragment(const uint8_t* lds, int t, int s) const {
     typedef __attribute__((address_space(3))) s16x4* Ptr;
@@ -292,15 +262,17 @@ struct FourBit {
       }
     }
   }
-  __device__ __forceinline__ void load(uint8_t* lds) const {
+  __device__ __forceinline__ void settle() {
 #pragma unroll
-    for (int p = 0; p < kLoads; ++p) {
-      const int r = own + p * 32 * W;
+    for (int p = 0; p < kLoads; ++p) asm volatile("" : "+v"(raw[p]), "+v"(scale[p]));
+  }
+  // load p of the block that was fetched last
+  __device__ __forceinline__ void load(int p, uint8_t* lds) const {
+    const int r = own + p * 32 * W;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<i32x4*>(lds + r * 128 + (((half * 4 + j) ^ (r >> 1 & 7)) << 4)) =
-            four_bit_values(raw[p][j], __uint_as_float(scale[p] << 23));
-    }
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<i32x4*>(lds + r * 128 + (((half * 4 + j) ^ (r >> 1 & 7)) << 4)) =
+          four_bit_values(raw[p][j], __uint_as_float(scale[p] << 23));
   }
   __device__ __forceinline__ i32x4 fragment(const uint8_t* lds, int t, int s) const {
     return *reinterpret_cast<const i32x4*>(lds + at[s] + (INNER ? 16 : 32) * 128 * t);
@@ -320,60 +292,81 @@ struct Tile16 {
   static __device__ __forceinline__ int inner_first(int wave) { return wave % WI * (IT * 32); }
   static __device__ __forceinline__ int outer_first(int wave) { return wave / WI * (OT * 32); }
 
-  // next(blk): whatever has to be fetched before block blk is loaded
-  template <typename Next>
-  static __device__ __forceinline__ void run(Inner& in, Outer& out, int K, uint8_t* lds, f32x16 (&acc)[OT][IT],
-                                             Next next) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int blocks = (K + kTileK - 1) / kTileK;
+  // loads.issue(i, blk, stage): one of the loads.kLoads loads of block blk to LDS, in order; loads.fetch(blk): what they
+  // need in registers; loads.settle(): waits for that
+  template <typename Loads>
+  static __device__ __forceinline__ void run(const Inner& in, const Outer& out, Loads& loads, int K, uint8_t* lds,
+                                             f32x16 (&acc)[OT][IT]) {
+    constexpr int kTiles = IT * OT, kReads = IT + OT;
+    const int blocks = (K - 1) / kTileK + 1;
+    i32x4 fi[2][IT], fo[2][OT];
 #pragma unroll
     for (int o = 0; o < OT; ++o)
 #pragma unroll
       for (int t = 0; t < IT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[o][t][i] = 0.0f;
-    const uint32_t lds_at = lds_address(lds);
-    auto load = [&](int b) {
-      const uint32_t stage = (b & 1) * kStageBytes;
-      // what was fetched last is waited for first, before there are new loads that the wait would cover too
-      if constexpr (Inner::kThroughRegisters) in.load(lds + stage);
-      out.load(b, K, wave, lds_at + stage + Inner::kBytes);
-      if constexpr (!Inner::kThroughRegisters) in.load(b, K, wave, lds_at + stage);
+    // fragment u of step s of a stage
+    auto read = [&](const uint8_t* stage, int s, int u) {
+      if (u < IT) fi[s & 1][u] = in.fragment(stage, u, s);
+      else fo[s & 1][u - IT] = out.fragment(stage + Inner::kBytes, u - IT, s);
     };
-    load(0);
-    next(1);
-    for (int b = 0; b < blocks; ++b) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();                     // the block is there, and all are done with the one before
-      if (b + 1 < blocks) load(b + 1);
-      next(b + 2);
-      const uint8_t* stage = lds + (b & 1) * kStageBytes;
+    // the products of step s, the next step's fragments read under them (and after the last step of a block, which leaves
+    // its stage free, the loads of a later block)
+    auto step = [&](int s, const uint8_t* stage, int blk, uint32_t slot) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        i32x4 fi[IT];
+      for (int j = 0; j < kTiles; ++j) {
+        const int o = j / IT, t = j % IT;
+        multiply(fi[s & 1][t], fo[s & 1][o], acc[o][t]);
 #pragma unroll
-        for (int t = 0; t < IT; ++t) fi[t] = in.fragment(stage, t, s);
+        for (int u = j * kReads / kTiles; u < (j + 1) * kReads / kTiles; ++u) read(stage, (s + 1) & 3, u);
+        if (s == 3) {
 #pragma unroll
-        for (int o = 0; o < OT; ++o) {
-          const i32x4 fo = out.fragment(stage + Inner::kBytes, o, s);
-          if constexpr (MODE == kBothBf16) {
-#pragma unroll
-            for (int t = 0; t < IT; ++t) acc[o][t] = mfma_bf16(fi[t], fo, acc[o][t]);
-          } else if constexpr (MODE == kBothF16) {
-#pragma unroll
-            for (int t = 0; t < IT; ++t)
-              acc[o][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, fi[t]),
-                                                                 __builtin_bit_cast(half8, fo), acc[o][t], 0, 0, 0);
-          } else {
-            i32x4 high, low;
-            split_f16(fo, high, low);
-#pragma unroll
-            for (int t = 0; t < IT; ++t) acc[o][t] = mfma_bf16(fi[t], high, acc[o][t]);
-#pragma unroll
-            for (int t = 0; t < IT; ++t) acc[o][t] = mfma_bf16(fi[t], low, acc[o][t]);
-          }
+          for (int i = j * Loads::kLoads / kTiles; i < (j + 1) * Loads::kLoads / kTiles; ++i) loads.issue(i, blk, slot);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    auto wait = [&] {
+      // this wave's loads have arrived and its reads are done; then those of all waves
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      loads.settle();
+    };
+    loads.fetch(0);
+    loads.settle();
+#pragma unroll
+    for (int i = 0; i < Loads::kLoads; ++i) loads.issue(i, 0, 0);
+    loads.fetch(1);
+    wait();
+#pragma unroll
+    for (int i = 0; i < Loads::kLoads; ++i) loads.issue(i, 1, kStageBytes);
+    loads.fetch(2);
+#pragma unroll
+    for (int u = 0; u < kReads; ++u) read(lds, 0, u);
+    for (int b = 0; b < blocks; ++b) {
+      const uint32_t slot = (b & 1) * kStageBytes;
+      const uint8_t* stage = lds + slot;
+      step(0, stage, 0, 0);
+      step(1, stage, 0, 0);
+      step(2, stage, 0, 0);
+      wait();                              // the next block is there, and all are done with this one
+      step(3, lds + (kStageBytes - slot), b + 2, slot);
+      loads.fetch(b + 3);
+    }
+    wait();                                // none may land in LDS that is no longer this workgroup's
+  }
+
+  static __device__ __forceinline__ void multiply(i32x4 a, i32x4 b, f32x16& acc) {
+    if constexpr (MODE == kBothBf16) {
+      acc = mfma_bf16(a, b, acc);
+    } else if constexpr (MODE == kBothF16) {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), acc, 0, 0,
+                                                   0);
+    } else {
+      i32x4 high, low;
+      split_f16(b, high, low);
+      acc = mfma_bf16(a, high, acc);
+      acc = mfma_bf16(a, low, acc);
     }
   }
 
@@ -424,7 +417,7 @@ struct InnerOperand {
 };
 template <int WI, int WO, int IT>
 struct InnerOperand<WI, WO, IT, kWeightsTransposed> {
-  typedef Across<WI * IT * 32, WI * WO, IT, true, false> Type;
+  typedef Across<WI * IT * 32, WI * WO, IT, true> Type;
 };
 template <int WI, int WO, int IT>
 struct InnerOperand<WI, WO, IT, kWeights4> {
@@ -434,6 +427,33 @@ struct InnerOperand<WI, WO, IT, kWeights4> {
 template <Mode MODE, int WI, int WO, int IT, int OT, Weights FORM>
 using LinearTile = Tile16<MODE, WI, WO, IT, OT, typename InnerOperand<WI, WO, IT, FORM>::Type,
                           Along<WO * OT * 32, WI * WO, OT, false>>;
+
+// The loads of a product's tile.
+template <typename Inner, typename Outer>
+struct LinearLoads {
+  static constexpr int kLoads = Inner::kLoads + Outer::kLoads;
+  Inner& in;
+  const Outer& out;
+  uint8_t* lds;
+  uint32_t at;
+  int K, wave;
+
+  // what goes through registers first: it was waited for, and nothing that was issued since is waited for with it
+  __device__ __forceinline__ void issue(int i, int blk, uint32_t slot) const {
+    if (i < Inner::kLoads) {
+      if constexpr (Inner::kThroughRegisters) in.load(i, lds + slot);
+      else in.load(i, blk, K, wave, at + slot);
+    } else {
+      out.load(i - Inner::kLoads, blk, K, wave, at + slot + Inner::kBytes);
+    }
+  }
+  __device__ __forceinline__ void fetch(int blk) {
+    if constexpr (Inner::kThroughRegisters) in.fetch(blk, K);
+  }
+  __device__ __forceinline__ void settle() {
+    if constexpr (Inner::kThroughRegisters) in.settle();
+  }
+};
 
 template <Mode MODE, int WI, int WO, int IT, int OT, Weights FORM>
 __global__ __launch_bounds__(WI* WO * 64) void linear_tile_kernel(Linear16Args a, int32_t columns) {
@@ -454,26 +474,24 @@ __global__ __launch_bounds__(WI* WO * 64) void linear_tile_kernel(Linear16Args a
     src[r] = r < t.rows && t.g < a.G ? source_of(a.rows, a.fd_topk, a.X, t.row + r) : -1;
   __syncthreads();
   f32x16 acc[OT][IT];
-  if (t.g < a.G) {
+  if (t.g < a.G && a.X > 0) {
     typename Tile_::Inner_ in;
     typename Tile_::Outer_ out;
     const uint8_t* w = static_cast<const uint8_t*>(a.w) + (int64_t)t.g * a.N * a.C * 2;
-    out.init(lane, wave, Tile_::outer_first(wave), [&](int r) -> const uint8_t* {
-      return src[r] < 0 ? nullptr : static_cast<const uint8_t*>(a.x) + src[r] * a.ld * 2;
-    });
+    // a row that has no source reads one that is there, and is not stored
+    out.init(lane, wave, Tile_::outer_first(wave),
+             [&](int r) { return static_cast<const uint8_t*>(a.x) + max(src[r], 0) * a.ld * 2; });
     if constexpr (FORM == kWeightsTransposed) {
       in.init(lane, wave, Tile_::inner_first(wave), w + i0 * 2, (int64_t)a.C * 2, width - i0);
-      Tile_::run(in, out, K, lds, acc, [](int) {});
     } else if constexpr (FORM == kWeights) {
       in.init(lane, wave, Tile_::inner_first(wave),
               [&](int r) { return w + (int64_t)min(i0 + r, width - 1) * K * 2; });
-      Tile_::run(in, out, K, lds, acc, [](int) {});
     } else {
       const int64_t n = (int64_t)t.g * a.N + i0;
       in.init(lane, wave, Tile_::inner_first(wave), a.q + n * (K / 2), a.scale + n * (K / kScaleGroup), K, width - i0);
-      in.fetch(0, K);
-      Tile_::run(in, out, K, lds, acc, [&](int b) { in.fetch(b, K); });
     }
+    LinearLoads<typename Tile_::Inner_, typename Tile_::Outer_> loads{in, out, lds, lds_address(lds), K, wave};
+    Tile_::run(in, out, loads, K, lds, acc);
   }
   Tile_::store(acc, a.y, a.y_dtype, width, width - i0,
                [&](int r) -> int64_t { return r < t.rows ? (int64_t)(t.row + r) * width + i0 : -1; },
