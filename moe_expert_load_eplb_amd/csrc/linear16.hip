@@ -6,47 +6,84 @@ namespace eplb {
 namespace {
 
 // The loads of a weight gradient's tile: both operands lie across, and their rows of memory are those of one grouping.
-// What rows names is held from one block to the next as it is read.
-template <typename Inner, typename Outer>
+// What `rows` names is the same for the lanes of a memory row, and read into scalar registers a block ahead.
+// FAR: x spans 2^31 bytes or more.
+template <bool ROWS, bool FAR, typename Inner, typename Outer, int W>
 struct WgradLoads {
-  static constexpr int kRows = Inner::kLoads, kLoads = 2 * kRows;
-  static_assert(Inner::kEach == Outer::kEach, "a lane loads the same rows of both");
-  const Inner& in;
-  const Outer& out;
-  const int32_t* rows;                     // of the group's first row on, or NULL
+  static constexpr int kEach = Inner::kEach, kRows = Inner::kLoads, kLoads = 2 * kRows, kDirect = kLoads;
+  static_assert(kEach == Outer::kEach, "a lane loads the same rows of both");
+  typedef const __attribute__((address_space(4))) int32_t* Scalars;
+  Inner in;
+  Outer out;
+  const int32_t* rows;                     // ROWS: of the group's first row on
   FastDiv topk;
-  int X, first;                            // rows of x, the group's first row
+  uint32_t X;                              // rows of x
   uint32_t at;
-  int K, wave;
-  int32_t named[kRows];
+  int K, wave, sub;                        // sub: which of the kEach memory rows of a load this lane is in
+  uint32_t column[Inner::kKinds];          // ROWS: where in a row of x this lane's parts lie
+  int32_t next[kRows][kEach];
+  uint32_t now[kRows][kEach];              // ROWS: offset (FAR: index) of the row of x, or outside
+  i32x4 from_x, from_dy;
 
   __device__ __forceinline__ void fetch(int blk) {
+    if (!ROWS) return;
 #pragma unroll
-    for (int p = 0; p < kRows; ++p) {
-      const uint32_t k = in.k_of(p, blk);
-      named[p] = rows == nullptr || k >= (uint32_t)K ? 0 : rows[k];
+    for (int p = 0; p < kRows; ++p)
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const uint32_t k = (uint32_t)blk * kTileK + (p * W + wave) * kEach + j;
+        next[p][j] = ((Scalars)rows)[k < (uint32_t)K ? k : (uint32_t)K - 1];
+      }
+  }
+  __device__ __forceinline__ void begin(int blk) {
+    from_dy = out.describe_block(blk, K);
+    if (!ROWS) {
+      from_x = in.describe_block(blk, K);
+      return;
     }
-  }
-  __device__ __forceinline__ void settle() {
 #pragma unroll
-    for (int p = 0; p < kRows; ++p) asm volatile("" : "+v"(named[p]));
+    for (int p = 0; p < kRows; ++p)
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const uint32_t k = (uint32_t)blk * kTileK + (p * W + wave) * kEach + j;
+        const uint32_t row = fastdiv_apply((uint32_t)next[p][j], topk) | (uint32_t)(next[p][j] >> 31);
+        now[p][j] = row < X && k < (uint32_t)K ? (FAR ? row : row * in.ld) : kOutside;
+      }
   }
-  __device__ __forceinline__ void issue(int i, int blk, uint32_t slot) const {
+  // a row of nothing counts for nothing, whatever dy holds there
+  __device__ __forceinline__ void issue(int i, uint32_t slot) const {
     const int p = i >> 1;
-    const uint32_t k = in.k_of(p, blk);
-    const int32_t row = (int32_t)(first + k);
-    int32_t from = rows == nullptr ? row : named[p] < 0 ? -1 : (int32_t)fastdiv_apply((uint32_t)named[p], topk);
-    if (k >= (uint32_t)K || from >= X) from = -1;
-    if (i & 1) in.load_row(p, from, wave, at + slot);
-    else out.load_row(p, from < 0 ? -1 : row, wave, at + slot + Inner::kBytes);   // a row of nothing counts for nothing
+    const uint32_t to = at + slot + (i & 1 ? 0 : Inner::kBytes);
+    if (!ROWS) {
+      if (i & 1) in.load(p, from_x, wave, to);
+      else out.load(p, from_dy, wave, to);
+      return;
+    }
+    uint32_t row = now[p][0];
+#pragma unroll
+    for (int j = 1; j < kEach; ++j) {
+      uint32_t other = now[p][j];
+      asm("" : "+s"(other));               // not an index into memory
+      row = sub == j ? other : row;
+    }
+    if (i & 1) {
+      const uint32_t c = column[p % Inner::kKinds];
+      if (!FAR) part_to_lds(from_x, row + c, 0, to + (p * W + wave) * 1024);
+      else part_to_lds((row | c) & kOutside ? g_zero_part : in.base + (uint64_t)row * in.ld + c, to + (p * W + wave) * 1024);
+    } else {
+      part_to_lds(from_dy, out.offset[p % Outer::kKinds] | (row & kOutside), p * (kEach * W) * out.ld,
+                  to + (p * W + wave) * 1024);
+    }
   }
 };
 
-template <Mode MODE, int WI, int WO, int IT, int OT>
+template <Mode MODE, int M, bool ROWS, bool FAR, int WI, int WO, int IT, int OT>
 __global__ __launch_bounds__(WI* WO * 64) void wgrad16_kernel(Wgrad16Args a, int32_t ni, int32_t no) {
-  typedef Across<WI * IT * 32, WI * WO, IT, true> Inner;
-  typedef Across<WO * OT * 32, WI * WO, OT, false> Outer;
-  typedef Tile16<MODE, WI, WO, IT, OT, Inner, Outer> Tile_;
+  typedef Across<WI * IT * 32, WI * WO, M> Inner;
+  typedef Across<WO * OT * 32, WI * WO, M> Outer;
+  typedef AcrossFragments<WI * IT * 32, M> InnerFragments;
+  typedef AcrossFragments<WO * OT * 32, M> OuterFragments;
+  typedef Tile16<MODE, M, WI, WO, IT, OT, InnerFragments, OuterFragments> Tile_;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t id = die_order(blockIdx.x, gridDim.x);
@@ -55,77 +92,94 @@ __global__ __launch_bounds__(WI* WO * 64) void wgrad16_kernel(Wgrad16Args a, int
   band_order(id - g * (ni * no), no, ni, row, column);
   const int i0 = column * Tile_::kInner, o0 = row * Tile_::kOuter;
   const Span span = group_span(a.offsets, g, a.G, a.R);
-  const int K = span.hi > span.lo ? span.hi - span.lo : 0;
-  f32x16 acc[OT][IT];
+  int K = span.hi > span.lo ? span.hi - span.lo : 0;
+  if (!ROWS && K > a.X - span.lo) K = a.X > span.lo ? (int)(a.X - span.lo) : 0;    // rows that x does not have
+  if (a.X == 0) K = 0;
+  typename Tile_::Sum acc[Tile_::kO][Tile_::kI];
   if (K > 0) {
-    Inner in;
-    Outer out;
-    in.init(lane, wave, Tile_::inner_first(wave), static_cast<const uint8_t*>(a.x) + i0 * 2, a.ld * 2, a.C - i0);
-    out.init(lane, wave, Tile_::outer_first(wave), static_cast<const uint8_t*>(a.dy) + o0 * 2, a.dy_ld * 2, a.N - o0);
-    WgradLoads<Inner, Outer> loads{in, out, a.rows == nullptr ? nullptr : a.rows + span.lo, a.fd_topk, (int)a.X, span.lo,
-                                   lds_address(lds), K, wave};
+    WgradLoads<ROWS, FAR, Inner, Outer, WI * WO> loads;
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + i0 * 2;
+    loads.in.init(lane, wave, ROWS ? x : x + span.lo * a.ld * 2, a.ld * 2, a.C - i0);
+    loads.out.init(lane, wave, static_cast<const uint8_t*>(a.dy) + (span.lo * a.dy_ld + o0) * 2, a.dy_ld * 2, a.N - o0);
+    loads.rows = ROWS ? a.rows + span.lo : nullptr;
+    loads.topk = a.fd_topk;
+    loads.X = (uint32_t)a.X;
+    loads.at = lds_address(lds);
+    loads.K = K;
+    loads.wave = wave;
+    loads.sub = lane / Inner::kParts;
+    if (ROWS) {
+#pragma unroll
+      for (int i = 0; i < Inner::kKinds; ++i) loads.column[i] = Inner::column(lane, wave, i, a.C - i0);
+      loads.from_x = describe(x, (uint64_t)a.X * a.ld * 2);
+    }
+    InnerFragments in;
+    OuterFragments out;
+    in.init(lane, Tile_::inner_first(wave));
+    out.init(lane, Tile_::outer_first(wave));
+    Tile_::start(loads);
     Tile_::run(in, out, loads, K, lds, acc);
   }
-  Tile_::store(acc, a.dw, a.dw_dtype, a.C, a.C - i0,
+  Tile_::store(acc, lds, a.dw, a.dw_dtype, a.C, a.C - i0,
                [&](int r) -> int64_t { return o0 + r < a.N ? ((int64_t)g * a.N + o0 + r) * a.C + i0 : -1; },
                [&](int) { return K > 0; });
 }
-
-// Tiles of 256 x 256 (four waves of 128 x 128) and of 128 x 128 (four of 64 x 64).
-constexpr int kWI = 2, kWO = 2;
-constexpr int kLarge = 256, kSmall = 128;
-
-int64_t tile_rows(int64_t R, int32_t G, int tile) {
+int64_t small_blocks(int64_t R, int64_t width, int32_t G) {
   // every group adds at most one tile that is not full, and a tile has a row
-  return std::min(R, R / tile + G) + 2;
+  return (std::min(R, R / 128 + G) + 2) * ceil_div(width, 128);
+}
+
+int64_t large_blocks(int64_t R, int64_t width, int32_t G) {
+  const int64_t columns = ceil_div(width, 256);
+  return R / 256 * columns + kUnits / 2 + 2 * columns * std::min(R, (int64_t)G + 2);
 }
 
 bool large_linear(int64_t R, int64_t width, int32_t G) {
-  return R >= 128 * (int64_t)G && (R / kLarge + G / 2) * ceil_div(width, kLarge) >= 128;
-}
-
-bool large_wgrad(int64_t N, int64_t C, int32_t G) { return G * ceil_div(N, kLarge) * ceil_div(C, kLarge) >= 128; }
-
-template <Mode MODE, int T, Weights FORM>
-hipError_t launch(const Linear16Args& a, hipStream_t stream) {
-  typedef LinearTile<MODE, kWI, kWO, T, T, FORM> Tile_;
-  const int64_t width = FORM == kWeightsTransposed ? a.C : a.N, columns = ceil_div(width, Tile_::kInner);
-  linear_tile_kernel<MODE, kWI, kWO, T, T, FORM>
-      <<<dim3((unsigned)(tile_rows(a.R, a.G, Tile_::kOuter) * columns)), dim3(Tile_::kThreads), Tile_::kLdsBytes,
-         stream>>>(a, (int32_t)columns);
-  return hipGetLastError();
+  return R >= 128 * (int64_t)G && (R / 256 + G / 2) * ceil_div(width, 256) >= 128;
 }
 
 template <Mode MODE, Weights FORM>
 hipError_t launch_form(const Linear16Args& a, hipStream_t stream) {
-  return large_linear(a.R, FORM == kWeightsTransposed ? a.C : a.N, a.G) ? launch<MODE, 4, FORM>(a, stream)
-                                                                        : launch<MODE, 2, FORM>(a, stream);
-}
-
-template <Mode MODE, int T>
-hipError_t launch_wgrad(const Wgrad16Args& a, hipStream_t stream) {
-  constexpr int kTile = 64 * T;
-  const int64_t ni = ceil_div(a.C, kTile), no = ceil_div(a.N, kTile);
-  wgrad16_kernel<MODE, kWI, kWO, T, T><<<dim3((unsigned)(a.G * ni * no)), dim3(256), 2 * 2 * kTile * 128, stream>>>(
-      a, (int32_t)ni, (int32_t)no);
+  const int64_t width = FORM == kWeightsTransposed ? a.C : a.N;
+  const bool far = a.X * a.ld * 2 >= (int64_t)kOutside;
+  if (!far && large_linear(a.R, width, a.G)) {
+    linear_large_kernel<MODE, FORM><<<dim3((unsigned)large_blocks(a.R, width, a.G)), dim3(512),
+                                      2 * 2 * 256 * 128, stream>>>(a, (int32_t)ceil_div(width, 256));
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)small_blocks(a.R, width, a.G));
+  const int32_t columns = (int32_t)ceil_div(width, 128);
+  if (far) linear_small_kernel<MODE, FORM, true><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
+  else linear_small_kernel<MODE, FORM, false><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
   return hipGetLastError();
 }
 
-template <Mode MODE>
+bool large_wgrad(int64_t N, int64_t C, int32_t G) { return G * ceil_div(N, 256) * ceil_div(C, 256) >= 128; }
+
+template <Mode MODE, bool ROWS>
 hipError_t launch_wgrad_form(const Wgrad16Args& a, hipStream_t stream) {
-  return large_wgrad(a.N, a.C, a.G) ? launch_wgrad<MODE, 4>(a, stream) : launch_wgrad<MODE, 2>(a, stream);
+  const bool far = ROWS && a.X * a.ld * 2 >= (int64_t)kOutside;
+  if (!far && large_wgrad(a.N, a.C, a.G)) {
+    const int64_t ni = ceil_div(a.C, 256), no = ceil_div(a.N, 256);
+    wgrad16_kernel<MODE, 16, ROWS, false, 4, 2, 2, 4>
+        <<<dim3((unsigned)(a.G * ni * no)), dim3(512), 2 * 2 * 256 * 128, stream>>>(a, (int32_t)ni, (int32_t)no);
+  } else {
+    const int64_t ni = ceil_div(a.C, 128), no = ceil_div(a.N, 128);
+    const dim3 grid((unsigned)(a.G * ni * no));
+    if (far) wgrad16_kernel<MODE, 16, ROWS, ROWS, 2, 2, 2, 2><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, ni, no);
+    else wgrad16_kernel<MODE, 16, ROWS, false, 2, 2, 2, 2><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, ni, no);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t linear16_blocks(int64_t R, int64_t outputs, int64_t, int32_t G, bool) {
-  const int tile = large_linear(R, outputs, G) ? kLarge : kSmall;
-  return tile_rows(R, G, tile) * ceil_div(outputs, tile);
+  return std::max(small_blocks(R, outputs, G), large_linear(R, outputs, G) ? large_blocks(R, outputs, G) : 0);
 }
 
 int64_t wgrad16_blocks(int64_t, int64_t N, int64_t C, int32_t G) {
-  const int tile = large_wgrad(N, C, G) ? kLarge : kSmall;
-  return (int64_t)G * ceil_div(N, tile) * ceil_div(C, tile);
+  return (int64_t)G * ceil_div(N, 128) * ceil_div(C, 128);       // of the smaller tiles, which every size may get
 }
 
 hipError_t launch_linear16(const Linear16Args& a, bool transpose, hipStream_t stream) {
@@ -136,7 +190,9 @@ hipError_t launch_linear16(const Linear16Args& a, bool transpose, hipStream_t st
 }
 
 hipError_t launch_wgrad16(const Wgrad16Args& a, hipStream_t stream) {
-  return a.dtype == kF16 ? launch_wgrad_form<kBothF16>(a, stream) : launch_wgrad_form<kBothBf16>(a, stream);
+  if (a.dtype == kF16)
+    return a.rows != nullptr ? launch_wgrad_form<kBothF16, true>(a, stream) : launch_wgrad_form<kBothF16, false>(a, stream);
+  return a.rows != nullptr ? launch_wgrad_form<kBothBf16, true>(a, stream) : launch_wgrad_form<kBothBf16, false>(a, stream);
 }
 
 }  // namespace eplb

@@ -10,16 +10,19 @@ namespace eplb {
 
 namespace {
 
-constexpr int kWI = 2, kWO = 2, kIT = 2, kOT = 2;
 constexpr int kTile = 128;
 
-template <Mode MODE>
+template <Mode MODE, bool FAR>
 hipError_t launch(const Linear16Args& a, hipStream_t stream) {
-  typedef LinearTile<MODE, kWI, kWO, kIT, kOT, kWeights4> Tile_;
-  linear_tile_kernel<MODE, kWI, kWO, kIT, kOT, kWeights4>
-      <<<dim3((unsigned)linear4_blocks(a.R, a.N, a.C, a.G)), dim3(Tile_::kThreads), Tile_::kLdsBytes, stream>>>(
+  linear_small_kernel<MODE, kWeights4, FAR>
+      <<<dim3((unsigned)linear4_blocks(a.R, a.N, a.C, a.G)), dim3(256), 2 * 2 * 128 * 128, stream>>>(
           a, (int32_t)ceil_div(a.N, kTile));
   return hipGetLastError();
+}
+
+template <Mode MODE>
+hipError_t launch_form(const Linear16Args& a, hipStream_t stream) {
+  return a.X * a.ld * 2 >= (int64_t)kOutside ? launch<MODE, true>(a, stream) : launch<MODE, false>(a, stream);
 }
 
 }  // namespace
@@ -31,7 +34,7 @@ int64_t linear4_blocks(int64_t R, int64_t N, int64_t, int32_t G) {
 
 hipError_t launch_linear4(const Linear16Args& a, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
-  return a.dtype == kF16 ? launch<kSplit>(a, stream) : launch<kBothBf16>(a, stream);
+  return a.dtype == kF16 ? launch_form<kSplit>(a, stream) : launch_form<kBothBf16>(a, stream);
 }
 
 }  // namespace eplb

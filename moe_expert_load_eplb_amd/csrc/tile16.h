@@ -2,10 +2,10 @@
 // products and the weight gradient have in common.
 //
 // out[o][i] = sum over k of O(o, k) * I(i, k).  A workgroup of WI x WO waves
-// computes (WI IT 32) inner x (WO OT 32) outer values, a wave IT x OT tiles of
-// 32 x 32.  The inner index is contiguous in the output; its operand is the
-// matrix instruction's first, whose rows are taken in an order that leaves a
-// lane with 16 consecutive inner values of one outer row for every tile.
+// computes (WI IT 32) inner x (WO OT 32) outer values, a wave IT 32 x OT 32 of
+// them, as tiles of the matrix instruction (M x M).  The inner index is
+// contiguous in the output; its operand is the matrix instruction's first, so
+// that a lane ends up with runs of four inner values of one outer row.
 //
 // Operands go from memory to LDS without passing through registers, a block of
 // 64 of k at a time, into one of two stages.  An operand lies in memory (and in
@@ -13,9 +13,12 @@
 //   along    a row of the operand is contiguous in k: 128 bytes of a block for
 //            each row, its eight 16-byte parts permuted by bits 1 to 3 of the row
 //   across   k runs over rows of memory: 2 ROWS bytes for each k, the 16-byte
-//            parts permuted by the lowest bits of k; fragments are read with
-//            the transposing LDS read
+//            parts permuted by bits of k; fragments are read with the transposing
+//            LDS read
 // in both so that the lanes of a read reach all banks.
+//
+// The loads take a buffer descriptor and 32-bit offsets: what is past the
+// descriptor's end, or marked by the offset's highest bit, arrives as zeros.
 #pragma once
 
 #include "experts_device.h"
@@ -29,13 +32,31 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTileK = 64;                 // k of a block
+constexpr uint32_t kOutside = 0x80000000u; // an offset that no descriptor reaches
 
-__device__ __attribute__((aligned(16))) static const uint8_t g_zero_part[16] = {};   // read in place of what lies outside
+__device__ __attribute__((aligned(16))) static const uint8_t g_zero_part[16] = {};
+
+// A descriptor of `bytes` bytes (2^31 at most) from p on.  The same for the wave.
+__device__ __forceinline__ i32x4 describe(const void* p, uint64_t bytes) {
+  const uint64_t at = (uint64_t)p;
+  i32x4 d;
+  d[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+  d[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32));
+  d[2] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(bytes < kOutside ? bytes : kOutside));
+  d[3] = 0x00020000;                       // raw, 32-bit elements
+  return d;
+}
 
 // 16 bytes of every lane to 1 KiB of LDS from `to` (the same for the wave).  Written out, as the compiler lets the
 // transposing reads wait for every such load in flight, whatever part of LDS it goes to: the waits for these loads are
 // the tile's own.  No register is written but M0, which nothing else in these kernels uses (it cannot be named as
 // clobbered) and which is read two instructions after it is set.
+__device__ __forceinline__ void part_to_lds(i32x4 from, uint32_t offset, uint32_t shift, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(offset), "s"(from),
+               "s"(shift));
+}
+
+// The same from an address of each lane.
 __device__ __forceinline__ void part_to_lds(const uint8_t* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from));
 }
@@ -48,10 +69,6 @@ __device__ __forceinline__ uint32_t lds_address(uint8_t* p) {
 // What the two operands hold.  kSplit: the first bfloat16, the second half precision, which is taken as two bfloat16
 // values that sum to it exactly (11 significant bits are 8 and 3).
 enum Mode { kBothBf16, kBothF16, kSplit };
-
-__device__ __forceinline__ f32x16 mfma_bf16(i32x4 a, i32x4 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
 
 // Eight half-precision values as bfloat16: the nearest ones, and what they leave (0 of an infinity).
 __device__ __forceinline__ void split_f16(i32x4 v, i32x4& high, i32x4& low) {
@@ -68,41 +85,6 @@ __device__ __forceinline__ void split_f16(i32x4 v, i32x4& high, i32x4& low) {
   low = __builtin_bit_cast(i32x4, l);
 }
 
-// Four consecutive values of one output row; `left` of them are inside.
-__device__ __forceinline__ void store_four(void* p, int32_t dtype, int64_t at, int left, bool vec, const float* v) {
-  if (vec && left >= 4) {
-    if (dtype == kF32) {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(p) + at) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-      u16 h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = dtype == kBf16 ? float_to_bf16(v[j]) : float_to_f16(v[j]);
-      *reinterpret_cast<uint2*>(static_cast<u16*>(p) + at) =
-          uint2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (j < left) store_float(p, dtype, at + j, v[j]);
-}
-
-// Eight consecutive values of one output row.
-__device__ __forceinline__ void store_eight(void* p, int32_t dtype, int64_t at, int left, int64_t width,
-                                            const float* v) {
-  if (dtype != kF32 && left >= 8 && width % 8 == 0) {
-    u16 h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = dtype == kBf16 ? float_to_bf16(v[j]) : float_to_f16(v[j]);
-    *reinterpret_cast<uint4*>(static_cast<u16*>(p) + at) =
-        uint4{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
-              h[6] | (uint32_t)h[7] << 16};
-    return;
-  }
-  store_four(p, dtype, at, left, width % 4 == 0, v);
-  if (left > 4) store_four(p, dtype, at + 4, left - 4, width % 4 == 0, v + 4);
-}
-
 // Eight 4-bit values times a power of two as bfloat16.  Of the scale only the exponent counts; all bits of it set (255
 // of a scale byte): NaN.
 __device__ __forceinline__ i32x4 four_bit_values(int codes, float scale) {
@@ -114,51 +96,118 @@ __device__ __forceinline__ i32x4 four_bit_values(int codes, float scale) {
   return v;
 }
 
+// ---------------------------------------------------------------- the matrix instruction
+template <int M>
+struct Matrix;
+
+template <>
+struct Matrix<32> {
+  typedef f32x16 Sum;
+  static constexpr int kK = 16;            // k of an instruction: lane / M takes eight of them
+  static __device__ __forceinline__ Sum bf16(i32x4 a, i32x4 b, Sum c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+  }
+  static __device__ __forceinline__ Sum f16(i32x4 a, i32x4 b, Sum c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  }
+  // first of the four inner values in elements 4 q .. 4 q + 3 of a sum
+  static __device__ __forceinline__ int four(int lane, int q) { return 8 * q + 4 * (lane >> 5); }
+};
+
+template <>
+struct Matrix<16> {
+  typedef f32x4 Sum;
+  static constexpr int kK = 32;
+  static __device__ __forceinline__ Sum bf16(i32x4 a, i32x4 b, Sum c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+  }
+  static __device__ __forceinline__ Sum f16(i32x4 a, i32x4 b, Sum c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int four(int lane, int) { return 4 * (lane >> 4); }
+};
+
 // ---------------------------------------------------------------- operands
-// ROWS rows of an operand loaded by W waves; T tiles of 32 rows to a wave;
-// INNER: the rows of a wave in the inner operand's order.
+// ROWS rows of an operand loaded by W waves.
 
-// The row of the operand, counted from the wave's first, that index `a` (0 .. 31) of tile t stands for.
-template <int T, bool INNER>
-__device__ __forceinline__ int tile_row(int a, int t) {
-  return INNER ? (a >> 2 & 1) * (16 * T) + 16 * t + (a >> 3) * 4 + (a & 3) : t * 32 + a;
-}
+// How the parts of row r are permuted where k lies along: two rows make one turn of the banks.
+__device__ __forceinline__ int along_key(int r) { return r >> 1 & 7; }
 
-template <int ROWS, int W, int T, bool INNER>
+// Where the fragments of a wave lie, in a stage of rows along k.
+template <int M>
+struct AlongFragments {
+  static constexpr int kSteps = kTileK / Matrix<M>::kK;
+  int at[kSteps];
+  __device__ __forceinline__ void init(int lane, int first_row) {
+    const int r = first_row + lane % M;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) at[s] = r * 128 + (((s * (Matrix<M>::kK / 8) + lane / M) ^ along_key(r)) << 4);
+  }
+  __device__ __forceinline__ i32x4 read(const uint8_t* lds, int t, int s) const {
+    return *reinterpret_cast<const i32x4*>(lds + at[s] + M * 128 * t);
+  }
+};
+
+// Rows that lie one after the other.
+template <int ROWS, int W>
 struct Along {
   static constexpr bool kThroughRegisters = false;
   static constexpr int kLoads = ROWS / 8 / W;
   static constexpr int kBytes = ROWS * 128;
   static_assert(ROWS % (8 * W) == 0 && W % 2 == 0, "whole loads, and the same part of every load's rows");
 
-  const uint8_t* row[kLoads];              // where this lane's part of block 0 lies
+  i32x4 from;
+  uint32_t offset, step;                   // of this lane's part, from one load's rows to the next one's
   int part;                                // its first k within a block
-  int at[4];                               // where the four steps' parts of this lane's row lie in LDS
 
-  // start(r): where row r of the tile begins (any valid row for one that is not stored)
-  template <typename Start>
-  __device__ __forceinline__ void init(int lane, int wave, int first, Start start) {
-    part = ((lane & 7) ^ ((wave * 8 + (lane >> 3)) >> 1 & 7)) * 8;
-#pragma unroll
-    for (int p = 0; p < kLoads; ++p) {
-      row[p] = start((p * W + wave) * 8 + (lane >> 3)) + part * 2;
-    }
-    const int r = tile_row<T, INNER>(lane & 31, 0);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) at[s] = (first + r) * 128 + (((s * 2 + (lane >> 5)) ^ (r >> 1 & 7)) << 4);
+  // `rows` rows of `ld` bytes from `start` on; those past them read as zeros
+  __device__ __forceinline__ void init(int lane, int wave, const uint8_t* start, uint32_t ld, int rows) {
+    from = describe(start, (uint64_t)min(rows, ROWS) * ld);
+    part = ((lane & 7) ^ along_key(wave * 8 + (lane >> 3))) * 8;
+    offset = (wave * 8 + (lane >> 3)) * ld + part * 2;
+    step = W * 8 * ld;
   }
   // load p of block blk, of K elements in all, to LDS
   __device__ __forceinline__ void load(int p, int blk, int K, int wave, uint32_t lds) const {
-    const bool in = blk * kTileK + part < K;
-    part_to_lds(in ? row[p] + (int64_t)blk * 128 : g_zero_part, lds + (p * W + wave) * 1024);
+    part_to_lds(from, part < K - blk * kTileK ? offset : kOutside, p * step + blk * 128, lds + (p * W + wave) * 1024);
   }
-  __device__ __forceinline__ i32x4 fragment(const uint8_t* lds, int t, int s) const {
-    return *reinterpret_cast<const i32x4*>(lds + at[s] + (INNER ? 16 : 32) * 128 * t);
+};
+
+// Rows that lie anywhere.  FAR: they span 2^31 bytes or more.
+template <int ROWS, int W, bool FAR>
+struct Gathered {
+  static constexpr int kLoads = ROWS / 8 / W;
+  static constexpr int kBytes = ROWS * 128;
+  static_assert(ROWS % (8 * W) == 0 && W % 2 == 0, "whole loads, and the same part of every load's rows");
+
+  i32x4 from;
+  uint32_t offset[FAR ? 1 : kLoads];
+  const uint8_t* row[FAR ? kLoads : 1];
+  int part;
+
+  // row(r): the row of memory that row r of the tile is, or -1 (what is read for it is not used)
+  template <typename Row>
+  __device__ __forceinline__ void init(int lane, int wave, const uint8_t* start, int64_t ld, int64_t rows, Row of) {
+    part = ((lane & 7) ^ along_key(wave * 8 + (lane >> 3))) * 8;
+    if (!FAR) from = describe(start, rows * ld);
+#pragma unroll
+    for (int p = 0; p < kLoads; ++p) {
+      const int32_t r = of((p * W + wave) * 8 + (lane >> 3));
+      if (FAR) row[p] = start + max(r, 0) * ld + part * 2;
+      else offset[p] = r < 0 ? kOutside : (uint32_t)r * (uint32_t)ld + part * 2;
+    }
+  }
+  __device__ __forceinline__ void load(int p, int blk, int K, int wave, uint32_t lds) const {
+    const bool in = part < K - blk * kTileK;
+    if (FAR) part_to_lds(in ? row[p] + (int64_t)blk * 128 : g_zero_part, lds + (p * W + wave) * 1024);
+    else part_to_lds(from, offset[p] | (in ? 0 : kOutside), blk * 128, lds + (p * W + wave) * 1024);
   }
 };
 
 // Memory rows are k; rows of the operand are columns there.
-template <int ROWS, int W, int T, bool INNER>
+template <int ROWS, int W, int M>
 struct Across {
   static constexpr bool kThroughRegisters = false;
   static constexpr int kParts = ROWS / 8;            // 16-byte parts of a memory row
@@ -166,49 +215,59 @@ struct Across {
   static constexpr int kLoads = kTileK / kEach / W;
   static constexpr int kBytes = ROWS * 128;
   static_assert(kParts <= 64 && kParts >= 16 && kTileK % (kEach * W) == 0, "whole loads");
-  static_assert(kEach * W % 4 == 0, "k & 3 is the same for every load of a lane");
+  // a lane's loads are kEach W memory rows apart: permutations that they have
+  static constexpr int kKinds = M == 32 || kEach * W % 16 == 0 ? 1 : 2;
+  static_assert(kEach * W % (M == 32 ? 4 : 8) == 0, "not more of them");
 
-  const uint8_t* base;                     // this lane's column of memory row 0 (one it has, if its own is outside)
-  int64_t ld;                              // bytes between memory rows
-  int first;                               // k within a block of this lane's first load; the next ones are kEach W on
-  bool inside;
-  int at[T];
+  const uint8_t* base;                     // column 0 of the tile in memory row 0
+  uint32_t ld;                             // bytes between memory rows
+  uint32_t offset[kKinds];                 // of this lane's part of load p, from the first memory row of load 0's on
 
-  // How the parts of memory row k are permuted: four consecutive k reach different banks.  The inner order reads parts
-  // {0, 1} and {2 T, 2 T + 1} from a tile's start at once, the outer order {0 .. 3}.
-  static __device__ __forceinline__ int key(int k) {
-    return !INNER ? (k & 3) << 2 : T == 4 ? (k & 3) << 1 : (k & 1) << 1 | (k & 2) << 2;
-  }
-  __device__ __forceinline__ uint32_t k_of(int p, int blk) const {
-    return (uint32_t)blk * kTileK + first + p * (kEach * W);
-  }
+  // How the parts of memory row k are permuted.  What 32 lanes read at once is four consecutive k of 64 bytes (M = 32), or
+  // twice four, eight apart, of 32 bytes.
+  static __device__ __forceinline__ int key(int k) { return M == 32 ? (k & 3) << 2 : (k & 3) << 1 | (k & 8); }
 
   // `columns` of the tile's columns are inside
-  __device__ __forceinline__ void init(int lane, int wave, int first_row, const uint8_t* start, int64_t ld_bytes,
-                                       int columns) {
-    first = wave * kEach + lane / kParts;
-    const int part = lane % kParts ^ key(first);
-    inside = part * 8 < columns;
-    base = start + (inside ? part * 16 : 0);
-    ld = ld_bytes;
-    const int kr = lane >> 2 & 3, half = lane >> 5, c = (lane >> 4 & 1) * 4 + (lane & 3);
+  __device__ __forceinline__ void init(int lane, int wave, const uint8_t* start, int64_t ld_bytes, int columns) {
+    base = start;
+    ld = (uint32_t)ld_bytes;
+    const int k = wave * kEach + lane / kParts;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int r = first_row + tile_row<T, INNER>(c * 4, t);      // four consecutive columns
-      at[t] = (half * 8 + kr) * (ROWS * 2) + (((r >> 3) ^ key(kr)) << 4) + (r >> 2 & 1) * 8;
+    for (int i = 0; i < kKinds; ++i) {
+      const uint32_t c = column(lane, wave, i, columns);
+      offset[i] = c == kOutside ? c : k * ld + c;
     }
   }
-  // load p of a block: memory row `row`, -1: zeros
-  __device__ __forceinline__ void load_row(int p, int row, int wave, uint32_t lds) const {
-    part_to_lds(inside && row >= 0 ? base + row * ld : g_zero_part, lds + (p * W + wave) * 1024);
+  // where in a memory row this lane's part of load p lies
+  static __device__ __forceinline__ uint32_t column(int lane, int wave, int p, int columns) {
+    const int part = lane % kParts ^ key((p * W + wave) * kEach + lane / kParts);
+    return part * 8 < columns ? part * 16 : kOutside;
   }
-  __device__ __forceinline__ void load(int p, int blk, int K, int wave, uint32_t lds) const {
-    const uint32_t k = k_of(p, blk);
-    load_row(p, k < (uint32_t)K ? (int)k : -1, wave, lds);
+  // of block blk, with memory rows up to K
+  __device__ __forceinline__ i32x4 describe_block(int blk, int K) const {
+    const uint32_t k = (uint32_t)blk * kTileK;
+    return describe(base + (uint64_t)k * ld, k < (uint32_t)K ? (uint64_t)((uint32_t)K - k) * ld : 0);
   }
-  __device__ __forceinline__ i32x4 fragment(const uint8_t* lds, int t, int s) const {
+  __device__ __forceinline__ void load(int p, const i32x4& from, int wave, uint32_t lds) const {
+    part_to_lds(from, offset[p % kKinds], p * (kEach * W) * ld, lds + (p * W + wave) * 1024);
+  }
+};
+
+template <int ROWS, int M>
+struct AcrossFragments {
+  static constexpr int kKinds = M == 32 ? 4 : 8;     // tiles that the permutation tells apart
+  int at[kKinds];
+  __device__ __forceinline__ void init(int lane, int first_row) {
+    const int k = lane / M * 8 + (lane >> 2 & 3), c = (lane % M >> 4) * 16 + (lane & 3) * 4;   // four consecutive columns
+#pragma unroll
+    for (int t = 0; t < kKinds; ++t) {
+      const int r = first_row + t * M + c;
+      at[t] = k * (ROWS * 2) + (((r >> 3) ^ Across<ROWS, 16, M>::key(k)) << 4) + (r >> 2 & 1) * 8;
+    }
+  }
+  __device__ __forceinline__ i32x4 read(const uint8_t* lds, int t, int s) const {
     typedef __attribute__((address_space(3))) s16x4* Ptr;
-    const uint8_t* from = lds + at[t] + s * 16 * (ROWS * 2);
+    const uint8_t* from = lds + at[t] + s * Matrix<M>::kK * (ROWS * 2);
     union {
       s16x4 h[2];
       i32x4 v;
@@ -220,8 +279,8 @@ struct Across {
 };
 
 // An operand of 4-bit values along k, its blocks of 32 scaled by powers of two: from memory to registers a block ahead,
-// and to LDS as bfloat16 (exactly), in the layout of Along.
-template <int ROWS, int W, int T, bool INNER>
+// and to LDS as bfloat16 (exactly), in the layout of rows along k.
+template <int ROWS, int W>
 struct FourBit {
   static constexpr bool kThroughRegisters = true;
   static constexpr int kLoads = ROWS / 32 / W;       // of 32 rows and both halves of a block
@@ -230,13 +289,12 @@ struct FourBit {
 
   const uint8_t* codes;                    // this lane's part of block 0 of its first row
   const uint8_t* scales;
-  int32_t ld_codes, ld_scales;             // bytes from one load's row to the next one's, which is 32 W rows on
+  int32_t ld_codes, ld_scales;
   int half, own, last;                     // half of a block, first row, last row inside
   i32x4 raw[kLoads];
   uint32_t scale[kLoads];
-  int at[4];
 
-  __device__ __forceinline__ void init(int lane, int wave, int first, const uint8_t* q, const uint8_t* s, int C, int n) {
+  __device__ __forceinline__ void init(int lane, int wave, const uint8_t* q, const uint8_t* s, int C, int n) {
     half = lane & 1;
     own = wave * 32 + (lane >> 1);
     last = n - 1;
@@ -244,9 +302,6 @@ struct FourBit {
     scales = s + half;
     ld_codes = C / 2;
     ld_scales = C / kScaleGroup;
-    const int r = tile_row<T, INNER>(lane & 31, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) at[j] = (first + r) * 128 + (((j * 2 + (lane >> 5)) ^ (r >> 1 & 7)) << 4);
   }
   // block blk of K elements in all; past the end of a row: zeros
   __device__ __forceinline__ void fetch(int blk, int K) {
@@ -271,128 +326,196 @@ struct FourBit {
     const int r = own + p * 32 * W;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<i32x4*>(lds + r * 128 + (((half * 4 + j) ^ (r >> 1 & 7)) << 4)) =
+      *reinterpret_cast<i32x4*>(lds + r * 128 + (((half * 4 + j) ^ along_key(r)) << 4)) =
           four_bit_values(raw[p][j], __uint_as_float(scale[p] << 23));
-  }
-  __device__ __forceinline__ i32x4 fragment(const uint8_t* lds, int t, int s) const {
-    return *reinterpret_cast<const i32x4*>(lds + at[s] + (INNER ? 16 : 32) * 128 * t);
   }
 };
 
 // ---------------------------------------------------------------- a tile
-template <Mode MODE, int WI, int WO, int IT, int OT, typename Inner, typename Outer>
+template <Mode MODE, int M, int WI, int WO, int IT, int OT, typename InnerFragments, typename OuterFragments>
 struct Tile16 {
-  typedef Inner Inner_;
-  typedef Outer Outer_;
+  typedef typename Matrix<M>::Sum Sum;
   static constexpr int kWaves = WI * WO, kThreads = kWaves * 64;
   static constexpr int kInner = WI * IT * 32, kOuter = WO * OT * 32;
-  static constexpr int kStageBytes = Inner::kBytes + Outer::kBytes;
-  static constexpr int kLdsBytes = 2 * kStageBytes;
+  static constexpr int kInnerBytes = kInner * 128, kStageBytes = kInnerBytes + kOuter * 128;
+  static constexpr int kOutBytes = 4096;             // of a wave, to bring its values into the output's order
+  static constexpr int kLdsBytes = 2 * kStageBytes;  // the same bytes, after the last block
+  static_assert(kLdsBytes >= kWaves * kOutBytes && kLdsBytes + kOuter * 4 <= 160 * 1024, "fits a compute unit");
+  static constexpr int kI = IT * 32 / M, kO = OT * 32 / M, kSteps = kTileK / Matrix<M>::kK;
 
   static __device__ __forceinline__ int inner_first(int wave) { return wave % WI * (IT * 32); }
   static __device__ __forceinline__ int outer_first(int wave) { return wave / WI * (OT * 32); }
 
-  // loads.issue(i, blk, stage): one of the loads.kLoads loads of block blk to LDS, in order; loads.fetch(blk): what they
-  // need in registers; loads.settle(): waits for that
+  // Blocks 0 and 1 of a tile on their way.
   template <typename Loads>
-  static __device__ __forceinline__ void run(const Inner& in, const Outer& out, Loads& loads, int K, uint8_t* lds,
-                                             f32x16 (&acc)[OT][IT]) {
-    constexpr int kTiles = IT * OT, kReads = IT + OT;
+  static __device__ __forceinline__ void start(Loads& loads) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      loads.fetch(b);
+      loads.begin(b);
+#pragma unroll
+      for (int i = 0; i < Loads::kLoads; ++i) loads.issue(i, b * kStageBytes);
+    }
+  }
+
+  // The products, after start().
+  //
+  // loads.issue(i, stage): one of the loads.kLoads loads of a block to LDS, in order.  What they need in registers
+  // is asked for by loads.fetch(blk), early, and waited for by loads.begin(blk), right before the first of them.
+  //
+  // A block is four quarters.  All its fragments are in registers after its first one: the last quarter (of the block
+  // before) and the first read those of half a block each, under the matrix instructions.  Its stage is then free for the
+  // block after the next one, whose loads go out in the second and third quarter, at half the rate the memory units take
+  // them, and have until the end of the next block's third, so that the last of them has a block's time.  A wait for all
+  // loads but the last block's, once a block, leaves the rest in flight.
+  template <typename Loads>
+  static __device__ __forceinline__ void run(const InnerFragments& in, const OuterFragments& out, Loads& loads, int K,
+                                             const uint8_t* lds, Sum (&acc)[kO][kI]) {
+    constexpr int kLoads = Loads::kLoads, kReads = kSteps / 2 * (kI + kO), kSlots = kSteps * kI * kO / 4;
     const int blocks = (K - 1) / kTileK + 1;
-    i32x4 fi[2][IT], fo[2][OT];
+    i32x4 fi[kSteps][kI], fo[kSteps][kO];
 #pragma unroll
-    for (int o = 0; o < OT; ++o)
+    for (int o = 0; o < kO; ++o)
 #pragma unroll
-      for (int t = 0; t < IT; ++t)
+      for (int t = 0; t < kI; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[o][t][i] = 0.0f;
-    // fragment u of step s of a stage
-    auto read = [&](const uint8_t* stage, int s, int u) {
-      if (u < IT) fi[s & 1][u] = in.fragment(stage, u, s);
-      else fo[s & 1][u - IT] = out.fragment(stage + Inner::kBytes, u - IT, s);
+        for (int i = 0; i < M * M / 64; ++i) acc[o][t][i] = 0.0f;
+    // fragment u of half `half` of a stage, in the order they are needed
+    auto read = [&](const uint8_t* stage, int half, int u) {
+      const int s = half * (kSteps / 2) + u / (kI + kO);
+      u %= kI + kO;
+      if (u == 0) fo[s][0] = out.read(stage + kInnerBytes, 0, s);
+      else if (u <= kI) fi[s][u - 1] = in.read(stage, u - 1, s);
+      else fo[s][u - kI] = out.read(stage + kInnerBytes, u - kI, s);
     };
-    // the products of step s, the next step's fragments read under them (and after the last step of a block, which leaves
-    // its stage free, the loads of a later block)
-    auto step = [&](int s, const uint8_t* stage, int blk, uint32_t slot) {
+    // the products of quarter q; under them the fragments of half `half` of a stage, or a part of the loads
+    auto quarter = [&](int q, const uint8_t* stage, int half, int part, uint32_t slot) {
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) {
-        const int o = j / IT, t = j % IT;
-        multiply(fi[s & 1][t], fo[s & 1][o], acc[o][t]);
+      for (int j = 0; j < kSlots; ++j) {
+        const int m = q * kSlots + j, s = m / (kI * kO), o = m % (kI * kO) / kI, t = m % kI;
+        multiply(fi[s][t], fo[s][o], acc[o][t]);
+        if (half >= 0) {
+          // all are under way three quarters through
+          constexpr int kEnd = kSlots * 3 / 4;
 #pragma unroll
-        for (int u = j * kReads / kTiles; u < (j + 1) * kReads / kTiles; ++u) read(stage, (s + 1) & 3, u);
-        if (s == 3) {
+          for (int u = j * kReads / kEnd; u < (j + 1) * kReads / kEnd && u < kReads; ++u) read(stage, half, u);
+        }
+        if (part >= 0) {
+          const int at = part * kSlots + j;
 #pragma unroll
-          for (int i = j * Loads::kLoads / kTiles; i < (j + 1) * Loads::kLoads / kTiles; ++i) loads.issue(i, blk, slot);
+          for (int i = at * kLoads / (2 * kSlots); i < (at + 1) * kLoads / (2 * kSlots); ++i) loads.issue(i, slot);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    auto wait = [&] {
-      // this wave's loads have arrived and its reads are done; then those of all waves
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      loads.settle();
-    };
-    loads.fetch(0);
-    loads.settle();
-#pragma unroll
-    for (int i = 0; i < Loads::kLoads; ++i) loads.issue(i, 0, 0);
-    loads.fetch(1);
-    wait();
-#pragma unroll
-    for (int i = 0; i < Loads::kLoads; ++i) loads.issue(i, 1, kStageBytes);
+    wait_for_loads<Loads::kDirect>();
     loads.fetch(2);
 #pragma unroll
     for (int u = 0; u < kReads; ++u) read(lds, 0, u);
     for (int b = 0; b < blocks; ++b) {
       const uint32_t slot = (b & 1) * kStageBytes;
-      const uint8_t* stage = lds + slot;
-      step(0, stage, 0, 0);
-      step(1, stage, 0, 0);
-      step(2, stage, 0, 0);
-      wait();                              // the next block is there, and all are done with this one
-      step(3, lds + (kStageBytes - slot), b + 2, slot);
+      quarter(0, lds + slot, 1, -1, 0);
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");     // all are done with this stage
+      loads.begin(b + 2);
+      quarter(1, nullptr, -1, 0, slot);
+      quarter(2, nullptr, -1, 1, slot);
+      wait_for_loads<Loads::kDirect>();    // the next block is there
       loads.fetch(b + 3);
+      quarter(3, lds + (kStageBytes - slot), 0, -1, 0);
     }
-    wait();                                // none may land in LDS that is no longer this workgroup's
+    wait_for_loads<0>();                   // both stages are free again, and none lands in LDS after the end
   }
 
-  static __device__ __forceinline__ void multiply(i32x4 a, i32x4 b, f32x16& acc) {
+  // Waits for all but the last N loads of every wave.
+  template <int N>
+  static __device__ __forceinline__ void wait_for_loads() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+  }
+
+  static __device__ __forceinline__ void multiply(i32x4 a, i32x4 b, Sum& acc) {
     if constexpr (MODE == kBothBf16) {
-      acc = mfma_bf16(a, b, acc);
+      acc = Matrix<M>::bf16(a, b, acc);
     } else if constexpr (MODE == kBothF16) {
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), acc, 0, 0,
-                                                   0);
+      acc = Matrix<M>::f16(a, b, acc);
     } else {
       i32x4 high, low;
       split_f16(b, high, low);
-      acc = mfma_bf16(a, high, acc);
-      acc = mfma_bf16(a, low, acc);
+      acc = Matrix<M>::bf16(a, high, acc);
+      acc = Matrix<M>::bf16(a, low, acc);
     }
   }
 
-  // Stores the wave's values: row(r) is outer row r's first element in the
-  // output or -1, some(r) whether it has values (else zeros), `left` the inner
-  // values from the tile's start on.
+  // Stores the wave's values: row(r) is outer row r's first element in the output or -1, some(r) whether it has values
+  // (else zeros), `left` the inner values from the tile's start on.  Runs of 32 rows and 128 bytes pass through a part of
+  // LDS that is the wave's own, so that memory gets whole lines.
   template <typename Row, typename Some>
-  static __device__ __forceinline__ void store(const f32x16 (&acc)[OT][IT], void* out, int32_t dtype, int64_t width,
-                                               int64_t left, Row row, Some some) {
+  static __device__ __forceinline__ void store(const Sum (&acc)[kO][kI], uint8_t* lds, void* out, int32_t dtype,
+                                               int64_t width, int64_t left, Row row, Some some) {
+    if (dtype == kF32) store_as<kF32>(acc, lds, out, width, left, row, some);
+    else if (dtype == kBf16) store_as<kBf16>(acc, lds, out, width, left, row, some);
+    else store_as<kF16>(acc, lds, out, width, left, row, some);
+  }
+
+  template <int DTYPE, typename Row, typename Some>
+  static __device__ __forceinline__ void store_as(const Sum (&acc)[kO][kI], uint8_t* lds, void* out, int64_t width,
+                                                  int64_t left, Row row, Some some) {
+    constexpr int kSize = DTYPE == kF32 ? 4 : 2, kPart = 16 / kSize;
+    constexpr int kRun = IT * 32 * kSize < 128 ? IT * 32 : 128 / kSize;    // inner values of a run
+    constexpr int kParts = kRun * kSize / 16, kAtOnce = 64 / kParts;       // 16-byte parts of its rows, rows of a store
+    static_assert(kRun % 32 == 0 && IT * 32 % kRun == 0 && (kParts == 8 || kParts == 4), "whole runs");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = inner_first(wave) + (lane >> 5) * (16 * IT), wo = outer_first(wave);
+    uint8_t* own = lds + wave * kOutBytes;
+    auto place = [](int r, int part) { return r * (kParts * 16) + ((part ^ (kParts == 8 ? r >> 1 & 7 : r >> 2 & 3)) << 4); };
+    const bool whole = width % kPart == 0;
 #pragma unroll
     for (int o = 0; o < OT; ++o) {
-      const int r = wo + o * 32 + (lane & 31);
-      const int64_t at = row(r);
-      if (at < 0) continue;
-      const bool in = some(r);
+      int64_t at[32 / kAtOnce];
+      bool in[32 / kAtOnce];
 #pragma unroll
-      for (int t = 0; t < IT; ++t) {
-        float v[16];
+      for (int j = 0; j < 32 / kAtOnce; ++j) {
+        const int r = outer_first(wave) + o * 32 + j * kAtOnce + lane / kParts;
+        at[j] = row(r);
+        in[j] = some(r);
+      }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = in ? acc[o][t][i] : 0.0f;
+      for (int run = 0; run < IT * 32 / kRun; ++run) {
+        // the run's values of 32 rows, four at a time
 #pragma unroll
-        for (int i = 0; i < 16; i += 8) {
-          const int64_t n = wi + 16 * t + i;
-          if (n < left) store_eight(out, dtype, at + n, left - n < 8 ? (int)(left - n) : 8, width, v + i);
+        for (int oo = 0; oo < 32 / M; ++oo)
+#pragma unroll
+          for (int tt = 0; tt < kRun / M; ++tt)
+#pragma unroll
+            for (int q = 0; q < M * M / 256; ++q) {
+              const Sum& v = acc[o * (32 / M) + oo][run * (kRun / M) + tt];
+              const int i = tt * M + Matrix<M>::four(lane, q);
+              uint8_t* to = own + place(oo * M + lane % M, i / kPart);
+              if constexpr (DTYPE == kF32) {
+                *reinterpret_cast<f32x4*>(to) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+              } else {
+                u16 h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = DTYPE == kBf16 ? float_to_bf16(v[4 * q + j]) : float_to_f16(v[4 * q + j]);
+                *reinterpret_cast<uint2*>(to + (i & 4) * 2) =
+                    uint2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+              }
+            }
+        const int64_t n = inner_first(wave) + run * kRun + lane % kParts * kPart;
+#pragma unroll
+        for (int j = 0; j < 32 / kAtOnce; ++j) {
+          i32x4 v = *reinterpret_cast<const i32x4*>(own + place(j * kAtOnce + lane / kParts, lane % kParts));
+          if (!in[j]) v = i32x4{0, 0, 0, 0};
+          if (at[j] < 0 || n >= left) continue;
+          uint8_t* to = static_cast<uint8_t*>(out) + (at[j] + n) * kSize;
+          if (whole && left - n >= kPart) {
+            *reinterpret_cast<i32x4*>(to) = v;
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPart; ++e)
+              if (e < left - n) {
+                if constexpr (DTYPE == kF32) reinterpret_cast<int*>(to)[e] = v[e];
+                else reinterpret_cast<u16*>(to)[e] = (u16)((uint32_t)v[e / 2] >> e % 2 * 16);
+              }
+          }
         }
       }
     }
@@ -411,91 +534,211 @@ __device__ __forceinline__ int32_t source_of(const int32_t* rows, FastDiv topk, 
 
 enum Weights { kWeights, kWeightsTransposed, kWeights4 };
 
-template <int WI, int WO, int IT, Weights FORM>
+template <int ROWS, int W, int M, Weights FORM>
 struct InnerOperand {
-  typedef Along<WI * IT * 32, WI * WO, IT, true> Type;
+  typedef Along<ROWS, W> Loader;
+  typedef AlongFragments<M> Fragments;
 };
-template <int WI, int WO, int IT>
-struct InnerOperand<WI, WO, IT, kWeightsTransposed> {
-  typedef Across<WI * IT * 32, WI * WO, IT, true> Type;
+template <int ROWS, int W, int M>
+struct InnerOperand<ROWS, W, M, kWeightsTransposed> {
+  typedef Across<ROWS, W, M> Loader;
+  typedef AcrossFragments<ROWS, M> Fragments;
 };
-template <int WI, int WO, int IT>
-struct InnerOperand<WI, WO, IT, kWeights4> {
-  typedef FourBit<WI * IT * 32, WI * WO, IT, true> Type;
+template <int ROWS, int W, int M>
+struct InnerOperand<ROWS, W, M, kWeights4> {
+  typedef FourBit<ROWS, W> Loader;
+  typedef AlongFragments<M> Fragments;
 };
-
-template <Mode MODE, int WI, int WO, int IT, int OT, Weights FORM>
-using LinearTile = Tile16<MODE, WI, WO, IT, OT, typename InnerOperand<WI, WO, IT, FORM>::Type,
-                          Along<WO * OT * 32, WI * WO, OT, false>>;
 
 // The loads of a product's tile.
-template <typename Inner, typename Outer>
+template <typename Inner, typename Outer, Weights FORM>
 struct LinearLoads {
   static constexpr int kLoads = Inner::kLoads + Outer::kLoads;
-  Inner& in;
-  const Outer& out;
+  static constexpr int kDirect = FORM == kWeights4 ? Outer::kLoads : kLoads;     // those to LDS directly
+  Inner in;
+  Outer out;
   uint8_t* lds;
   uint32_t at;
-  int K, wave;
+  int K, wave, blk;
+  i32x4 from;
 
+  __device__ __forceinline__ void fetch(int b) {
+    if constexpr (FORM == kWeights4) in.fetch(b, K);
+  }
+  __device__ __forceinline__ void begin(int b) {
+    blk = b;
+    if constexpr (FORM == kWeights4) in.settle();
+    if constexpr (FORM == kWeightsTransposed) from = in.describe_block(b, K);
+  }
   // what goes through registers first: it was waited for, and nothing that was issued since is waited for with it
-  __device__ __forceinline__ void issue(int i, int blk, uint32_t slot) const {
+  __device__ __forceinline__ void issue(int i, uint32_t slot) const {
     if (i < Inner::kLoads) {
-      if constexpr (Inner::kThroughRegisters) in.load(i, lds + slot);
+      if constexpr (FORM == kWeights4) in.load(i, lds + slot);
+      else if constexpr (FORM == kWeightsTransposed) in.load(i, from, wave, at + slot);
       else in.load(i, blk, K, wave, at + slot);
     } else {
       out.load(i - Inner::kLoads, blk, K, wave, at + slot + Inner::kBytes);
     }
   }
-  __device__ __forceinline__ void fetch(int blk) {
-    if constexpr (Inner::kThroughRegisters) in.fetch(blk, K);
-  }
-  __device__ __forceinline__ void settle() {
-    if constexpr (Inner::kThroughRegisters) in.settle();
+};
+
+// WI IT 32 outputs of WO OT 32 rows.
+template <Mode MODE, int M, int WI, int WO, int IT, int OT, Weights FORM, bool FAR>
+struct LinearUnit {
+  typedef InnerOperand<WI * IT * 32, WI * WO, M, FORM> Inner;
+  typedef Gathered<WO * OT * 32, WI * WO, FAR> Outer;
+  typedef Tile16<MODE, M, WI, WO, IT, OT, typename Inner::Fragments, AlongFragments<M>> Tile_;
+
+  // rows t.row .. of group t.g, outputs i0 ..
+  static __device__ __forceinline__ void run(const Linear16Args& a, const Tile& t, int i0, uint8_t* lds, int32_t* src) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int width = FORM == kWeightsTransposed ? a.C : a.N, K = FORM == kWeightsTransposed ? a.N : a.C;
+    for (int r = threadIdx.x; r < Tile_::kOuter; r += Tile_::kThreads)
+      src[r] = r < t.rows && t.g < a.G ? source_of(a.rows, a.fd_topk, a.X, t.row + r) : -1;
+    __syncthreads();
+    typename Tile_::Sum acc[Tile_::kO][Tile_::kI];
+    if (t.g < a.G && a.X > 0) {
+      LinearLoads<typename Inner::Loader, Outer, FORM> loads;
+      loads.lds = lds;
+      loads.at = lds_address(lds);
+      loads.K = K;
+      loads.wave = wave;
+      const int64_t n = (int64_t)t.g * a.N;
+      if constexpr (FORM == kWeightsTransposed)
+        loads.in.init(lane, wave, static_cast<const uint8_t*>(a.w) + (n * a.C + i0) * 2, (int64_t)a.C * 2, width - i0);
+      else if constexpr (FORM == kWeights)
+        loads.in.init(lane, wave, static_cast<const uint8_t*>(a.w) + (n + i0) * K * 2, (uint32_t)K * 2, width - i0);
+      else
+        loads.in.init(lane, wave, a.q + (n + i0) * (K / 2), a.scale + (n + i0) * (K / kScaleGroup), K, width - i0);
+      loads.out.init(lane, wave, static_cast<const uint8_t*>(a.x), a.ld * 2, a.X, [&](int r) { return src[r]; });
+      typename Inner::Fragments in;
+      AlongFragments<M> out;
+      in.init(lane, Tile_::inner_first(wave));
+      out.init(lane, Tile_::outer_first(wave));
+      Tile_::start(loads);
+      Tile_::run(in, out, loads, K, lds, acc);
+    }
+    Tile_::store(acc, lds, a.y, a.y_dtype, width, width - i0,
+                 [&](int r) -> int64_t { return r < t.rows ? (int64_t)(t.row + r) * width + i0 : -1; },
+                 [&](int r) { return src[r] >= 0; });
   }
 };
 
-template <Mode MODE, int WI, int WO, int IT, int OT, Weights FORM>
-__global__ __launch_bounds__(WI* WO * 64) void linear_tile_kernel(Linear16Args a, int32_t columns) {
-  typedef LinearTile<MODE, WI, WO, IT, OT, FORM> Tile_;
+// Tiles of 128 x 128, four waves, two workgroups to a compute unit.
+template <Mode MODE, Weights FORM, bool FAR>
+__global__ __launch_bounds__(256) void linear_small_kernel(Linear16Args a, int32_t columns) {
+  typedef LinearUnit<MODE, 16, 2, 2, 2, 2, FORM, FAR> Unit;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ int32_t src[Tile_::kOuter];
-  const int32_t row_tiles = count_tiles(a.offsets, a.G, a.R, Tile_::kOuter, true);
+  __shared__ int32_t src[128];
+  const int32_t row_tiles = count_tiles(a.offsets, a.G, a.R, 128, true);
   const int64_t tiles = min((int64_t)row_tiles * columns, (int64_t)gridDim.x);    // less where offsets decrease
   if (blockIdx.x >= tiles) return;
   int32_t row, column;
   band_order(die_order(blockIdx.x, (int32_t)tiles), row_tiles, columns, row, column);
-  const Tile t = find_tile(a.offsets, a.G, a.R, Tile_::kOuter, row, true);
+  const Tile t = find_tile(a.offsets, a.G, a.R, 128, row, true);
   if (t.g < 0) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int width = FORM == kWeightsTransposed ? a.C : a.N, K = FORM == kWeightsTransposed ? a.N : a.C;
-  const int i0 = column * Tile_::kInner;
-  for (int r = threadIdx.x; r < Tile_::kOuter; r += Tile_::kThreads)
-    src[r] = r < t.rows && t.g < a.G ? source_of(a.rows, a.fd_topk, a.X, t.row + r) : -1;
-  __syncthreads();
-  f32x16 acc[OT][IT];
-  if (t.g < a.G && a.X > 0) {
-    typename Tile_::Inner_ in;
-    typename Tile_::Outer_ out;
-    const uint8_t* w = static_cast<const uint8_t*>(a.w) + (int64_t)t.g * a.N * a.C * 2;
-    // a row that has no source reads one that is there, and is not stored
-    out.init(lane, wave, Tile_::outer_first(wave),
-             [&](int r) { return static_cast<const uint8_t*>(a.x) + max(src[r], 0) * a.ld * 2; });
-    if constexpr (FORM == kWeightsTransposed) {
-      in.init(lane, wave, Tile_::inner_first(wave), w + i0 * 2, (int64_t)a.C * 2, width - i0);
-    } else if constexpr (FORM == kWeights) {
-      in.init(lane, wave, Tile_::inner_first(wave),
-              [&](int r) { return w + (int64_t)min(i0 + r, width - 1) * K * 2; });
-    } else {
-      const int64_t n = (int64_t)t.g * a.N + i0;
-      in.init(lane, wave, Tile_::inner_first(wave), a.q + n * (K / 2), a.scale + n * (K / kScaleGroup), K, width - i0);
+  Unit::run(a, t, column * 128, lds, src);
+}
+
+// Tiles of 256 x 256, eight waves, one workgroup to a compute unit.  The chip takes 256 at a time, so what does not fill a
+// round of them is given out in smaller pieces at the end: full tiles past the last whole round as two of 256 x 128 each
+// (where that makes one round of half the time), and what a group has behind its last 256 rows as 256 x 128 or, for 128
+// rows or fewer, 128 x 128.
+constexpr int kUnits = 256;                // compute units
+
+struct LargePlan {
+  int32_t full_rows, part_rows;            // row tiles of 256 rows; groups with rows behind them
+  int64_t whole, split;                    // tiles given out whole, and in two pieces
+  int64_t blocks;
+};
+
+__host__ __device__ __forceinline__ LargePlan plan_large(int32_t full_rows, int32_t part_rows, int64_t columns) {
+  LargePlan p;
+  p.full_rows = full_rows;
+  p.part_rows = part_rows;
+  const int64_t full = full_rows * columns, over = full % kUnits;
+  p.split = over <= kUnits / 2 ? over : 0;
+  p.whole = full - p.split;
+  p.blocks = p.whole + 2 * p.split + 2 * columns * part_rows;
+  return p;
+}
+
+// Row tile `want` of 256 rows of all groups in order, or (want past them) what is behind the last one of a group.
+__device__ __forceinline__ Tile find_large(const int32_t* offsets, int32_t G, int32_t R, int32_t want, bool part) {
+  const int lane = threadIdx.x & 63;
+  int32_t carry = 0;
+  for (int32_t g0 = 0; g0 < G + 2; g0 += 64) {
+    const int32_t g = g0 + lane;
+    const Span s = g < G + 2 ? group_span(offsets, g, G, R) : Span{0, 0};
+    const int32_t rows = s.hi > s.lo ? s.hi - s.lo : 0, tiles = part ? rows % 256 != 0 : rows / 256;
+    int32_t incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t v = __shfl_up(incl, d);
+      if (lane >= d) incl = add_tiles(incl, v);
     }
-    LinearLoads<typename Tile_::Inner_, typename Tile_::Outer_> loads{in, out, lds, lds_address(lds), K, wave};
-    Tile_::run(in, out, loads, K, lds, acc);
+    const int32_t before = add_tiles(carry, incl - tiles);
+    const u64 here = __ballot(want >= before && want - before < tiles);
+    if (here != 0) {
+      const int at = __ffsll((unsigned long long)here) - 1;
+      const int32_t skip = part ? __shfl(rows, at) / 256 : want - __shfl(before, at);
+      Tile t;
+      t.g = __builtin_amdgcn_readfirstlane(g0 + at);
+      t.row = __builtin_amdgcn_readfirstlane(__shfl(s.lo, at) + skip * 256);
+      t.rows = __builtin_amdgcn_readfirstlane(part ? __shfl(rows, at) % 256 : 256);
+      return t;
+    }
+    carry = __builtin_amdgcn_readfirstlane(__shfl(add_tiles(carry, incl), 63));
   }
-  Tile_::store(acc, a.y, a.y_dtype, width, width - i0,
-               [&](int r) -> int64_t { return r < t.rows ? (int64_t)(t.row + r) * width + i0 : -1; },
-               [&](int r) { return src[r] >= 0; });
+  return Tile{-1, 0, 0};
+}
+
+__device__ __forceinline__ LargePlan plan_large(const int32_t* offsets, int32_t G, int32_t R, int64_t columns) {
+  const int lane = threadIdx.x & 63;
+  int32_t full = 0, part = 0;
+  for (int32_t g = lane; g < G + 2; g += 64) {
+    const Span s = group_span(offsets, g, G, R);
+    const int32_t rows = s.hi > s.lo ? s.hi - s.lo : 0;
+    full = add_tiles(full, rows / 256);
+    part += rows % 256 != 0;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    full = add_tiles(full, __shfl_xor(full, d));
+    part += __shfl_xor(part, d);
+  }
+  return plan_large(__builtin_amdgcn_readfirstlane(full), __builtin_amdgcn_readfirstlane(part), columns);
+}
+
+template <Mode MODE, Weights FORM>
+__global__ __launch_bounds__(512) void linear_large_kernel(Linear16Args a, int32_t columns) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ int32_t src[256];
+  const LargePlan p = plan_large(a.offsets, a.G, a.R, columns);
+  int64_t id = blockIdx.x;
+  if (id < p.whole) {
+    int32_t row, column;
+    band_order(die_order((int32_t)id, (int32_t)min(p.whole, (int64_t)gridDim.x)), p.full_rows, columns, row, column);
+    const Tile t = find_large(a.offsets, a.G, a.R, row, false);
+    if (t.g >= 0) LinearUnit<MODE, 16, 4, 2, 2, 4, FORM, false>::run(a, t, column * 256, lds, src);
+    return;
+  }
+  id -= p.whole;
+  const int32_t width = FORM == kWeightsTransposed ? a.C : a.N;
+  int32_t row, column;
+  Tile t;
+  if (id < 2 * p.split) {
+    band_order((int32_t)(p.whole + id / 2), p.full_rows, columns, row, column);
+    t = find_large(a.offsets, a.G, a.R, row, false);
+    column = column * 256 + (int32_t)(id & 1) * 128;
+  } else {
+    id -= 2 * p.split;
+    t = find_large(a.offsets, a.G, a.R, (int32_t)min(id / (2 * columns), (int64_t)0x7FFFFFFF), true);
+    column = (int32_t)(id % (2 * columns)) * 128;
+  }
+  if (t.g < 0 || column >= width) return;
+  if (t.rows > 128) LinearUnit<MODE, 16, 4, 2, 1, 4, FORM, false>::run(a, t, column, lds, src);
+  else LinearUnit<MODE, 16, 4, 2, 1, 2, FORM, false>::run(a, t, column, lds, src);
 }
 
 }  // namespace eplb

@@ -77,6 +77,11 @@ CASES = [
     ([1] * 70 + [40], 1, 0, 64, 2, 96, 264, "f16", "f32", True),
     ([4, 4], 0, 0, 0, 1, 24, 40, "bf16", "bf16", True),
     ([300, 212], 0, 0, 512, 1, 1024, 320, "f16", "f16", False),
+    # tiles of 256 rows: whole ones, pieces of them at the end, and what is behind a group's last 256 rows
+    ([700, 257, 0, 900], 3, 6, 933, 2, 3801, 72, "bf16", "bf16", True),
+    ([2304], 0, 0, 2304, 1, 4097, 136, "f16", "f32", False),
+    ([1025, 511], 0, 300, 918, 2, 6000, 64, "bf16", "f16", True),
+    ([256 * 9], 0, 0, 2304, 1, 3840, 200, "bf16", "bf16", False),
 ]
 
 
@@ -111,7 +116,8 @@ def test_product(counts, head, tail, X, topk, N, C, dtype, out, rows):
 
 
 @pytest.mark.parametrize("counts,head,tail,X,topk,N,C,dtype,out,rows",
-                         [c[:5] + (-(-c[5] // 8) * 8,) + c[6:] for c in CASES])
+                         [c[:5] + (-(-c[5] // 8) * 8,) + c[6:] for c in CASES[:11]] +
+                         [c[:5] + (c[6], -(-c[5] // 8) * 8) + c[7:] for c in CASES[11:]])
 def test_product_transposed(counts, head, tail, X, topk, N, C, dtype, out, rows):
     off, R = grouping(counts, head, tail)
     note("transposed", counts[:6], head, tail, X, topk, N, C, dtype, out, rows)
@@ -133,7 +139,10 @@ def test_product_transposed(counts, head, tail, X, topk, N, C, dtype, out, rows)
 
 
 @pytest.mark.parametrize("counts,head,tail,X,topk,N,C,dtype,out,rows",
-                         [c[:5] + (-(-c[5] // 8) * 8,) + c[6:] for c in CASES])
+                         [c[:5] + (-(-c[5] // 8) * 8,) + c[6:] for c in CASES[:11]] + [
+                             # tiles of 256 x 256, with rows and without
+                             ([70, 0, 193, 64, 1], 3, 2, 111, 3, 1288, 1800, "bf16", "f32", True),
+                             ([300, 100], 0, 0, 400, 1, 2056, 2048, "f16", "f16", False)])
 def test_weight_gradient(counts, head, tail, X, topk, N, C, dtype, out, rows):
     off, R = grouping(counts, head, tail)
     note("wgrad", counts[:6], head, tail, X, topk, N, C, dtype, out, rows)
