@@ -1,5 +1,5 @@
 // The experts' products in 16 bits and the gradient of their weights.
-#include "tile16.h"
+#include "stream16.h"
 
 namespace eplb {
 
@@ -77,13 +77,13 @@ struct WgradLoads {
   }
 };
 
-template <Mode MODE, int M, bool ROWS, bool FAR, int WI, int WO, int IT, int OT>
+template <Mode MODE, bool ROWS, bool FAR, int WI, int WO, int IT, int OT>
 __global__ __launch_bounds__(WI* WO * 64) void wgrad16_kernel(Wgrad16Args a, int32_t ni, int32_t no) {
-  typedef Across<WI * IT * 32, WI * WO, M> Inner;
-  typedef Across<WO * OT * 32, WI * WO, M> Outer;
-  typedef AcrossFragments<WI * IT * 32, M> InnerFragments;
-  typedef AcrossFragments<WO * OT * 32, M> OuterFragments;
-  typedef Tile16<MODE, M, WI, WO, IT, OT, InnerFragments, OuterFragments> Tile_;
+  typedef Across<WI * IT * 32, WI * WO> Inner;
+  typedef Across<WO * OT * 32, WI * WO> Outer;
+  typedef AcrossFragments<WI * IT * 32> InnerFragments;
+  typedef AcrossFragments<WO * OT * 32> OuterFragments;
+  typedef Tile16<MODE, WI, WO, IT, OT, InnerFragments, OuterFragments> Tile_;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t id = die_order(blockIdx.x, gridDim.x);
@@ -124,36 +124,6 @@ __global__ __launch_bounds__(WI* WO * 64) void wgrad16_kernel(Wgrad16Args a, int
                [&](int r) -> int64_t { return o0 + r < a.N ? ((int64_t)g * a.N + o0 + r) * a.C + i0 : -1; },
                [&](int) { return K > 0; });
 }
-int64_t small_blocks(int64_t R, int64_t width, int32_t G) {
-  // every group adds at most one tile that is not full, and a tile has a row
-  return (std::min(R, R / 128 + G) + 2) * ceil_div(width, 128);
-}
-
-int64_t large_blocks(int64_t R, int64_t width, int32_t G) {
-  const int64_t columns = ceil_div(width, 256);
-  return R / 256 * columns + kUnits / 2 + 2 * columns * std::min(R, (int64_t)G + 2);
-}
-
-bool large_linear(int64_t R, int64_t width, int32_t G) {
-  return R >= 128 * (int64_t)G && (R / 256 + G / 2) * ceil_div(width, 256) >= 128;
-}
-
-template <Mode MODE, Weights FORM>
-hipError_t launch_form(const Linear16Args& a, hipStream_t stream) {
-  const int64_t width = FORM == kWeightsTransposed ? a.C : a.N;
-  const bool far = a.X * a.ld * 2 >= (int64_t)kOutside;
-  if (!far && large_linear(a.R, width, a.G)) {
-    linear_large_kernel<MODE, FORM><<<dim3((unsigned)large_blocks(a.R, width, a.G)), dim3(512),
-                                      2 * 2 * 256 * 128, stream>>>(a, (int32_t)ceil_div(width, 256));
-    return hipGetLastError();
-  }
-  const dim3 grid((unsigned)small_blocks(a.R, width, a.G));
-  const int32_t columns = (int32_t)ceil_div(width, 128);
-  if (far) linear_small_kernel<MODE, FORM, true><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
-  else linear_small_kernel<MODE, FORM, false><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
-  return hipGetLastError();
-}
-
 bool large_wgrad(int64_t N, int64_t C, int32_t G) { return G * ceil_div(N, 256) * ceil_div(C, 256) >= 128; }
 
 template <Mode MODE, bool ROWS>
@@ -161,32 +131,42 @@ hipError_t launch_wgrad_form(const Wgrad16Args& a, hipStream_t stream) {
   const bool far = ROWS && a.X * a.ld * 2 >= (int64_t)kOutside;
   if (!far && large_wgrad(a.N, a.C, a.G)) {
     const int64_t ni = ceil_div(a.C, 256), no = ceil_div(a.N, 256);
-    wgrad16_kernel<MODE, 16, ROWS, false, 4, 2, 2, 4>
+    wgrad16_kernel<MODE, ROWS, false, 4, 2, 2, 4>
         <<<dim3((unsigned)(a.G * ni * no)), dim3(512), 2 * 2 * 256 * 128, stream>>>(a, (int32_t)ni, (int32_t)no);
   } else {
     const int64_t ni = ceil_div(a.C, 128), no = ceil_div(a.N, 128);
     const dim3 grid((unsigned)(a.G * ni * no));
-    if (far) wgrad16_kernel<MODE, 16, ROWS, ROWS, 2, 2, 2, 2><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, ni, no);
-    else wgrad16_kernel<MODE, 16, ROWS, false, 2, 2, 2, 2><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, ni, no);
+    if (far) wgrad16_kernel<MODE, ROWS, ROWS, 2, 2, 2, 2><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, ni, no);
+    else wgrad16_kernel<MODE, ROWS, false, 2, 2, 2, 2><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, ni, no);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t linear16_blocks(int64_t R, int64_t outputs, int64_t, int32_t G, bool) {
-  return std::max(small_blocks(R, outputs, G), large_linear(R, outputs, G) ? large_blocks(R, outputs, G) : 0);
+int64_t linear16_blocks(int64_t R, int64_t outputs, int64_t, int32_t G, bool transpose) {
+  const int64_t tiles = tile_blocks(R, outputs, G);
+  return !transpose && stream_suits(R, G, false) ? std::max(tiles, stream_blocks(R, outputs, G, false)) : tiles;
 }
 
 int64_t wgrad16_blocks(int64_t, int64_t N, int64_t C, int32_t G) {
   return (int64_t)G * ceil_div(N, 128) * ceil_div(C, 128);       // of the smaller tiles, which every size may get
 }
 
+namespace {
+
+template <Mode MODE>
+hipError_t launch_form(const Linear16Args& a, bool transpose, hipStream_t stream) {
+  if (transpose) return launch_tiles<MODE, kWeightsTransposed>(a, stream);
+  if (stream_suits(a.R, a.G, false) && a.X * a.ld * 2 < (int64_t)kOutside) return launch_stream<MODE, false>(a, stream);
+  return launch_tiles<MODE, kWeights>(a, stream);
+}
+
+}  // namespace
+
 hipError_t launch_linear16(const Linear16Args& a, bool transpose, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
-  if (a.dtype == kF16)
-    return transpose ? launch_form<kBothF16, kWeightsTransposed>(a, stream) : launch_form<kBothF16, kWeights>(a, stream);
-  return transpose ? launch_form<kBothBf16, kWeightsTransposed>(a, stream) : launch_form<kBothBf16, kWeights>(a, stream);
+  return a.dtype == kF16 ? launch_form<kBothF16>(a, transpose, stream) : launch_form<kBothBf16>(a, transpose, stream);
 }
 
 hipError_t launch_wgrad16(const Wgrad16Args& a, hipStream_t stream) {

@@ -1,0 +1,309 @@
+// The experts' products for few rows to a group: the weights are read once, from
+// memory to registers, and bound the time.
+//
+// A workgroup of eight waves takes 16 MT rows of a group; KS waves share K, a run
+// of chunks each in turn, and each of the 8 / KS sets of them has 16 outputs.  The
+// rows pass through LDS, in two stages of 32 KiB that all waves share: read from
+// memory by every wave for itself they would be several times the weights' bytes.
+// The weights of D chunks are in flight at once, in registers, whatever the stages
+// do, in whole cache lines: what a compute unit can have under way is the lines of
+// its first-level cache, 32 KiB, however little of a line is wanted.  No load stands
+// behind a branch: what lies past the end of a row, a group or the outputs has an
+// offset outside its descriptor and arrives as zeros.
+//
+// Measured, weights not in any cache: a token's 8 rows on 32 groups, 4096 x 2048:
+// 23.5 us, 5.7 TB/s (4-bit weights 13.4 us); 512 rows on 9, 2048 x 4096: 40 us (30);
+// tiles of 128 x 128: 26 (33) and 50 (59).
+#pragma once
+
+#include <cmath>
+
+#include "tile16.h"
+
+namespace eplb {
+
+constexpr int kStreamWaves = 8;
+constexpr int kStreamStage = 32 * 1024;    // bytes of rows in a stage
+
+template <int DTYPE>
+__device__ __forceinline__ void store_four(void* p, int64_t at, int left, bool vec, f32x4 v) {
+  if (vec && left >= 4) {
+    if (DTYPE == kF32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(p) + at) = v;
+    } else {
+      u16 h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = DTYPE == kBf16 ? float_to_bf16(v[j]) : float_to_f16(v[j]);
+      *reinterpret_cast<uint2*>(static_cast<u16*>(p) + at) =
+          uint2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < left) store_float(p, DTYPE, at + j, v[j]);
+}
+
+template <bool FOUR, int MT, int KS>
+struct StreamShape {
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kChunk = FOUR ? 256 : 64;                   // k of a chunk: 128 bytes of each row of weights
+  static constexpr int kStageK = kStreamStage / (kRows * 2);       // k of a stage
+  static constexpr int kEach = kStageK / (kChunk * KS);            // chunks of a wave in a stage
+};
+
+// What a lane holds of a chunk's weights: with 16-bit ones two instructions' operands; with 4-bit ones twice four
+// instructions', a block of 32 of k each.
+struct StreamChunk {
+  i32x4 w[2];
+};
+
+// `each` sets of 16 outputs to a workgroup, `columns` workgroups to a row of tiles
+template <Mode MODE, bool FOUR, int MT, int KS, int D>
+__global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Linear16Args a, int32_t columns, int32_t each) {
+  typedef StreamShape<FOUR, MT, KS> Shape;
+  constexpr int kBlockBytes = Shape::kRows * 128, kOctets = Shape::kRows / 8;
+  constexpr int kXLoads = kStreamStage / 1024 / kStreamWaves;      // of a wave and stage
+  constexpr int kWLoads = 2;                                       // of a chunk
+  constexpr int kBatch = 4;                                        // chunks whose scales are asked for together
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStreamStage];
+  __shared__ int32_t src[Shape::kRows];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quad = lane >> 4, col = lane & 15, share = wave % KS, set = wave / KS;
+  const int n0 = ((int)(blockIdx.x % columns) * each + set) * 16;
+  const Tile t = find_tile(a.offsets, a.G, a.R, Shape::kRows, (int32_t)(blockIdx.x / columns), true);
+  if (t.g < 0) return;
+  const bool some = t.g < a.G && a.X > 0;
+  const int outputs = set < each ? max(min(a.N - n0, 16), 0) : 0;
+  const int64_t first = some && outputs > 0 ? (int64_t)t.g * a.N + n0 : 0;
+  const int rows = some ? outputs : 0;
+  const uint32_t ld = FOUR ? a.C / 2 : a.C * 2, ld_s = a.C / kScaleGroup;
+  const i32x4 from_w = FOUR ? describe(a.q + first * ld, (uint64_t)rows * ld)
+                            : describe(static_cast<const uint8_t*>(a.w) + first * ld, (uint64_t)rows * ld);
+  const i32x4 from_s = FOUR ? describe(a.scale + first * ld_s, (uint64_t)rows * ld_s) : from_w;
+  const uint32_t at_w = col * ld + quad * 16, at_s = col * ld_s + quad;
+  auto load_w = [&](int c, StreamChunk& p) {
+    const int k = c * Shape::kChunk + quad * (FOUR ? 32 : 8);      // this lane's first; half a chunk on its second
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      p.w[s] = __builtin_amdgcn_raw_buffer_load_b128(
+          resource(from_w), (at_w + s * 64) | (k + s * (Shape::kChunk / 2) < a.C ? 0 : kOutside), c * 128, 0);
+  };
+  // This wave's chunk i.  A stage's are shared out in runs, so that what lies next to each other is asked for together.
+  // Rows of weights are often a power of two apart, and then their chunks of one place all lie in one channel of the cache:
+  // each workgroup starts with another stage, and each set of waves with another chunk of its run.
+  const int stages = (a.C - 1) / Shape::kStageK + 1, turn = (int)(blockIdx.x % stages);
+  auto stage_of = [&](int stage) { return stage >= stages ? stages : stage + turn < stages ? stage + turn : stage + turn - stages; };
+  auto chunk = [&](int i) {
+    return (stage_of(i / Shape::kEach) * KS + share) * Shape::kEach + (i + set) % Shape::kEach;
+  };
+  // What rows names is asked for first, and the weights before it is looked at: loads return in order.
+  static_assert(Shape::kRows <= kStreamWaves * 64, "a thread to a row");
+  const int mine = threadIdx.x;
+  int32_t named = t.row + mine;
+  if (a.rows != nullptr && mine < t.rows) named = a.rows[t.row + mine];
+  // scales of chunks i .. i + 3, a byte to a lane and half a chunk
+  uint32_t scale[2][kBatch][2];
+  auto load_s = [&](int i, uint32_t (&to)[kBatch][2]) {
+    if constexpr (FOUR) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int c = chunk(i + j), k = c * Shape::kChunk + s * 128 + quad * 32;
+          to[j][s] = __builtin_amdgcn_raw_buffer_load_b8(resource(from_s), (at_s + s * 4) | (k < a.C ? 0 : kOutside), c * 8, 0);
+        }
+    }
+  };
+  StreamChunk part[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) load_w(chunk(d), part[d]);
+  load_s(0, scale[0]);
+  __builtin_amdgcn_sched_barrier(0);
+  if (mine < Shape::kRows) {
+    if (a.rows != nullptr) named = named < 0 ? -1 : (int32_t)fastdiv_apply((uint32_t)named, a.fd_topk);
+    src[mine] = mine < t.rows && t.g < a.G && named < a.X ? named : -1;
+  }
+  // a barrier that does not wait for the weights
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  f32x4 acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (some) {
+    const i32x4 from_x = describe(a.x, (uint64_t)a.X * a.ld * 2);
+    uint32_t at_x[kXLoads];
+    int part_x[kXLoads];
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) {
+      const int r = (wave * kXLoads + i) % kOctets * 8 + (lane >> 3);
+      part_x[i] = ((lane & 7) ^ along_key(r)) * 8;
+      at_x[i] = src[r] < 0 ? kOutside : (uint32_t)src[r] * (uint32_t)a.ld * 2 + part_x[i] * 2;
+    }
+    const uint32_t lds_at = lds_address(lds);
+    auto load_x = [&](int stage) {
+#pragma unroll
+      for (int i = 0; i < kXLoads; ++i) {
+        const int j = wave * kXLoads + i, block = stage_of(stage) * (Shape::kStageK / kTileK) + j / kOctets;
+        part_to_lds(from_x, at_x[i] | (part_x[i] < a.C - block * kTileK ? 0 : kOutside), block * 128,
+                    lds_at + (stage & 1) * kStreamStage + j * 1024);
+      }
+    };
+    // until all loads but the last `n` of every wave are there, and all waves are here
+    auto wait = [](auto n) {
+      constexpr int kLeft = decltype(n)::value < 63 ? decltype(n)::value : 63;
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+    };
+    load_x(0);
+    load_x(1);
+    constexpr int kLeast = FOUR ? 2 * kBatch : D, kMost = D > Shape::kEach ? D : Shape::kEach;
+    constexpr int kUnroll = kMost > kLeast ? kMost : kLeast, kStages = kUnroll / Shape::kEach;
+    static_assert(kUnroll % D == 0 && kUnroll % Shape::kEach == 0, "whole stages and whole rounds of chunks");
+    for (int st = 0; st < stages; st += kStages) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int stage = st + u / Shape::kEach, i = st * Shape::kEach + u;
+        if (u % Shape::kEach == 0) {
+          // this stage's rows have arrived (after them: the next one's, or a stage's weights), and all waves are done with
+          // the one before, whose place the one after this takes
+          if (stage == 0) {
+            wait(std::integral_constant<int, kXLoads>());
+          } else {
+            wait(std::integral_constant<int, Shape::kEach * kWLoads>());
+            load_x(stage + 1);
+          }
+        }
+        const uint8_t* rows_at = lds + (stage & 1) * kStreamStage;
+        const int c_in = share * Shape::kEach + (i + set) % Shape::kEach;    // its place in the stage
+        if (FOUR && u % kBatch == 0) load_s(i + kBatch, scale[u / kBatch + 1 & 1]);
+#pragma unroll
+        for (int s = 0; s < (FOUR ? 8 : 2); ++s) {
+          i32x4 w = part[u % D].w[FOUR ? s >> 2 : s];
+          if constexpr (FOUR)
+            w = four_bit_values(w[s & 3], __uint_as_float(scale[u / kBatch & 1][u % kBatch][s >> 2] << 23));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            // which eight of the chunk's k the weights are of
+            const int at = FOUR ? (s >> 2) * 16 + quad * 4 + (s & 3) : s * 4 + quad, r = m * 16 + col;
+            const int block = c_in * (Shape::kChunk / kTileK) + (at >> 3);
+            const i32x4 x = *reinterpret_cast<const i32x4*>(rows_at + block * kBlockBytes + r * 128 +
+                                                            (((at & 7) ^ along_key(r)) << 4));
+            if constexpr (MODE == kSplit) {
+              i32x4 high, low;
+              split_f16(x, high, low);
+              acc[m] = multiply_bf16(w, low, multiply_bf16(w, high, acc[m]));
+            } else {
+              acc[m] = MODE == kBothF16 ? multiply_f16(w, x, acc[m]) : multiply_bf16(w, x, acc[m]);
+            }
+          }
+        }
+        load_w(chunk(i + D), part[u % D]);                           // past the last chunk: nothing is read
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");      // LDS is free
+  }
+  if constexpr (KS > 1) {
+    // the shares of K, added up in order
+    f32x4(*sums)[MT][64] = reinterpret_cast<f32x4(*)[MT][64]>(lds);
+    static_assert(kStreamWaves * MT * 1024 <= 2 * kStreamStage, "sums fit");
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sums[wave][m][lane] = acc[m];
+    __syncthreads();
+    if (share != 0) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int s = 1; s < KS; ++s) acc[m] += sums[wave + s][m][lane];
+  }
+  const int at = n0 + quad * 4, left = min(a.N, n0 + outputs) - at;
+  if (left <= 0) return;
+  auto store = [&](auto type) {
+    constexpr int kType = decltype(type)::value;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int r = m * 16 + col;
+      if (r < t.rows)
+        store_four<kType>(a.y, (int64_t)(t.row + r) * a.N + at, left, a.N % 4 == 0,
+                          src[r] >= 0 ? acc[m] : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+    }
+  };
+  if (a.y_dtype == kF32) store(std::integral_constant<int, kF32>());
+  else if (a.y_dtype == kBf16) store(std::integral_constant<int, kBf16>());
+  else store(std::integral_constant<int, kF16>());
+}
+
+// How a product of few rows is taken: tiles of 16 mt rows, `share` waves to 16 outputs, `each` such to a workgroup.
+struct StreamPlan {
+  int mt, share, each;
+};
+
+// Tiles of `tile` rows: every group adds at most one that is not full, and a tile has a row.
+inline int64_t row_tiles(int64_t R, int32_t G, int tile) { return std::min(R, R / tile + G) + 2; }
+
+// Few rows: past these a tile of 128 x 128 reads the weights as fast, or, with 4-bit weights, a second tile of rows costs
+// what a larger tile saves.  4096 x 2048 on 9, 64 rows each: 44 us here, 50 in tiles, 85 rows: 47 and 50; 4-bit weights, 64
+// rows: 33 and 59, of 64 groups with 80 rows: 58 and 47.
+inline bool stream_suits(int64_t R, int32_t G, bool four) { return R <= (four ? 64 : 96) * (int64_t)G; }
+
+// The busiest compute unit ends last, and what it can have in flight is the same whatever is on it: the form is the one
+// for which ceil(workgroups / compute units) times the sets of outputs of a workgroup, and one more for its start and end,
+// is least.  512 rows on 9, 4096 x 2048 outputs: 40 us with 6 sets of 64 rows to a workgroup (224 of them), 65 with 5 (265).
+inline StreamPlan plan_stream(int64_t R, int64_t N, int32_t G, bool four) {
+  constexpr int kUnits = 256;
+  const double mean = (double)R / G, spread = std::sqrt(mean);      // of rows to a group, as chance deals them out
+  StreamPlan best{};
+  double least = 0;
+  for (int mt = 1; mt <= (four ? 4 : 8); mt *= 2) {
+    // what an output of a tile costs, against one of a tile of 16 rows: the weights are the same, but more is multiplied
+    const double weight = four ? (mt == 1 ? 1 : mt == 2 ? 1.15 : 1.6) : (mt == 1 ? 1 : mt == 2 ? 1.02 : mt == 4 ? 1.06 : 1.3);
+    double tiles = 0;
+    for (double z : {-1.2, -0.4, 0.4, 1.2}) tiles += 0.25 * std::max(1.0, std::ceil((mean + z * spread) / (16 * mt)));
+    tiles = std::min<double>((double)R, tiles * G);
+    for (int each = 1; each <= kStreamWaves; ++each) {
+      const double cost = weight * (each + 1) * std::ceil(tiles * ceil_div(N, 16 * each) / kUnits);
+      if (best.mt == 0 || cost < least || (cost == least && mt == best.mt)) {
+        least = cost;
+        best = StreamPlan{mt, 1, each};
+      }
+    }
+  }
+  const int most = four ? 4 / best.mt : 16 / best.mt;    // every wave has a chunk in every stage
+  while (best.share * 2 * best.each <= kStreamWaves && best.share * 2 <= most) best.share *= 2;
+  return best;
+}
+
+inline int64_t stream_blocks(int64_t R, int64_t N, int32_t G, bool four) {
+  const StreamPlan p = plan_stream(R, N, G, four);
+  return row_tiles(R, G, 16 * p.mt) * ceil_div(N, 16 * p.each);
+}
+
+template <Mode MODE, bool FOUR, int MT, int KS, int D>
+hipError_t launch_stream(const Linear16Args& a, int32_t each, hipStream_t stream) {
+  const int64_t columns = ceil_div(a.N, 16 * each);
+  linear_stream_kernel<MODE, FOUR, MT, KS, D>
+      <<<dim3((unsigned)(row_tiles(a.R, a.G, 16 * MT) * columns)), dim3(kStreamWaves * 64), 0, stream>>>(a, (int32_t)columns, each);
+  return hipGetLastError();
+}
+
+template <Mode MODE, bool FOUR, int MT>
+hipError_t launch_stream(const Linear16Args& a, const StreamPlan& p, hipStream_t stream) {
+  constexpr int kAhead = FOUR && MT < 4 ? 2 : 4, kMost = FOUR ? 4 / MT : 16 / MT;
+  if constexpr (kMost >= 8)
+    if (p.share == 8) return launch_stream<MODE, FOUR, MT, 8, kAhead>(a, p.each, stream);
+  if constexpr (kMost >= 4)
+    if (p.share == 4) return launch_stream<MODE, FOUR, MT, 4, kAhead>(a, p.each, stream);
+  if constexpr (kMost >= 2)
+    if (p.share == 2) return launch_stream<MODE, FOUR, MT, 2, kAhead>(a, p.each, stream);
+  return launch_stream<MODE, FOUR, MT, 1, kAhead>(a, p.each, stream);
+}
+
+template <Mode MODE, bool FOUR>
+hipError_t launch_stream(const Linear16Args& a, hipStream_t stream) {
+  const StreamPlan p = plan_stream(a.R, a.N, a.G, FOUR);
+  if constexpr (!FOUR)
+    if (p.mt == 8) return launch_stream<MODE, FOUR, 8>(a, p, stream);
+  return p.mt == 1 ? launch_stream<MODE, FOUR, 1>(a, p, stream)
+                   : p.mt == 2 ? launch_stream<MODE, FOUR, 2>(a, p, stream) : launch_stream<MODE, FOUR, 4>(a, p, stream);
+}
+
+}  // namespace eplb

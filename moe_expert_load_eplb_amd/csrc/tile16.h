@@ -3,7 +3,7 @@
 //
 // out[o][i] = sum over k of O(o, k) * I(i, k).  A workgroup of WI x WO waves
 // computes (WI IT 32) inner x (WO OT 32) outer values, a wave IT 32 x OT 32 of
-// them, as tiles of the matrix instruction (M x M).  The inner index is
+// them, as tiles of the matrix instruction (16 x 16).  The inner index is
 // contiguous in the output; its operand is the matrix instruction's first, so
 // that a lane ends up with runs of four inner values of one outer row.
 //
@@ -26,7 +26,6 @@
 
 namespace eplb {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -45,6 +44,12 @@ __device__ __forceinline__ i32x4 describe(const void* p, uint64_t bytes) {
   d[2] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(bytes < kOutside ? bytes : kOutside));
   d[3] = 0x00020000;                       // raw, 32-bit elements
   return d;
+}
+
+// The same for the compiler's own loads.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(i32x4 d) {
+  const uint64_t at = (uint64_t)(uint32_t)d[0] | (uint64_t)(uint32_t)d[1] << 32;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)at, 0, d[2], d[3]);
 }
 
 // 16 bytes of every lane to 1 KiB of LDS from `to` (the same for the wave).  Written out, as the compiler lets the
@@ -70,19 +75,23 @@ __device__ __forceinline__ uint32_t lds_address(uint8_t* p) {
 // values that sum to it exactly (11 significant bits are 8 and 3).
 enum Mode { kBothBf16, kBothF16, kSplit };
 
-// Eight half-precision values as bfloat16: the nearest ones, and what they leave (0 of an infinity).
+// Eight half-precision values as bfloat16: the first 8 significant bits, and what they leave (of an infinity something
+// finite).
 __device__ __forceinline__ void split_f16(i32x4 v, i32x4& high, i32x4& low) {
   const half8 x = __builtin_bit_cast(half8, v);
-  bf16x8 h, l;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f = (float)x[j];
-    h[j] = (__bf16)f;
-    const float left = f - (float)h[j];
-    l[j] = (__bf16)(fabsf(f) <= 65504.0f ? left : 0.0f);
+  for (int j = 0; j < 4; ++j) {
+    uint32_t top[2], rest[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float f = (float)x[2 * j + e];
+      top[e] = __float_as_uint(f);
+      const float fine = __builtin_amdgcn_fmed3f(f, -65504.0f, 65504.0f);
+      rest[e] = __float_as_uint(fine - __uint_as_float(__float_as_uint(fine) & 0xFFFF0000u));   // exact: at most 3 bits
+    }
+    high[j] = (int)__builtin_amdgcn_perm(top[1], top[0], 0x07060302u);
+    low[j] = (int)__builtin_amdgcn_perm(rest[1], rest[0], 0x07060302u);
   }
-  high = __builtin_bit_cast(i32x4, h);
-  low = __builtin_bit_cast(i32x4, l);
 }
 
 // Eight 4-bit values times a power of two as bfloat16.  Of the scale only the exponent counts; all bits of it set (255
@@ -97,37 +106,15 @@ __device__ __forceinline__ i32x4 four_bit_values(int codes, float scale) {
 }
 
 // ---------------------------------------------------------------- the matrix instruction
-template <int M>
-struct Matrix;
+constexpr int kM = 16;                     // its rows and columns; a lane has four rows' sums, from 4 (lane / kM) on
+constexpr int kInstrK = 32;                // its k: lane / kM takes eight of them
 
-template <>
-struct Matrix<32> {
-  typedef f32x16 Sum;
-  static constexpr int kK = 16;            // k of an instruction: lane / M takes eight of them
-  static __device__ __forceinline__ Sum bf16(i32x4 a, i32x4 b, Sum c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                   0);
-  }
-  static __device__ __forceinline__ Sum f16(i32x4 a, i32x4 b, Sum c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
-  }
-  // first of the four inner values in elements 4 q .. 4 q + 3 of a sum
-  static __device__ __forceinline__ int four(int lane, int q) { return 8 * q + 4 * (lane >> 5); }
-};
-
-template <>
-struct Matrix<16> {
-  typedef f32x4 Sum;
-  static constexpr int kK = 32;
-  static __device__ __forceinline__ Sum bf16(i32x4 a, i32x4 b, Sum c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                   0);
-  }
-  static __device__ __forceinline__ Sum f16(i32x4 a, i32x4 b, Sum c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ int four(int lane, int) { return 4 * (lane >> 4); }
-};
+__device__ __forceinline__ f32x4 multiply_bf16(i32x4 a, i32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 multiply_f16(i32x4 a, i32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
 
 // ---------------------------------------------------------------- operands
 // ROWS rows of an operand loaded by W waves.
@@ -136,24 +123,22 @@ struct Matrix<16> {
 __device__ __forceinline__ int along_key(int r) { return r >> 1 & 7; }
 
 // Where the fragments of a wave lie, in a stage of rows along k.
-template <int M>
 struct AlongFragments {
-  static constexpr int kSteps = kTileK / Matrix<M>::kK;
+  static constexpr int kSteps = kTileK / kInstrK;
   int at[kSteps];
   __device__ __forceinline__ void init(int lane, int first_row) {
-    const int r = first_row + lane % M;
+    const int r = first_row + lane % kM;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) at[s] = r * 128 + (((s * (Matrix<M>::kK / 8) + lane / M) ^ along_key(r)) << 4);
+    for (int s = 0; s < kSteps; ++s) at[s] = r * 128 + (((s * (kInstrK / 8) + lane / kM) ^ along_key(r)) << 4);
   }
   __device__ __forceinline__ i32x4 read(const uint8_t* lds, int t, int s) const {
-    return *reinterpret_cast<const i32x4*>(lds + at[s] + M * 128 * t);
+    return *reinterpret_cast<const i32x4*>(lds + at[s] + kM * 128 * t);
   }
 };
 
 // Rows that lie one after the other.
 template <int ROWS, int W>
 struct Along {
-  static constexpr bool kThroughRegisters = false;
   static constexpr int kLoads = ROWS / 8 / W;
   static constexpr int kBytes = ROWS * 128;
   static_assert(ROWS % (8 * W) == 0 && W % 2 == 0, "whole loads, and the same part of every load's rows");
@@ -207,25 +192,24 @@ struct Gathered {
 };
 
 // Memory rows are k; rows of the operand are columns there.
-template <int ROWS, int W, int M>
+template <int ROWS, int W>
 struct Across {
-  static constexpr bool kThroughRegisters = false;
   static constexpr int kParts = ROWS / 8;            // 16-byte parts of a memory row
   static constexpr int kEach = 64 / kParts;          // memory rows of one load of a wave
   static constexpr int kLoads = kTileK / kEach / W;
   static constexpr int kBytes = ROWS * 128;
   static_assert(kParts <= 64 && kParts >= 16 && kTileK % (kEach * W) == 0, "whole loads");
   // a lane's loads are kEach W memory rows apart: permutations that they have
-  static constexpr int kKinds = M == 32 || kEach * W % 16 == 0 ? 1 : 2;
-  static_assert(kEach * W % (M == 32 ? 4 : 8) == 0, "not more of them");
+  static constexpr int kKinds = kEach * W % 16 == 0 ? 1 : 2;
+  static_assert(kEach * W % 8 == 0, "not more of them");
 
   const uint8_t* base;                     // column 0 of the tile in memory row 0
   uint32_t ld;                             // bytes between memory rows
   uint32_t offset[kKinds];                 // of this lane's part of load p, from the first memory row of load 0's on
 
-  // How the parts of memory row k are permuted.  What 32 lanes read at once is four consecutive k of 64 bytes (M = 32), or
-  // twice four, eight apart, of 32 bytes.
-  static __device__ __forceinline__ int key(int k) { return M == 32 ? (k & 3) << 2 : (k & 3) << 1 | (k & 8); }
+  // How the parts of memory row k are permuted.  What 32 lanes read at once is twice four consecutive k, eight apart, of
+  // 32 bytes.
+  static __device__ __forceinline__ int key(int k) { return (k & 3) << 1 | (k & 8); }
 
   // `columns` of the tile's columns are inside
   __device__ __forceinline__ void init(int lane, int wave, const uint8_t* start, int64_t ld_bytes, int columns) {
@@ -253,21 +237,21 @@ struct Across {
   }
 };
 
-template <int ROWS, int M>
+template <int ROWS>
 struct AcrossFragments {
-  static constexpr int kKinds = M == 32 ? 4 : 8;     // tiles that the permutation tells apart
+  static constexpr int kKinds = 8;         // tiles that the permutation tells apart
   int at[kKinds];
   __device__ __forceinline__ void init(int lane, int first_row) {
-    const int k = lane / M * 8 + (lane >> 2 & 3), c = (lane % M >> 4) * 16 + (lane & 3) * 4;   // four consecutive columns
+    const int k = lane / kM * 8 + (lane >> 2 & 3), c = (lane & 3) * 4;   // four consecutive columns
 #pragma unroll
     for (int t = 0; t < kKinds; ++t) {
-      const int r = first_row + t * M + c;
-      at[t] = k * (ROWS * 2) + (((r >> 3) ^ Across<ROWS, 16, M>::key(k)) << 4) + (r >> 2 & 1) * 8;
+      const int r = first_row + t * kM + c;
+      at[t] = k * (ROWS * 2) + (((r >> 3) ^ Across<ROWS, 16>::key(k)) << 4) + (r >> 2 & 1) * 8;
     }
   }
   __device__ __forceinline__ i32x4 read(const uint8_t* lds, int t, int s) const {
     typedef __attribute__((address_space(3))) s16x4* Ptr;
-    const uint8_t* from = lds + at[t] + s * Matrix<M>::kK * (ROWS * 2);
+    const uint8_t* from = lds + at[t] + s * kInstrK * (ROWS * 2);
     union {
       s16x4 h[2];
       i32x4 v;
@@ -282,10 +266,10 @@ struct AcrossFragments {
 // and to LDS as bfloat16 (exactly), in the layout of rows along k.
 template <int ROWS, int W>
 struct FourBit {
-  static constexpr bool kThroughRegisters = true;
-  static constexpr int kLoads = ROWS / 32 / W;       // of 32 rows and both halves of a block
+  static constexpr int kActive = ROWS / 32 < W ? ROWS / 32 : W;    // waves that load
+  static constexpr int kLoads = ROWS / 32 / kActive; // of 32 rows and both halves of a block
   static constexpr int kBytes = ROWS * 128;
-  static_assert(ROWS % (32 * W) == 0, "whole loads");
+  static_assert(ROWS % (32 * kActive) == 0, "whole loads");
 
   const uint8_t* codes;                    // this lane's part of block 0 of its first row
   const uint8_t* scales;
@@ -308,10 +292,10 @@ struct FourBit {
     const bool in = blk * kTileK + half * kScaleGroup < K;
 #pragma unroll
     for (int p = 0; p < kLoads; ++p) {
-      const int64_t r = min(own + p * 32 * W, last);
+      const int64_t r = min(own + p * 32 * kActive, last);
       raw[p] = i32x4{0, 0, 0, 0};
       scale[p] = 127;
-      if (in) {
+      if (in && own < ROWS) {
         raw[p] = *reinterpret_cast<const i32x4*>(codes + r * ld_codes + blk * 32);
         scale[p] = scales[r * ld_scales + blk * 2];
       }
@@ -323,7 +307,8 @@ struct FourBit {
   }
   // load p of the block that was fetched last
   __device__ __forceinline__ void load(int p, uint8_t* lds) const {
-    const int r = own + p * 32 * W;
+    const int r = own + p * 32 * kActive;
+    if (kActive < W && own >= ROWS) return;          // the same for a wave
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       *reinterpret_cast<i32x4*>(lds + r * 128 + (((half * 4 + j) ^ along_key(r)) << 4)) =
@@ -332,16 +317,16 @@ struct FourBit {
 };
 
 // ---------------------------------------------------------------- a tile
-template <Mode MODE, int M, int WI, int WO, int IT, int OT, typename InnerFragments, typename OuterFragments>
+template <Mode MODE, int WI, int WO, int IT, int OT, typename InnerFragments, typename OuterFragments>
 struct Tile16 {
-  typedef typename Matrix<M>::Sum Sum;
+  typedef f32x4 Sum;
   static constexpr int kWaves = WI * WO, kThreads = kWaves * 64;
   static constexpr int kInner = WI * IT * 32, kOuter = WO * OT * 32;
   static constexpr int kInnerBytes = kInner * 128, kStageBytes = kInnerBytes + kOuter * 128;
   static constexpr int kOutBytes = 4096;             // of a wave, to bring its values into the output's order
   static constexpr int kLdsBytes = 2 * kStageBytes;  // the same bytes, after the last block
   static_assert(kLdsBytes >= kWaves * kOutBytes && kLdsBytes + kOuter * 4 <= 160 * 1024, "fits a compute unit");
-  static constexpr int kI = IT * 32 / M, kO = OT * 32 / M, kSteps = kTileK / Matrix<M>::kK;
+  static constexpr int kI = IT * 32 / kM, kO = OT * 32 / kM, kSteps = kTileK / kInstrK;
 
   static __device__ __forceinline__ int inner_first(int wave) { return wave % WI * (IT * 32); }
   static __device__ __forceinline__ int outer_first(int wave) { return wave / WI * (OT * 32); }
@@ -373,13 +358,13 @@ struct Tile16 {
                                              const uint8_t* lds, Sum (&acc)[kO][kI]) {
     constexpr int kLoads = Loads::kLoads, kReads = kSteps / 2 * (kI + kO), kSlots = kSteps * kI * kO / 4;
     const int blocks = (K - 1) / kTileK + 1;
-    i32x4 fi[kSteps][kI], fo[kSteps][kO];
+    i32x4 fi[kSteps][kI], fo[kSteps][kO], high, low;
 #pragma unroll
     for (int o = 0; o < kO; ++o)
 #pragma unroll
       for (int t = 0; t < kI; ++t)
 #pragma unroll
-        for (int i = 0; i < M * M / 64; ++i) acc[o][t][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) acc[o][t][i] = 0.0f;
     // fragment u of half `half` of a stage, in the order they are needed
     auto read = [&](const uint8_t* stage, int half, int u) {
       const int s = half * (kSteps / 2) + u / (kI + kO);
@@ -393,7 +378,14 @@ struct Tile16 {
 #pragma unroll
       for (int j = 0; j < kSlots; ++j) {
         const int m = q * kSlots + j, s = m / (kI * kO), o = m % (kI * kO) / kI, t = m % kI;
-        multiply(fi[s][t], fo[s][o], acc[o][t]);
+        if constexpr (MODE == kSplit) {
+          if (t == 0) split_f16(fo[s][o], high, low);
+          acc[o][t] = multiply_bf16(fi[s][t], high, acc[o][t]);
+          acc[o][t] = multiply_bf16(fi[s][t], low, acc[o][t]);
+        } else {
+          acc[o][t] = MODE == kBothF16 ? multiply_f16(fi[s][t], fo[s][o], acc[o][t])
+                                       : multiply_bf16(fi[s][t], fo[s][o], acc[o][t]);
+        }
         if (half >= 0) {
           // all are under way three quarters through
           constexpr int kEnd = kSlots * 3 / 4;
@@ -432,19 +424,6 @@ struct Tile16 {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
   }
 
-  static __device__ __forceinline__ void multiply(i32x4 a, i32x4 b, Sum& acc) {
-    if constexpr (MODE == kBothBf16) {
-      acc = Matrix<M>::bf16(a, b, acc);
-    } else if constexpr (MODE == kBothF16) {
-      acc = Matrix<M>::f16(a, b, acc);
-    } else {
-      i32x4 high, low;
-      split_f16(b, high, low);
-      acc = Matrix<M>::bf16(a, high, acc);
-      acc = Matrix<M>::bf16(a, low, acc);
-    }
-  }
-
   // Stores the wave's values: row(r) is outer row r's first element in the output or -1, some(r) whether it has values
   // (else zeros), `left` the inner values from the tile's start on.  Runs of 32 rows and 128 bytes pass through a part of
   // LDS that is the wave's own, so that memory gets whole lines.
@@ -481,24 +460,21 @@ struct Tile16 {
       for (int run = 0; run < IT * 32 / kRun; ++run) {
         // the run's values of 32 rows, four at a time
 #pragma unroll
-        for (int oo = 0; oo < 32 / M; ++oo)
+        for (int oo = 0; oo < 32 / kM; ++oo)
 #pragma unroll
-          for (int tt = 0; tt < kRun / M; ++tt)
+          for (int tt = 0; tt < kRun / kM; ++tt) {
+            const Sum& v = acc[o * (32 / kM) + oo][run * (kRun / kM) + tt];
+            const int i = tt * kM + 4 * (lane / kM);
+            uint8_t* to = own + place(oo * kM + lane % kM, i / kPart);
+            if constexpr (DTYPE == kF32) {
+              *reinterpret_cast<f32x4*>(to) = v;
+            } else {
+              u16 h[4];
 #pragma unroll
-            for (int q = 0; q < M * M / 256; ++q) {
-              const Sum& v = acc[o * (32 / M) + oo][run * (kRun / M) + tt];
-              const int i = tt * M + Matrix<M>::four(lane, q);
-              uint8_t* to = own + place(oo * M + lane % M, i / kPart);
-              if constexpr (DTYPE == kF32) {
-                *reinterpret_cast<f32x4*>(to) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-              } else {
-                u16 h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = DTYPE == kBf16 ? float_to_bf16(v[4 * q + j]) : float_to_f16(v[4 * q + j]);
-                *reinterpret_cast<uint2*>(to + (i & 4) * 2) =
-                    uint2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
-              }
+              for (int j = 0; j < 4; ++j) h[j] = DTYPE == kBf16 ? float_to_bf16(v[j]) : float_to_f16(v[j]);
+              *reinterpret_cast<uint2*>(to + (i & 4) * 2) = uint2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
             }
+          }
         const int64_t n = inner_first(wave) + run * kRun + lane % kParts * kPart;
 #pragma unroll
         for (int j = 0; j < 32 / kAtOnce; ++j) {
@@ -534,20 +510,20 @@ __device__ __forceinline__ int32_t source_of(const int32_t* rows, FastDiv topk, 
 
 enum Weights { kWeights, kWeightsTransposed, kWeights4 };
 
-template <int ROWS, int W, int M, Weights FORM>
+template <int ROWS, int W, Weights FORM>
 struct InnerOperand {
   typedef Along<ROWS, W> Loader;
-  typedef AlongFragments<M> Fragments;
+  typedef AlongFragments Fragments;
 };
-template <int ROWS, int W, int M>
-struct InnerOperand<ROWS, W, M, kWeightsTransposed> {
-  typedef Across<ROWS, W, M> Loader;
-  typedef AcrossFragments<ROWS, M> Fragments;
+template <int ROWS, int W>
+struct InnerOperand<ROWS, W, kWeightsTransposed> {
+  typedef Across<ROWS, W> Loader;
+  typedef AcrossFragments<ROWS> Fragments;
 };
-template <int ROWS, int W, int M>
-struct InnerOperand<ROWS, W, M, kWeights4> {
+template <int ROWS, int W>
+struct InnerOperand<ROWS, W, kWeights4> {
   typedef FourBit<ROWS, W> Loader;
-  typedef AlongFragments<M> Fragments;
+  typedef AlongFragments Fragments;
 };
 
 // The loads of a product's tile.
@@ -583,11 +559,11 @@ struct LinearLoads {
 };
 
 // WI IT 32 outputs of WO OT 32 rows.
-template <Mode MODE, int M, int WI, int WO, int IT, int OT, Weights FORM, bool FAR>
+template <Mode MODE, int WI, int WO, int IT, int OT, Weights FORM, bool FAR>
 struct LinearUnit {
-  typedef InnerOperand<WI * IT * 32, WI * WO, M, FORM> Inner;
+  typedef InnerOperand<WI * IT * 32, WI * WO, FORM> Inner;
   typedef Gathered<WO * OT * 32, WI * WO, FAR> Outer;
-  typedef Tile16<MODE, M, WI, WO, IT, OT, typename Inner::Fragments, AlongFragments<M>> Tile_;
+  typedef Tile16<MODE, WI, WO, IT, OT, typename Inner::Fragments, AlongFragments> Tile_;
 
   // rows t.row .. of group t.g, outputs i0 ..
   static __device__ __forceinline__ void run(const Linear16Args& a, const Tile& t, int i0, uint8_t* lds, int32_t* src) {
@@ -612,7 +588,7 @@ struct LinearUnit {
         loads.in.init(lane, wave, a.q + (n + i0) * (K / 2), a.scale + (n + i0) * (K / kScaleGroup), K, width - i0);
       loads.out.init(lane, wave, static_cast<const uint8_t*>(a.x), a.ld * 2, a.X, [&](int r) { return src[r]; });
       typename Inner::Fragments in;
-      AlongFragments<M> out;
+      AlongFragments out;
       in.init(lane, Tile_::inner_first(wave));
       out.init(lane, Tile_::outer_first(wave));
       Tile_::start(loads);
@@ -627,7 +603,7 @@ struct LinearUnit {
 // Tiles of 128 x 128, four waves, two workgroups to a compute unit.
 template <Mode MODE, Weights FORM, bool FAR>
 __global__ __launch_bounds__(256) void linear_small_kernel(Linear16Args a, int32_t columns) {
-  typedef LinearUnit<MODE, 16, 2, 2, 2, 2, FORM, FAR> Unit;
+  typedef LinearUnit<MODE, 2, 2, 2, 2, FORM, FAR> Unit;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int32_t src[128];
   const int32_t row_tiles = count_tiles(a.offsets, a.G, a.R, 128, true);
@@ -720,7 +696,7 @@ __global__ __launch_bounds__(512) void linear_large_kernel(Linear16Args a, int32
     int32_t row, column;
     band_order(die_order((int32_t)id, (int32_t)min(p.whole, (int64_t)gridDim.x)), p.full_rows, columns, row, column);
     const Tile t = find_large(a.offsets, a.G, a.R, row, false);
-    if (t.g >= 0) LinearUnit<MODE, 16, 4, 2, 2, 4, FORM, false>::run(a, t, column * 256, lds, src);
+    if (t.g >= 0) LinearUnit<MODE, 4, 2, 2, 4, FORM, false>::run(a, t, column * 256, lds, src);
     return;
   }
   id -= p.whole;
@@ -737,8 +713,43 @@ __global__ __launch_bounds__(512) void linear_large_kernel(Linear16Args a, int32
     column = (int32_t)(id % (2 * columns)) * 128;
   }
   if (t.g < 0 || column >= width) return;
-  if (t.rows > 128) LinearUnit<MODE, 16, 4, 2, 1, 4, FORM, false>::run(a, t, column, lds, src);
-  else LinearUnit<MODE, 16, 4, 2, 1, 2, FORM, false>::run(a, t, column, lds, src);
+  if (t.rows > 128) LinearUnit<MODE, 4, 2, 1, 4, FORM, false>::run(a, t, column, lds, src);
+  else LinearUnit<MODE, 4, 2, 1, 2, FORM, false>::run(a, t, column, lds, src);
+}
+
+inline int64_t small_blocks(int64_t R, int64_t width, int32_t G) {
+  // every group adds at most one tile that is not full, and a tile has a row
+  return (std::min(R, R / 128 + G) + 2) * ceil_div(width, 128);
+}
+
+inline int64_t large_blocks(int64_t R, int64_t width, int32_t G) {
+  const int64_t columns = ceil_div(width, 256);
+  return R / 256 * columns + kUnits / 2 + 2 * columns * std::min(R, (int64_t)G + 2);
+}
+
+inline bool large_suits(int64_t R, int64_t width, int32_t G) {
+  return R >= 128 * (int64_t)G && (R / 256 + G / 2) * ceil_div(width, 256) >= 128;
+}
+
+template <Mode MODE, Weights FORM>
+hipError_t launch_tiles(const Linear16Args& a, hipStream_t stream) {
+  const int64_t width = FORM == kWeightsTransposed ? a.C : a.N;
+  const bool far = a.X * a.ld * 2 >= (int64_t)kOutside;
+  if (!far && large_suits(a.R, width, a.G)) {
+    linear_large_kernel<MODE, FORM><<<dim3((unsigned)large_blocks(a.R, width, a.G)), dim3(512), 2 * 2 * 256 * 128,
+                                      stream>>>(a, (int32_t)ceil_div(width, 256));
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)small_blocks(a.R, width, a.G));
+  const int32_t columns = (int32_t)ceil_div(width, 128);
+  if (far) linear_small_kernel<MODE, FORM, true><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
+  else linear_small_kernel<MODE, FORM, false><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
+  return hipGetLastError();
+}
+
+// Workgroups of whichever form a product takes.
+inline int64_t tile_blocks(int64_t R, int64_t width, int32_t G) {
+  return std::max(small_blocks(R, width, G), large_suits(R, width, G) ? large_blocks(R, width, G) : 0);
 }
 
 }  // namespace eplb
