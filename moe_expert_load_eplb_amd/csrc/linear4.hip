@@ -1,9 +1,11 @@
 // The experts' products with 4-bit weights.
 //
 // What a code and its scale stand for has two significant bits, so it is a
-// bfloat16 number exactly: codes become bfloat16 operands of the matrix
-// instruction, one conversion instruction for two of them, and no scale is left
-// to apply to sums.  Half-precision rows are taken as two bfloat16 values each.
+// bfloat16 number exactly: against bfloat16 rows, codes become bfloat16 operands of
+// the matrix instruction, one conversion instruction for two of them, and no scale
+// is left to apply to sums.  Against half-precision rows, whose range a scale may
+// leave, they become half-precision operands without it, and each instruction's sum
+// over 32 of k, one scale's, is multiplied by it in 32 bits.
 #include "stream16.h"
 
 namespace eplb {
@@ -25,7 +27,7 @@ int64_t linear4_blocks(int64_t R, int64_t N, int64_t, int32_t G) {
 
 hipError_t launch_linear4(const Linear16Args& a, hipStream_t stream) {
   if (a.R == 0) return hipSuccess;
-  return a.dtype == kF16 ? launch_form<kSplit>(a, stream) : launch_form<kBothBf16>(a, stream);
+  return a.dtype == kF16 ? launch_form<kScaled>(a, stream) : launch_form<kBothBf16>(a, stream);
 }
 
 }  // namespace eplb

@@ -58,6 +58,22 @@ struct StreamChunk {
   i32x4 w[2];
 };
 
+// Lane 16 q + c holds M[q][s] in element s: from now on M[s][q].
+__device__ __forceinline__ void turn_quads(i32x4& v) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const auto p = __builtin_amdgcn_permlane32_swap((uint32_t)v[s], (uint32_t)v[s + 2], false, false);
+    v[s] = (int)p[0];
+    v[s + 2] = (int)p[1];
+  }
+#pragma unroll
+  for (int s = 0; s < 4; s += 2) {
+    const auto p = __builtin_amdgcn_permlane16_swap((uint32_t)v[s], (uint32_t)v[s + 1], false, false);
+    v[s] = (int)p[0];
+    v[s + 1] = (int)p[1];
+  }
+}
+
 // `each` sets of 16 outputs to a workgroup, `columns` workgroups to a row of tiles
 template <Mode MODE, bool FOUR, int MT, int KS, int D>
 __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Linear16Args a, int32_t columns, int32_t each) {
@@ -175,23 +191,42 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Lin
         const uint8_t* rows_at = lds + (stage & 1) * kStreamStage;
         const int c_in = share * Shape::kEach + (i + set) % Shape::kEach;    // its place in the stage
         if (FOUR && u % kBatch == 0) load_s(i + kBatch, scale[u / kBatch + 1 & 1]);
+        auto rows_of = [&](int m, int at) {       // eight of k, part `at` of the chunk, of row `col` of tile m
+          const int block = c_in * (Shape::kChunk / kTileK) + (at >> 3), r = m * 16 + col;
+          return *reinterpret_cast<const i32x4*>(rows_at + block * kBlockBytes + r * 128 + (((at & 7) ^ along_key(r)) << 4));
+        };
+        if constexpr (MODE == kScaled) {
 #pragma unroll
-        for (int s = 0; s < (FOUR ? 8 : 2); ++s) {
-          i32x4 w = part[u % D].w[FOUR ? s >> 2 : s];
-          if constexpr (FOUR)
-            w = four_bit_values(w[s & 3], __uint_as_float(scale[u / kBatch & 1][u % kBatch][s >> 2] << 23));
+          for (int h = 0; h < 2; ++h) {
+            // An instruction's k has to be one block of 32: quad s has block s, and register q becomes part of quad q.
+            i32x4 w = part[u % D].w[h], scales;
+            turn_quads(w);
+            const int mine = (int)scale_bits(scale[u / kBatch & 1][u % kBatch][h]);
+            scales = i32x4{mine, mine, mine, mine};
+            turn_quads(scales);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            // which eight of the chunk's k the weights are of
-            const int at = FOUR ? (s >> 2) * 16 + quad * 4 + (s & 3) : s * 4 + quad, r = m * 16 + col;
-            const int block = c_in * (Shape::kChunk / kTileK) + (at >> 3);
-            const i32x4 x = *reinterpret_cast<const i32x4*>(rows_at + block * kBlockBytes + r * 128 +
-                                                            (((at & 7) ^ along_key(r)) << 4));
-            if constexpr (MODE == kSplit) {
-              i32x4 high, low;
-              split_f16(x, high, low);
-              acc[m] = multiply_bf16(w, low, multiply_bf16(w, high, acc[m]));
-            } else {
+            for (int s = 0; s < 4; ++s) {
+              const i32x4 values = four_bit_halves(w[s]);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                // the rows first: a lane's sums are of one output then, and have one scale
+                const f32x4 products =
+                    multiply_f16(rows_of(m, h * 16 + s * 4 + quad), values, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = fmaf(__int_as_float(scales[s]), products[j], acc[m][j]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < (FOUR ? 8 : 2); ++s) {
+            i32x4 w = part[u % D].w[FOUR ? s >> 2 : s];
+            if constexpr (FOUR)
+              w = four_bit_values(w[s & 3], __uint_as_float(scale[u / kBatch & 1][u % kBatch][s >> 2] << 23));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              // which eight of the chunk's k the weights are of
+              const i32x4 x = rows_of(m, FOUR ? (s >> 2) * 16 + quad * 4 + (s & 3) : s * 4 + quad);
               acc[m] = MODE == kBothF16 ? multiply_f16(w, x, acc[m]) : multiply_bf16(w, x, acc[m]);
             }
           }
@@ -215,16 +250,23 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Lin
 #pragma unroll
       for (int s = 1; s < KS; ++s) acc[m] += sums[wave + s][m][lane];
   }
-  const int at = n0 + quad * 4, left = min(a.N, n0 + outputs) - at;
-  if (left <= 0) return;
   auto store = [&](auto type) {
     constexpr int kType = decltype(type)::value;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int r = m * 16 + col;
-      if (r < t.rows)
-        store_four<kType>(a.y, (int64_t)(t.row + r) * a.N + at, left, a.N % 4 == 0,
-                          src[r] >= 0 ? acc[m] : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      if constexpr (MODE == kScaled) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = m * 16 + quad * 4 + j;
+          if (r < t.rows && col < outputs)
+            store_float(a.y, kType, (int64_t)(t.row + r) * a.N + n0 + col, src[r] >= 0 ? acc[m][j] : 0.0f);
+        }
+      } else {
+        const int r = m * 16 + col;
+        if (r < t.rows)
+          store_four<kType>(a.y, (int64_t)(t.row + r) * a.N + n0 + quad * 4, outputs - quad * 4, a.N % 4 == 0,
+                            src[r] >= 0 ? acc[m] : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      }
     }
   };
   if (a.y_dtype == kF32) store(std::integral_constant<int, kF32>());

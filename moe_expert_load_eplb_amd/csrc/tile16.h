@@ -71,28 +71,11 @@ __device__ __forceinline__ uint32_t lds_address(uint8_t* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)p);
 }
 
-// What the two operands hold.  kSplit: the first bfloat16, the second half precision, which is taken as two bfloat16
-// values that sum to it exactly (11 significant bits are 8 and 3).
-enum Mode { kBothBf16, kBothF16, kSplit };
-
-// Eight half-precision values as bfloat16: the first 8 significant bits, and what they leave (of an infinity something
-// finite).
-__device__ __forceinline__ void split_f16(i32x4 v, i32x4& high, i32x4& low) {
-  const half8 x = __builtin_bit_cast(half8, v);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t top[2], rest[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float f = (float)x[2 * j + e];
-      top[e] = __float_as_uint(f);
-      const float fine = __builtin_amdgcn_fmed3f(f, -65504.0f, 65504.0f);
-      rest[e] = __float_as_uint(fine - __uint_as_float(__float_as_uint(fine) & 0xFFFF0000u));   // exact: at most 3 bits
-    }
-    high[j] = (int)__builtin_amdgcn_perm(top[1], top[0], 0x07060302u);
-    low[j] = (int)__builtin_amdgcn_perm(rest[1], rest[0], 0x07060302u);
-  }
-}
+// What the two operands hold.  kScaled: the first 4-bit values without their scales, as half precision, the second half
+// precision; what an instruction adds up, 32 of k, is multiplied by the scales then.  (A value times its scale is a
+// bfloat16 number, but not one of half precision; with the rows as two bfloat16 numbers each, 16384 rows on 9, 4096 x
+// 4096, took 1210 us, so 855.)
+enum Mode { kBothBf16, kBothF16, kScaled };
 
 // Eight 4-bit values times a power of two as bfloat16.  Of the scale only the exponent counts; all bits of it set (255
 // of a scale byte): NaN.
@@ -103,6 +86,21 @@ __device__ __forceinline__ i32x4 four_bit_values(int codes, float scale) {
   v[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)codes, scale, 2));
   v[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((uint32_t)codes, scale, 3));
   return v;
+}
+
+// Eight 4-bit values as half precision.
+__device__ __forceinline__ i32x4 four_bit_halves(int codes) {
+  i32x4 v;
+  v[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)codes, 1.0f, 0));
+  v[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)codes, 1.0f, 1));
+  v[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)codes, 1.0f, 2));
+  v[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)codes, 1.0f, 3));
+  return v;
+}
+
+// What a scale byte stands for, 2^(byte - 127) or NaN (255), as a float whose lower half is zeros.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) {
+  return byte << 23 | (byte == 0 || byte == 255 ? 0x00400000u : 0);
 }
 
 // ---------------------------------------------------------------- the matrix instruction
@@ -263,8 +261,9 @@ struct AcrossFragments {
 };
 
 // An operand of 4-bit values along k, its blocks of 32 scaled by powers of two: from memory to registers a block ahead,
-// and to LDS as bfloat16 (exactly), in the layout of rows along k.
-template <int ROWS, int W>
+// and to LDS as bfloat16 (exactly), in the layout of rows along k.  SCALED: without the scales, as half precision; the
+// scales follow the block, in bfloat16, those of all rows' first half and then those of the second.
+template <int ROWS, int W, bool SCALED>
 struct FourBit {
   static constexpr int kActive = ROWS / 32 < W ? ROWS / 32 : W;    // waves that load
   static constexpr int kLoads = ROWS / 32 / kActive; // of 32 rows and both halves of a block
@@ -306,13 +305,14 @@ struct FourBit {
     for (int p = 0; p < kLoads; ++p) asm volatile("" : "+v"(raw[p]), "+v"(scale[p]));
   }
   // load p of the block that was fetched last
-  __device__ __forceinline__ void load(int p, uint8_t* lds) const {
+  __device__ __forceinline__ void load(int p, uint8_t* lds, uint8_t* lds_scales) const {
     const int r = own + p * 32 * kActive;
     if (kActive < W && own >= ROWS) return;          // the same for a wave
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       *reinterpret_cast<i32x4*>(lds + r * 128 + (((half * 4 + j) ^ along_key(r)) << 4)) =
-          four_bit_values(raw[p][j], __uint_as_float(scale[p] << 23));
+          SCALED ? four_bit_halves(raw[p][j]) : four_bit_values(raw[p][j], __uint_as_float(scale[p] << 23));
+    if (SCALED) reinterpret_cast<u16*>(lds_scales)[half * ROWS + r] = (u16)(scale_bits(scale[p]) >> 16);
   }
 };
 
@@ -322,7 +322,8 @@ struct Tile16 {
   typedef f32x4 Sum;
   static constexpr int kWaves = WI * WO, kThreads = kWaves * 64;
   static constexpr int kInner = WI * IT * 32, kOuter = WO * OT * 32;
-  static constexpr int kInnerBytes = kInner * 128, kStageBytes = kInnerBytes + kOuter * 128;
+  static constexpr int kInnerBytes = kInner * 128, kScales = kInnerBytes + kOuter * 128;
+  static constexpr int kStageBytes = kScales + (MODE == kScaled ? kInner * 4 : 0);
   static constexpr int kOutBytes = 4096;             // of a wave, to bring its values into the output's order
   static constexpr int kLdsBytes = 2 * kStageBytes;  // the same bytes, after the last block
   static_assert(kLdsBytes >= kWaves * kOutBytes && kLdsBytes + kOuter * 4 <= 160 * 1024, "fits a compute unit");
@@ -358,7 +359,12 @@ struct Tile16 {
                                              const uint8_t* lds, Sum (&acc)[kO][kI]) {
     constexpr int kLoads = Loads::kLoads, kReads = kSteps / 2 * (kI + kO), kSlots = kSteps * kI * kO / 4;
     const int blocks = (K - 1) / kTileK + 1;
-    i32x4 fi[kSteps][kI], fo[kSteps][kO], high, low;
+    i32x4 fi[kSteps][kI], fo[kSteps][kO];
+    // kScaled: the scales of a lane's four inner values of each tile, two to a register; those of the current tile; and the
+    // products of the instruction before
+    const int at_scales = kScales + (inner_first(threadIdx.x >> 6) + 4 * ((threadIdx.x & 63) / kM)) * 2;
+    uint2 scales[kSteps][kI];
+    f32x4 scale, before;
 #pragma unroll
     for (int o = 0; o < kO; ++o)
 #pragma unroll
@@ -372,17 +378,26 @@ struct Tile16 {
       if (u == 0) fo[s][0] = out.read(stage + kInnerBytes, 0, s);
       else if (u <= kI) fi[s][u - 1] = in.read(stage, u - 1, s);
       else fo[s][u - kI] = out.read(stage + kInnerBytes, u - kI, s);
+      if (MODE == kScaled && u < kI)
+        scales[s][u] = *reinterpret_cast<const uint2*>(stage + at_scales + (s * kInner + u * kM) * 2);
     };
     // the products of quarter q; under them the fragments of half `half` of a stage, or a part of the loads
     auto quarter = [&](int q, const uint8_t* stage, int half, int part, uint32_t slot) {
 #pragma unroll
       for (int j = 0; j < kSlots; ++j) {
-        const int m = q * kSlots + j, s = m / (kI * kO), o = m % (kI * kO) / kI, t = m % kI;
-        if constexpr (MODE == kSplit) {
-          if (t == 0) split_f16(fo[s][o], high, low);
-          acc[o][t] = multiply_bf16(fi[s][t], high, acc[o][t]);
-          acc[o][t] = multiply_bf16(fi[s][t], low, acc[o][t]);
+        const int m = q * kSlots + j, s = m / (kI * kO);
+        if constexpr (MODE == kScaled) {
+          static_assert(kSlots % kO == 0 && kInstrK == kScaleGroup, "a tile's scale is looked up within the quarter");
+          const int t = m % (kI * kO) / kO, o = j % kO;
+          const f32x4 products = multiply_f16(fi[s][t], fo[s][o], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          if (j > 0) add_scaled(acc[(j - 1) % kO][(m - 1) % (kI * kO) / kO], scale, before);
+          if (o == 0)
+            scale = f32x4{__uint_as_float(scales[s][t].x << 16), __uint_as_float(scales[s][t].x & 0xFFFF0000u),
+                          __uint_as_float(scales[s][t].y << 16), __uint_as_float(scales[s][t].y & 0xFFFF0000u)};
+          before = products;
+          if (j == kSlots - 1) add_scaled(acc[o][t], scale, before);
         } else {
+          const int o = m % (kI * kO) / kI, t = m % kI;
           acc[o][t] = MODE == kBothF16 ? multiply_f16(fi[s][t], fo[s][o], acc[o][t])
                                        : multiply_bf16(fi[s][t], fo[s][o], acc[o][t]);
         }
@@ -416,6 +431,11 @@ struct Tile16 {
       quarter(3, lds + (kStageBytes - slot), 0, -1, 0);
     }
     wait_for_loads<0>();                   // both stages are free again, and none lands in LDS after the end
+  }
+
+  static __device__ __forceinline__ void add_scaled(Sum& to, const f32x4& scale, const f32x4& products) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = fmaf(scale[i], products[i], to[i]);
   }
 
   // Waits for all but the last N loads of every wave.
@@ -510,19 +530,19 @@ __device__ __forceinline__ int32_t source_of(const int32_t* rows, FastDiv topk, 
 
 enum Weights { kWeights, kWeightsTransposed, kWeights4 };
 
-template <int ROWS, int W, Weights FORM>
+template <int ROWS, int W, Weights FORM, Mode MODE>
 struct InnerOperand {
   typedef Along<ROWS, W> Loader;
   typedef AlongFragments Fragments;
 };
-template <int ROWS, int W>
-struct InnerOperand<ROWS, W, kWeightsTransposed> {
+template <int ROWS, int W, Mode MODE>
+struct InnerOperand<ROWS, W, kWeightsTransposed, MODE> {
   typedef Across<ROWS, W> Loader;
   typedef AcrossFragments<ROWS> Fragments;
 };
-template <int ROWS, int W>
-struct InnerOperand<ROWS, W, kWeights4> {
-  typedef FourBit<ROWS, W> Loader;
+template <int ROWS, int W, Mode MODE>
+struct InnerOperand<ROWS, W, kWeights4, MODE> {
+  typedef FourBit<ROWS, W, MODE == kScaled> Loader;
   typedef AlongFragments Fragments;
 };
 
@@ -549,7 +569,7 @@ struct LinearLoads {
   // what goes through registers first: it was waited for, and nothing that was issued since is waited for with it
   __device__ __forceinline__ void issue(int i, uint32_t slot) const {
     if (i < Inner::kLoads) {
-      if constexpr (FORM == kWeights4) in.load(i, lds + slot);
+      if constexpr (FORM == kWeights4) in.load(i, lds + slot, lds + slot + Inner::kBytes + Outer::kBytes);
       else if constexpr (FORM == kWeightsTransposed) in.load(i, from, wave, at + slot);
       else in.load(i, blk, K, wave, at + slot);
     } else {
@@ -561,7 +581,7 @@ struct LinearLoads {
 // WI IT 32 outputs of WO OT 32 rows.
 template <Mode MODE, int WI, int WO, int IT, int OT, Weights FORM, bool FAR>
 struct LinearUnit {
-  typedef InnerOperand<WI * IT * 32, WI * WO, FORM> Inner;
+  typedef InnerOperand<WI * IT * 32, WI * WO, FORM, MODE> Inner;
   typedef Gathered<WO * OT * 32, WI * WO, FAR> Outer;
   typedef Tile16<MODE, WI, WO, IT, OT, typename Inner::Fragments, AlongFragments> Tile_;
 
@@ -602,7 +622,7 @@ struct LinearUnit {
 
 // Tiles of 128 x 128, four waves, two workgroups to a compute unit.
 template <Mode MODE, Weights FORM, bool FAR>
-__global__ __launch_bounds__(256) void linear_small_kernel(Linear16Args a, int32_t columns) {
+__global__ __launch_bounds__(256, 2) void linear_small_kernel(Linear16Args a, int32_t columns) {
   typedef LinearUnit<MODE, 2, 2, 2, 2, FORM, FAR> Unit;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int32_t src[128];
@@ -696,7 +716,15 @@ __global__ __launch_bounds__(512) void linear_large_kernel(Linear16Args a, int32
     int32_t row, column;
     band_order(die_order((int32_t)id, (int32_t)min(p.whole, (int64_t)gridDim.x)), p.full_rows, columns, row, column);
     const Tile t = find_large(a.offsets, a.G, a.R, row, false);
-    if (t.g >= 0) LinearUnit<MODE, 4, 2, 2, 4, FORM, false>::run(a, t, column * 256, lds, src);
+    if (t.g < 0) return;
+    if constexpr (MODE == kScaled) {
+      // scales take the registers that the sums of half the rows would: one half after the other
+      LinearUnit<MODE, 4, 2, 2, 2, FORM, false>::run(a, Tile{t.g, t.row, 128}, column * 256, lds, src);
+      __syncthreads();
+      LinearUnit<MODE, 4, 2, 2, 2, FORM, false>::run(a, Tile{t.g, t.row + 128, 128}, column * 256, lds, src);
+    } else {
+      LinearUnit<MODE, 4, 2, 2, 4, FORM, false>::run(a, t, column * 256, lds, src);
+    }
     return;
   }
   id -= p.whole;
@@ -731,19 +759,21 @@ inline bool large_suits(int64_t R, int64_t width, int32_t G) {
   return R >= 128 * (int64_t)G && (R / 256 + G / 2) * ceil_div(width, 256) >= 128;
 }
 
+// Two stages of a block of both operands, and of scales where they are apart.
+constexpr unsigned lds_bytes(Mode mode, int side) { return 2 * (2 * side * 128 + (mode == kScaled ? side * 4 : 0)); }
+
 template <Mode MODE, Weights FORM>
 hipError_t launch_tiles(const Linear16Args& a, hipStream_t stream) {
   const int64_t width = FORM == kWeightsTransposed ? a.C : a.N;
   const bool far = a.X * a.ld * 2 >= (int64_t)kOutside;
   if (!far && large_suits(a.R, width, a.G)) {
-    linear_large_kernel<MODE, FORM><<<dim3((unsigned)large_blocks(a.R, width, a.G)), dim3(512), 2 * 2 * 256 * 128,
-                                      stream>>>(a, (int32_t)ceil_div(width, 256));
+    linear_large_kernel<MODE, FORM><<<dim3((unsigned)large_blocks(a.R, width, a.G)), dim3(512), lds_bytes(MODE, 256), stream>>>(a, (int32_t)ceil_div(width, 256));
     return hipGetLastError();
   }
   const dim3 grid((unsigned)small_blocks(a.R, width, a.G));
   const int32_t columns = (int32_t)ceil_div(width, 128);
-  if (far) linear_small_kernel<MODE, FORM, true><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
-  else linear_small_kernel<MODE, FORM, false><<<grid, dim3(256), 2 * 2 * 128 * 128, stream>>>(a, columns);
+  if (far) linear_small_kernel<MODE, FORM, true><<<grid, dim3(256), lds_bytes(MODE, 128), stream>>>(a, columns);
+  else linear_small_kernel<MODE, FORM, false><<<grid, dim3(256), lds_bytes(MODE, 128), stream>>>(a, columns);
   return hipGetLastError();
 }
 
