@@ -1,17 +1,19 @@
-"""The router and the experts' product as differentiable functions of torch.
+"""The router, the experts' products and their join as differentiable functions
+of torch.
 
 Thin wrappers: forward and backward are the calls of the package, chained as a
 training step chains them.  ``route`` carries gradients through the weights and
-the balance loss to the logits; ``expert_linear`` through the product to the
-rows and to the weights.  Neither has a second derivative: asking for one raises
-RuntimeError.
+the balance loss to the logits; ``expert_linear`` (8-bit blocks) and
+``expert_linear16`` (16 bits) through the product to the rows and to the weights;
+``combine`` through the weighted sum to the experts' rows and to the router's
+weights.  None has a second derivative: asking for one raises RuntimeError.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (expert_matmul, expert_wgrad, gate_backward, gate_loss, quantize_columns, quantize_rows,
-               quantize_weights)
+from . import (combine_rows, combine_rows_backward, expert_matmul, expert_matmul16, expert_wgrad, expert_wgrad16,
+               gate_backward, gate_loss, quantize_columns, quantize_rows, quantize_weights)
 
 
 class _Final(torch.autograd.Function):
@@ -23,7 +25,7 @@ class _Final(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *_):
-        raise RuntimeError("route and expert_linear have no second derivative")
+        raise RuntimeError("route, the expert_linears and combine have no second derivative")
 
 
 def _final(grad, *through):
@@ -108,3 +110,75 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows:
     if rows is not None and rows.shape[0] != x.shape[0] * K:
         raise ValueError(f"rows must be [{x.shape[0] * K}]")
     return _ExpertLinear.apply(x, w, offsets, rows, place, K, x_grad)
+
+
+class _ExpertLinear16(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets, rows, place, K):
+        ctx.save_for_backward(x, w, offsets, rows, place)
+        ctx.K = K
+        return expert_matmul16(x, w, offsets, rows=rows, K=K)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets, rows, place = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            # a token's rows are summed in 32 bits, in the order of its choices, and rounded once
+            dx = expert_matmul16(dy, w, offsets, transpose=True, dtype=x.dtype if rows is None else torch.float32)
+            if rows is not None:
+                dx = combine_rows(dx, place.view(x.shape[0], ctx.K), None, dtype=x.dtype)
+        if ctx.needs_input_grad[1]:
+            dw = expert_wgrad16(dy, x, offsets, rows=rows, K=ctx.K, dtype=w.dtype)
+        return _final(dx, dy, w), _final(dw, dy, x), None, None, None, None
+
+
+def expert_linear16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                    place: torch.Tensor | None = None, K: int = 1) -> torch.Tensor:
+    """Every grouped row times the transposed weights of its expert, in 16 bits
+    with 32-bit sums, differentiable in x and w.
+
+    x [T, C], w [G, N, C] of one type, bfloat16 or float16, C a multiple of 8, and
+    N too where x or w needs a gradient; offsets, rows and place: one layer of
+    group_rows' outputs (offsets, order, place), rows and place together.  Without
+    them x is in grouped order itself.  Returns [R, N]."""
+    if x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1]:
+        raise ValueError("x [T, C] and w [G, N, C] expected")
+    if x.shape[1] % 8 != 0:
+        raise ValueError(f"C must be a multiple of 8, got {x.shape[1]}")
+    if w.shape[1] % 8 != 0 and torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+        raise ValueError(f"N must be a multiple of 8 for the gradients, got {w.shape[1]}")
+    if (rows is None) != (place is None):
+        raise ValueError("rows and place go together")
+    if rows is not None and (rows.shape[0] != x.shape[0] * K or place.numel() != x.shape[0] * K):
+        raise ValueError(f"rows and place must be [{x.shape[0] * K}]")
+    return _ExpertLinear16.apply(x, w, offsets, rows, place, K)
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, place, order, dtype):
+        ctx.save_for_backward(y, weights, place, order)
+        return combine_rows(y, place, weights, dtype=dtype)
+
+    @staticmethod
+    def backward(ctx, d_out):
+        y, weights, place, order = ctx.saved_tensors
+        dy, dw = combine_rows_backward(d_out.contiguous(), y, place, order, weights)
+        return (_final(dy, d_out, weights) if ctx.needs_input_grad[0] else None,
+                _final(dw, d_out, y) if ctx.needs_input_grad[1] else None, None, None, None)
+
+
+def combine(y: torch.Tensor, weights: torch.Tensor, place: torch.Tensor, order: torch.Tensor,
+            dtype: torch.dtype | None = None) -> torch.Tensor:
+    """The experts' rows joined to tokens, out[t] = sum over k of weights[t, k] *
+    y[place[t, k]], differentiable in y and weights.
+
+    y [T * K, C]; weights [T, K] float32; place and order: one layer of
+    group_rows' outputs.  Returns [T, C] in ``dtype`` (y's without)."""
+    if y.dim() != 2 or weights.dim() != 2 or y.shape[0] != weights.numel():
+        raise ValueError("y [T * K, C] and weights [T, K] expected")
+    if place.numel() != weights.numel() or order.numel() != weights.numel():
+        raise ValueError(f"place and order must be [{weights.numel()}]")
+    return _Combine.apply(y, weights, place, order, dtype)
