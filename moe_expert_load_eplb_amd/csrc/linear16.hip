@@ -146,7 +146,7 @@ hipError_t launch_wgrad_form(const Wgrad16Args& a, hipStream_t stream) {
 
 int64_t linear16_blocks(int64_t R, int64_t outputs, int64_t, int32_t G, bool transpose) {
   const int64_t tiles = tile_blocks(R, outputs, G);
-  return !transpose && stream_suits(R, G, false) ? std::max(tiles, stream_blocks(R, outputs, G, false)) : tiles;
+  return !transpose && stream_suits(R, G) ? std::max(tiles, stream_blocks(R, outputs, G, false)) : tiles;
 }
 
 int64_t wgrad16_blocks(int64_t, int64_t N, int64_t C, int32_t G) {
@@ -158,7 +158,7 @@ namespace {
 template <Mode MODE>
 hipError_t launch_form(const Linear16Args& a, bool transpose, hipStream_t stream) {
   if (transpose) return launch_tiles<MODE, kWeightsTransposed>(a, stream);
-  if (stream_suits(a.R, a.G, false) && a.X * a.ld * 2 < (int64_t)kOutside) return launch_stream<MODE, false>(a, stream);
+  if (stream_suits(a.R, a.G) && a.X * a.ld * 2 < (int64_t)kOutside) return launch_stream<MODE, false>(a, stream);
   return launch_tiles<MODE, kWeights>(a, stream);
 }
 

@@ -14,7 +14,7 @@ namespace {
 
 template <Mode MODE>
 hipError_t launch_form(const Linear16Args& a, hipStream_t stream) {
-  if (stream_suits(a.R, a.G, true) && a.X * a.ld * 2 < (int64_t)kOutside) return launch_stream<MODE, true>(a, stream);
+  if (stream_suits(a.R, a.G) && a.X * a.ld * 2 < (int64_t)kOutside) return launch_stream<MODE, true>(a, stream);
   return launch_tiles<MODE, kWeights4>(a, stream);
 }
 
@@ -22,7 +22,7 @@ hipError_t launch_form(const Linear16Args& a, hipStream_t stream) {
 
 int64_t linear4_blocks(int64_t R, int64_t N, int64_t, int32_t G) {
   const int64_t tiles = tile_blocks(R, N, G);
-  return stream_suits(R, G, true) ? std::max(tiles, stream_blocks(R, N, G, true)) : tiles;
+  return stream_suits(R, G) ? std::max(tiles, stream_blocks(R, N, G, true)) : tiles;
 }
 
 hipError_t launch_linear4(const Linear16Args& a, hipStream_t stream) {

@@ -106,12 +106,14 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Lin
           resource(from_w), (at_w + s * 64) | (k + s * (Shape::kChunk / 2) < a.C ? 0 : kOutside), c * 128, 0);
   };
   // This wave's chunk i.  A stage's are shared out in runs, so that what lies next to each other is asked for together.
-  // Rows of weights are often a power of two apart, and then their chunks of one place all lie in one channel of the cache:
-  // each workgroup starts with another stage, and each set of waves with another chunk of its run.
-  const int stages = (a.C - 1) / Shape::kStageK + 1, turn = (int)(blockIdx.x % stages);
+  // Rows of weights are often a power of two apart, and then their chunks of one place all lie in one channel of a die's
+  // cache: each workgroup of a die (every eighth) starts with another stage, and each set of waves with another chunk of
+  // its run.
+  const int stages = (a.C - 1) / Shape::kStageK + 1, turn = (int)((blockIdx.x >> 3) % stages),
+            chunk_turn = set + (int)((blockIdx.x >> 3) / stages % Shape::kEach);
   auto stage_of = [&](int stage) { return stage >= stages ? stages : stage + turn < stages ? stage + turn : stage + turn - stages; };
   auto chunk = [&](int i) {
-    return (stage_of(i / Shape::kEach) * KS + share) * Shape::kEach + (i + set) % Shape::kEach;
+    return (stage_of(i / Shape::kEach) * KS + share) * Shape::kEach + (i + chunk_turn) % Shape::kEach;
   };
   // What rows names is asked for first, and the weights before it is looked at: loads return in order.
   static_assert(Shape::kRows <= kStreamWaves * 64, "a thread to a row");
@@ -189,7 +191,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Lin
           }
         }
         const uint8_t* rows_at = lds + (stage & 1) * kStreamStage;
-        const int c_in = share * Shape::kEach + (i + set) % Shape::kEach;    // its place in the stage
+        const int c_in = share * Shape::kEach + (i + chunk_turn) % Shape::kEach;    // its place in the stage
         if (FOUR && u % kBatch == 0) load_s(i + kBatch, scale[u / kBatch + 1 & 1]);
         auto rows_of = [&](int m, int at) {       // eight of k, part `at` of the chunk, of row `col` of tile m
           const int block = c_in * (Shape::kChunk / kTileK) + (at >> 3), r = m * 16 + col;
@@ -282,27 +284,31 @@ struct StreamPlan {
 // Tiles of `tile` rows: every group adds at most one that is not full, and a tile has a row.
 inline int64_t row_tiles(int64_t R, int32_t G, int tile) { return std::min(R, R / tile + G) + 2; }
 
-// Few rows: past these a tile of 128 x 128 reads the weights as fast, or, with 4-bit weights, a second tile of rows costs
-// what a larger tile saves.  4096 x 2048 on 9, 64 rows each: 44 us here, 50 in tiles, 85 rows: 47 and 50; 4-bit weights, 64
-// rows: 33 and 59, of 64 groups with 80 rows: 58 and 47.
-inline bool stream_suits(int64_t R, int32_t G, bool four) { return R <= (four ? 64 : 96) * (int64_t)G; }
+// Few rows: past these a tile of 128 x 128 is as good or better.  4096 x 2048 on 9, 64 rows each: 46 us here, 50 in tiles;
+// of 64 groups with 80 rows: 72 and 61; 4-bit weights, 64 rows: 33 and 59, of 64 groups with 80: 58 and 47.
+inline bool stream_suits(int64_t R, int32_t G) { return R <= 64 * (int64_t)G; }
 
 // The busiest compute unit ends last, and what it can have in flight is the same whatever is on it: the form is the one
-// for which ceil(workgroups / compute units) times the sets of outputs of a workgroup, and one more for its start and end,
-// is least.  512 rows on 9, 4096 x 2048 outputs: 40 us with 6 sets of 64 rows to a workgroup (224 of them), 65 with 5 (265).
+// for which ceil(workgroups / compute units) times what a workgroup costs, its sets of outputs and its start and end, is
+// least.  512 rows on 9, 4096 x 2048 outputs: 40 us with 6 sets of 64 rows to a workgroup (224 of them), 65 with 5 (265).
 inline StreamPlan plan_stream(int64_t R, int64_t N, int32_t G, bool four) {
   constexpr int kUnits = 256;
-  const double mean = (double)R / G, spread = std::sqrt(mean);      // of rows to a group, as chance deals them out
+  // rows to a group: as chance deals them out, and a fifth of the mean besides, which a balanced placement leaves
+  const double mean = (double)R / G, spread = std::sqrt(mean + 0.04 * mean * mean);
   StreamPlan best{};
   double least = 0;
   for (int mt = 1; mt <= (four ? 4 : 8); mt *= 2) {
     // what an output of a tile costs, against one of a tile of 16 rows: the weights are the same, but more is multiplied
     const double weight = four ? (mt == 1 ? 1 : mt == 2 ? 1.15 : 1.6) : (mt == 1 ? 1 : mt == 2 ? 1.02 : mt == 4 ? 1.06 : 1.3);
-    double tiles = 0;
-    for (double z : {-1.2, -0.4, 0.4, 1.2}) tiles += 0.25 * std::max(1.0, std::ceil((mean + z * spread) / (16 * mt)));
-    tiles = std::min<double>((double)R, tiles * G);
+    double tiles = G, more_of_them = 0;    // and how many groups have another one; what chance may add
+    for (int t = 1; t <= 64 && 16 * mt * t < mean + 3 * spread; ++t) {
+      const double more = 0.5 * std::erfc((16 * mt * t - mean) / (spread * std::sqrt(2.0)));
+      tiles += G * more;
+      more_of_them += std::sqrt(G * more * (1 - more));
+    }
     for (int each = 1; each <= kStreamWaves; ++each) {
-      const double cost = weight * (each + 1) * std::ceil(tiles * ceil_div(N, 16 * each) / kUnits);
+      auto turns = [&](double t) { return std::ceil(std::min((double)R, t) * ceil_div(N, 16 * each) / kUnits); };
+      const double cost = (weight * each + 1 + 0.25 * mt) * (turns(tiles) + turns(tiles + more_of_them));
       if (best.mt == 0 || cost < least || (cost == least && mt == best.mt)) {
         least = cost;
         best = StreamPlan{mt, 1, each};
