@@ -100,8 +100,8 @@ int32_t eplb_quantize_weights4(const void* w, int32_t dtype, int32_t G, int64_t 
  * eplb_expert_matmul4 -- eplb_expert_matmul16 (not transposed) with weights in
  * that format: what a code and its scale stand for is multiplied exactly, as
  * long as it is 0 or its magnitude is at least 2^-126 (scales of 2 .. 254; what
- * is below may count as 0, and a value past the largest finite 32-bit number is
- * an infinity).
+ * is below may count as 0, and a value past the largest finite 32-bit number
+ * may be an infinity).
  *   q          [G][N][C / 2]     16-byte aligned
  *   scale      [G][N][C / 32]    4-byte aligned
  *   C                            a multiple of 32

@@ -97,6 +97,11 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Lin
   const i32x4 from_w = FOUR ? describe(a.q + first * ld, (uint64_t)rows * ld)
                             : describe(static_cast<const uint8_t*>(a.w) + first * ld, (uint64_t)rows * ld);
   const i32x4 from_s = FOUR ? describe(a.scale + first * ld_s, (uint64_t)rows * ld_s) : from_w;
+  // Where a part of 16 bytes lies in a row's 128.  Quads 0 and 1, 2 and 3 read together, without conflicts where their parts
+  // are 1 apart: parts that are 4 apart, as with 4-bit values (which are 32 of k to a lane), become neighbours.
+  constexpr bool kFours = FOUR && MODE != kScaled;
+  auto place_of = [](int part) { return kFours ? (part & 3) << 1 | part >> 2 : part; };
+  auto part_at = [](int place) { return kFours ? (place & 1) << 2 | place >> 1 : place; };
   const uint32_t at_w = col * ld + quad * 16, at_s = col * ld_s + quad;
   auto load_w = [&](int c, StreamChunk& p) {
     const int k = c * Shape::kChunk + quad * (FOUR ? 32 : 8);      // this lane's first; half a chunk on its second
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Lin
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
       const int r = (wave * kXLoads + i) % kOctets * 8 + (lane >> 3);
-      part_x[i] = ((lane & 7) ^ along_key(r)) * 8;
+      part_x[i] = part_at((lane & 7) ^ along_key(r)) * 8;
       at_x[i] = src[r] < 0 ? kOutside : (uint32_t)src[r] * (uint32_t)a.ld * 2 + part_x[i] * 2;
     }
     const uint32_t lds_at = lds_address(lds);
@@ -195,7 +200,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 4) void linear_stream_kernel(Lin
         if (FOUR && u % kBatch == 0) load_s(i + kBatch, scale[u / kBatch + 1 & 1]);
         auto rows_of = [&](int m, int at) {       // eight of k, part `at` of the chunk, of row `col` of tile m
           const int block = c_in * (Shape::kChunk / kTileK) + (at >> 3), r = m * 16 + col;
-          return *reinterpret_cast<const i32x4*>(rows_at + block * kBlockBytes + r * 128 + (((at & 7) ^ along_key(r)) << 4));
+          return *reinterpret_cast<const i32x4*>(rows_at + block * kBlockBytes + r * 128 + ((place_of(at & 7) ^ along_key(r)) << 4));
         };
         if constexpr (MODE == kScaled) {
 #pragma unroll
@@ -299,7 +304,7 @@ inline StreamPlan plan_stream(int64_t R, int64_t N, int32_t G, bool four) {
   double least = 0;
   for (int mt = 1; mt <= (four ? 4 : 8); mt *= 2) {
     // what an output of a tile costs, against one of a tile of 16 rows: the weights are the same, but more is multiplied
-    const double weight = four ? (mt == 1 ? 1 : mt == 2 ? 1.15 : 1.6) : (mt == 1 ? 1 : mt == 2 ? 1.02 : mt == 4 ? 1.06 : 1.3);
+    const double weight = four ? (mt == 1 ? 1 : mt == 2 ? 1.15 : 1.6) : (mt == 1 ? 1 : mt == 2 ? 1.02 : mt == 4 ? 1.06 : 1.25);
     double tiles = G, more_of_them = 0;    // and how many groups have another one; what chance may add
     for (int t = 1; t <= 64 && 16 * mt * t < mean + 3 * spread; ++t) {
       const double more = 0.5 * std::erfc((16 * mt * t - mean) / (spread * std::sqrt(2.0)));
