@@ -125,35 +125,43 @@ Width width_for(int64_t C) {
   return Width{(int)ceil_div(waves, slices), (int)slices};
 }
 
-template <int DTYPE, int U>
+// `K` choices of 8 / K tokens at once: a token of few choices alone asks for too little at a time (8192 tokens of 2 rows of
+// 4096 32-bit values: 73 us by fours, 92 alone).
+template <int DTYPE, int U, int K>
 __global__ __launch_bounds__(kWidest) void combine_kernel(CombineArgs a, int32_t waves) {
+  constexpr int kTokens = 8 / K;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int each = waves == 1 ? kAlone : 1;
   const int begin = ((int)blockIdx.y * waves + (waves == 1 ? 0 : wave)) * (64 * kEach), left = (int)a.C - begin;
   const int first = begin + (int)(threadIdx.x & 63) * U;
-  for (int64_t t = (int64_t)blockIdx.x * each + (waves == 1 ? wave : 0); t < a.T; t += (int64_t)gridDim.x * each) {
-    float sum[kEach] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 8) {
+  for (int64_t t0 = ((int64_t)blockIdx.x * each + (waves == 1 ? wave : 0)) * kTokens; t0 < a.T;
+       t0 += (int64_t)gridDim.x * each * kTokens) {
+    float sum[kTokens][kEach] = {};
+    for (int k0 = 0; k0 < a.K; k0 += K) {
       Eight<DTYPE, U> v[8];
       float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t i = t * a.K + min(k0 + j, a.K - 1);
+        const int64_t t = min(t0 + j / K, a.T - 1), i = t * a.K + min(k0 + j % K, a.K - 1);
         const int32_t p = a.place[i];
-        const bool some = k0 + j < a.K && p >= 0 && p < a.R;
+        const bool some = k0 + j % K < a.K && p >= 0 && p < a.R;
         w[j] = !some ? 0.0f : a.weights == nullptr ? 1.0f : a.weights[i];
-        if (k0 + j < a.K) v[j].load(row_of(a.y, p, a.C * size_of(DTYPE), some), first, left);
+        if (k0 + j % K < a.K && t0 + j / K < a.T) v[j].load(row_of(a.y, p, a.C * size_of(DTYPE), some), first, left);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (k0 + j < a.K) {
+        if (k0 + j % K < a.K && t0 + j / K < a.T) {
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) sum[e] = fmaf(w[j], v[j][e], sum[e]);
+          for (int e = 0; e < kEach; ++e) sum[j / K][e] = fmaf(w[j], v[j][e], sum[j / K][e]);
         }
     }
-    if (a.out_dtype == kF32) store_eight<kF32, U>(a.out, t, a.C, first, left, sum);
-    else if (a.out_dtype == kBf16) store_eight<kBf16, U>(a.out, t, a.C, first, left, sum);
-    else store_eight<kF16, U>(a.out, t, a.C, first, left, sum);
+#pragma unroll
+    for (int n = 0; n < kTokens; ++n) {
+      if (t0 + n >= a.T) break;
+      if (a.out_dtype == kF32) store_eight<kF32, U>(a.out, t0 + n, a.C, first, left, sum[n]);
+      else if (a.out_dtype == kBf16) store_eight<kBf16, U>(a.out, t0 + n, a.C, first, left, sum[n]);
+      else store_eight<kF16, U>(a.out, t0 + n, a.C, first, left, sum[n]);
+    }
   }
 }
 
@@ -252,20 +260,31 @@ __global__ __launch_bounds__(kWidest) void combine_backward_kernel(CombineBackwa
 }
 
 // Workgroups along the tokens: what is past them is taken in turns.
-unsigned groups_for(int64_t T, int waves) {
-  return (unsigned)std::min(ceil_div(T, waves == 1 ? kAlone : 1), int64_t(1) << 22);
+unsigned groups_for(int64_t T, int waves, int tokens) {
+  return (unsigned)std::min(ceil_div(T, (waves == 1 ? kAlone : 1) * tokens), int64_t(1) << 22);
+}
+
+template <int DTYPE, int U, int K>
+void launch_choices(const CombineArgs& a, hipStream_t stream) {
+  const Width w = width_for(a.C);
+  combine_kernel<DTYPE, U, K><<<dim3(groups_for(a.T, w.waves, 8 / K), w.slices), w.block(), 0, stream>>>(a, w.waves);
 }
 
 template <int DTYPE, int U>
 void launch(const CombineArgs& a, hipStream_t stream) {
-  const Width w = width_for(a.C);
-  combine_kernel<DTYPE, U><<<dim3(groups_for(a.T, w.waves), w.slices), w.block(), 0, stream>>>(a, w.waves);
+  // several tokens to a wave only where there are workgroups for the chip all the same (64 tokens of 2 rows of 4096: 7.7 us
+  // by fours, 5.1 alone)
+  const int waves = width_for(a.C).waves, few = a.K <= 2 ? 2 : a.K <= 4 ? 4 : 8;
+  const int choices = groups_for(a.T, waves, 8 / few) >= 512 ? few : 8;
+  if (choices == 2) launch_choices<DTYPE, U, 2>(a, stream);
+  else if (choices == 4) launch_choices<DTYPE, U, 4>(a, stream);
+  else launch_choices<DTYPE, U, 8>(a, stream);
 }
 
 template <int DTYPE, int U>
 void launch(const CombineBackwardArgs& a, hipStream_t stream) {
   const Width w = width_for(a.C);
-  combine_backward_kernel<DTYPE, U><<<groups_for(a.T, w.waves), w.block(), 0, stream>>>(a, w.waves);
+  combine_backward_kernel<DTYPE, U><<<groups_for(a.T, w.waves, 1), w.block(), 0, stream>>>(a, w.waves);
 }
 
 template <int DTYPE, typename Args>

@@ -170,3 +170,19 @@ def test_graph_and_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want if i % 2 else other))
+
+
+@pytest.mark.parametrize("T,K,C,dtype", [(2049, 1, 520, "bf16"), (8301, 2, 100, "f32"), (1027, 3, 1030, "f16"),
+                                         (1025, 4, 4104, "bf16"), (8195, 2, 33, "f16")])
+def test_many_tokens_of_few_choices(T, K, C, dtype):
+    """Several tokens at a time, the last ones fewer: the sums of the same tokens taken alone, bit for bit, and right."""
+    note("few choices", T, K, C, dtype)
+    y, place, order, w, _ = case(T, K, C, dtype, T + C)
+    y, place, w = y.to(DEV), place.to(DEV).view(T, K), w.to(DEV)
+    place[5], place[T - 1, K - 1] = -1, T * K
+    got = eplb.combine_rows(y, place, w)
+    some = torch.cat([torch.arange(40), torch.arange(T - 40, T)]).to(DEV)
+    assert torch.equal(eplb.combine_rows(y, place[some].contiguous(), w[some].contiguous()), got[some])
+    inside = (place >= 0) & (place < T * K)
+    rows = y.double()[place.clamp(0, T * K - 1).long()] * inside.unsqueeze(2) * w.double().unsqueeze(2)
+    check(got, rows.sum(1).cpu(), rows.abs().sum(1).cpu(), K, "out")
