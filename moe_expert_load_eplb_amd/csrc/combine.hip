@@ -287,11 +287,16 @@ void launch(const CombineBackwardArgs& a, hipStream_t stream) {
   combine_backward_kernel<DTYPE, U><<<groups_for(a.T, w.waves, 1), w.block(), 0, stream>>>(a, w.waves);
 }
 
+bool on_words(const void* p) { return (uintptr_t)p % 4 == 0; }
+bool on_words(const CombineArgs& a) { return on_words(a.y) && on_words(a.out); }
+bool on_words(const CombineBackwardArgs& a) { return on_words(a.d_out) && on_words(a.y) && on_words(a.d_y); }
+
+// Units of more than two bytes need rows that start at a multiple of four.
 template <int DTYPE, typename Args>
 void launch_for(const Args& a, hipStream_t stream) {
-  if (a.C % 8 == 0 && a.C > 128) launch<DTYPE, 16 / size_of(DTYPE)>(a, stream);
-  else if (a.C % 2 == 0) launch<DTYPE, 2>(a, stream);
-  else launch<DTYPE, 1>(a, stream);
+  if (a.C % 2 != 0 || !on_words(a)) launch<DTYPE, 1>(a, stream);
+  else if (a.C % 8 == 0 && a.C > 128) launch<DTYPE, 16 / size_of(DTYPE)>(a, stream);
+  else launch<DTYPE, 2>(a, stream);
 }
 
 }  // namespace

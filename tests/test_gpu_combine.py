@@ -186,3 +186,33 @@ def test_many_tokens_of_few_choices(T, K, C, dtype):
     inside = (place >= 0) & (place < T * K)
     rows = y.double()[place.clamp(0, T * K - 1).long()] * inside.unsqueeze(2) * w.double().unsqueeze(2)
     check(got, rows.sum(1).cpu(), rows.abs().sum(1).cpu(), K, "out")
+
+
+@pytest.mark.parametrize("C", [520, 66])
+@pytest.mark.parametrize("shifted", ["y", "out", "d_out", "d_y", "all"])
+def test_arrays_at_odd_elements(C, shifted):
+    """16-bit arrays that start between words: the same bits as arrays that do not."""
+    T, K = 37, 3
+    note("odd elements", C, shifted)
+    y, place, order, w, d = (t.to(DEV) for t in case(T, K, C, "bf16", C))
+    d = d.bfloat16()
+
+    def at(t, name):
+        n = 1 if shifted in (name, "all") else 0
+        flat = torch.zeros((t.numel() + 2,), dtype=t.dtype, device=DEV)
+        flat[n:n + t.numel()] = t.reshape(-1)
+        return flat[n:n + t.numel()].view(t.shape), flat
+
+    want = eplb.combine_rows(y, place, w), *eplb.combine_rows_backward(d, y, place, order, w)
+    (ys, _), (ds, _) = at(y, "y"), at(d, "d_out")
+    (out, flat_out), (dy, flat_dy) = at(torch.zeros_like(want[0]), "out"), at(torch.zeros_like(want[1]), "d_y")
+    eplb.combine_rows(ys, place, w, out=out)
+    dw = torch.empty_like(want[2])
+    eplb.combine_rows_backward(ds, ys, place, order, w, out=(dy, dw))
+    assert torch.equal(out, want[0]) and torch.equal(dy, want[1])
+    assert torch.equal(dw, want[2]) or shifted != "out"               # lanes have other elements then
+    exact = (y.double()[place.long()].view(T, K, C) * d.double().unsqueeze(1))
+    check(dw, exact.sum(2).cpu(), exact.abs().sum(2).cpu(), C, "d_weights")
+    for flat, t in ((flat_out, out), (flat_dy, dy)):
+        first = t.storage_offset()
+        assert (flat[:first] == 0).all() and (flat[first + t.numel():] == 0).all()
