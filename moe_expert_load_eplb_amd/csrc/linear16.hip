@@ -124,6 +124,8 @@ __global__ __launch_bounds__(WI* WO * 64) void wgrad16_kernel(Wgrad16Args a, int
                [&](int r) -> int64_t { return o0 + r < a.N ? ((int64_t)g * a.N + o0 + r) * a.C + i0 : -1; },
                [&](int) { return K > 0; });
 }
+// 128 tiles: 28.7 us in small ones, 24.4 in large ones (8 groups of 512 rows, 512 x 2048), 256: 50 and 26 (4 groups of 512
+// rows, 2048 x 2048).
 bool large_wgrad(int64_t N, int64_t C, int32_t G) { return G * ceil_div(N, 256) * ceil_div(C, 256) >= 128; }
 
 template <Mode MODE, bool ROWS>
@@ -145,7 +147,7 @@ hipError_t launch_wgrad_form(const Wgrad16Args& a, hipStream_t stream) {
 }  // namespace
 
 int64_t linear16_blocks(int64_t R, int64_t outputs, int64_t, int32_t G, bool transpose) {
-  const int64_t tiles = tile_blocks(R, outputs, G);
+  const int64_t tiles = tile_blocks(R, outputs, G, false);
   return !transpose && stream_suits(R, G) ? std::max(tiles, stream_blocks(R, outputs, G, false)) : tiles;
 }
 

@@ -21,7 +21,7 @@ hipError_t launch_form(const Linear16Args& a, hipStream_t stream) {
 }  // namespace
 
 int64_t linear4_blocks(int64_t R, int64_t N, int64_t, int32_t G) {
-  const int64_t tiles = tile_blocks(R, N, G);
+  const int64_t tiles = tile_blocks(R, N, G, true);
   return stream_suits(R, G) ? std::max(tiles, stream_blocks(R, N, G, true)) : tiles;
 }
 

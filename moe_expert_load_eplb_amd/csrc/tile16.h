@@ -755,8 +755,12 @@ inline int64_t large_blocks(int64_t R, int64_t width, int32_t G) {
   return R / 256 * columns + kUnits / 2 + 2 * columns * std::min(R, (int64_t)G + 2);
 }
 
-inline bool large_suits(int64_t R, int64_t width, int32_t G) {
-  return R >= 128 * (int64_t)G && (R / 256 + G / 2) * ceil_div(width, 256) >= 128;
+// Large tiles where there are enough of them for the chip: 16-bit weights, 256 tiles: 122 us in small ones, 105 in large ones
+// (4096 rows of one group, 4096 x 4096), 288: 147 and 140 (8192 rows on 9, 2048 x 4096), 160: 86 and 105 (4096 rows), 192: 50
+// and 68 (8192 rows on 32, 1024 x 2048).  4-bit weights are converted once for twice the rows there: 224 tiles: 130 and 114
+// (6144 rows on 9), 160: 112 and 110, 128: 36.2 and 35.3 (4096 rows on 32, 1024 x 2048), 40: 29 and 33.
+inline bool large_suits(int64_t R, int64_t width, int32_t G, bool four) {
+  return R >= 128 * (int64_t)G && (R / 256 + G / 2) * ceil_div(width, 256) >= (four ? 128 : 256);
 }
 
 // Two stages of a block of both operands, and of scales where they are apart.
@@ -766,7 +770,7 @@ template <Mode MODE, Weights FORM>
 hipError_t launch_tiles(const Linear16Args& a, hipStream_t stream) {
   const int64_t width = FORM == kWeightsTransposed ? a.C : a.N;
   const bool far = a.X * a.ld * 2 >= (int64_t)kOutside;
-  if (!far && large_suits(a.R, width, a.G)) {
+  if (!far && large_suits(a.R, width, a.G, FORM == kWeights4)) {
     linear_large_kernel<MODE, FORM><<<dim3((unsigned)large_blocks(a.R, width, a.G)), dim3(512), lds_bytes(MODE, 256), stream>>>(a, (int32_t)ceil_div(width, 256));
     return hipGetLastError();
   }
@@ -778,8 +782,8 @@ hipError_t launch_tiles(const Linear16Args& a, hipStream_t stream) {
 }
 
 // Workgroups of whichever form a product takes.
-inline int64_t tile_blocks(int64_t R, int64_t width, int32_t G) {
-  return std::max(small_blocks(R, width, G), large_suits(R, width, G) ? large_blocks(R, width, G) : 0);
+inline int64_t tile_blocks(int64_t R, int64_t width, int32_t G, bool four) {
+  return std::max(small_blocks(R, width, G), large_suits(R, width, G, four) ? large_blocks(R, width, G) : 0);
 }
 
 }  // namespace eplb

@@ -82,6 +82,11 @@ CASES = [
     ([2304], 0, 0, 2304, 1, 4097, 136, "f16", "f32", False),
     ([1025, 511], 0, 300, 918, 2, 6000, 64, "bf16", "f16", True),
     ([256 * 9], 0, 0, 2304, 1, 3840, 200, "bf16", "bf16", False),
+    ([700, 257, 0, 900], 3, 6, 933, 2, 8001, 72, "bf16", "bf16", True),
+    ([2304], 0, 0, 2304, 1, 7433, 136, "f16", "f32", False),
+    ([1025, 511], 0, 300, 918, 2, 9000, 64, "bf16", "f16", True),
+    ([256 * 9], 0, 0, 2304, 1, 7680, 200, "bf16", "bf16", False),
+    ([384, 130, 129, 513, 1], 0, 5, 1162, 1, 9728, 64, "f16", "f16", True),
 ]
 
 

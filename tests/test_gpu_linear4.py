@@ -124,7 +124,13 @@ def check(got, ref, absolute, n, what):
     ([127, 128, 129], 0, 0, 384, 1, 130, 1056, "bf16", "f32", False),
     ([257, 1, 0, 16], 3, 5, 140, 2, 264, 288, "f16", "bf16", True),
     ([1] * 70 + [40], 1, 0, 64, 2, 96, 256, "bf16", "f32", True),
-    ([4, 4], 0, 0, 0, 1, 24, 64, "bf16", "bf16", True)])
+    ([4, 4], 0, 0, 0, 1, 24, 64, "bf16", "bf16", True),
+    # tiles of 256 rows: whole ones, pieces of them at the end, and what is behind a group's last 256 rows
+    ([700, 257, 0, 900], 3, 6, 933, 2, 4001, 96, "bf16", "bf16", True),
+    ([700, 257, 0, 900], 3, 6, 933, 2, 4001, 96, "f16", "f16", True),
+    ([2304], 0, 0, 2304, 1, 4000, 224, "f16", "f32", False),
+    ([1025, 511], 0, 300, 918, 2, 6000, 64, "bf16", "f16", True),
+    ([384, 130, 129, 513, 1], 0, 5, 1162, 1, 5120, 160, "f16", "bf16", True)])
 def test_product(counts, head, tail, X, topk, N, C, dtype, out, rows):
     G, R = len(counts), head + sum(counts) + tail
     note("product", counts[:6], head, tail, X, topk, N, C, dtype, out, rows)
