@@ -12,7 +12,7 @@
 // offset outside its descriptor and arrives as zeros.
 //
 // Measured, weights not in any cache: a token's 8 rows on 32 groups, 4096 x 2048:
-// 23.5 us, 5.7 TB/s (4-bit weights 13.4 us); 512 rows on 9, 2048 x 4096: 40 us (30);
+// 23.5 us, 5.7 TB/s (4-bit weights 13.6 us); 512 rows on 9, 2048 x 4096: 44 us (30);
 // tiles of 128 x 128: 26 (33) and 50 (59).
 #pragma once
 
@@ -290,7 +290,7 @@ struct StreamPlan {
 inline int64_t row_tiles(int64_t R, int32_t G, int tile) { return std::min(R, R / tile + G) + 2; }
 
 // Few rows: past these a tile of 128 x 128 is as good or better.  4096 x 2048 on 9, 64 rows each: 46 us here, 50 in tiles;
-// of 64 groups with 80 rows: 72 and 61; 4-bit weights, 64 rows: 33 and 59, of 64 groups with 80: 58 and 47.
+// of 64 groups with 80 rows: 72 and 61; 4-bit weights, 64 rows: 31 and 59, of 64 groups with 80: 58 and 47.
 inline bool stream_suits(int64_t R, int32_t G) { return R <= 64 * (int64_t)G; }
 
 // The busiest compute unit ends last, and what it can have in flight is the same whatever is on it: the form is the one
@@ -340,7 +340,9 @@ hipError_t launch_stream(const Linear16Args& a, int32_t each, hipStream_t stream
 
 template <Mode MODE, bool FOUR, int MT>
 hipError_t launch_stream(const Linear16Args& a, const StreamPlan& p, hipStream_t stream) {
-  constexpr int kAhead = FOUR && MT < 4 ? 2 : 4, kMost = FOUR ? 4 / MT : 16 / MT;
+  // chunks in flight.  16-bit weights, 2 and 4: 43 and 37 us (252 rows on 9, 2048 x 4096), 55 and 45 (512 rows); 4-bit
+  // weights (a chunk is four times the k): 13.8 and 14.3 (a token's 8 rows, 4096 x 2048), but 24.1 and 23.2 (252 rows)
+  constexpr int kAhead = FOUR && MT == 1 ? 2 : 4, kMost = FOUR ? 4 / MT : 16 / MT;
   if constexpr (kMost >= 8)
     if (p.share == 8) return launch_stream<MODE, FOUR, MT, 8, kAhead>(a, p.each, stream);
   if constexpr (kMost >= 4)
