@@ -1051,8 +1051,8 @@ def _choices(place: torch.Tensor, weights: torch.Tensor | None) -> tuple[int, in
     if shaped.dim() != 2:
         raise ValueError("weights must be [T, K]" if weights is not None else "place must be [T, K] without weights")
     T, K = shaped.shape
-    if place.numel() != T * K or place.dim() > 2:
-        raise ValueError(f"place must have {T * K} elements")
+    if place.shape not in ((T, K), (T * K,), (1, T * K)):     # a layer of group_rows' place, by itself or not
+        raise ValueError(f"place must have {T * K} elements, as [{T}, {K}] or [{T * K}]")
     return T, K
 
 
