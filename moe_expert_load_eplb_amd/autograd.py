@@ -112,6 +112,19 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows:
     return _ExpertLinear.apply(x, w, offsets, rows, place, K, x_grad)
 
 
+MOST_CHOICES = 64            # of a token, in combine_rows
+
+
+def _index(t: torch.Tensor, name: str, like: torch.Tensor) -> None:
+    """Refuses what a backward pass could not use as an index array beside `like`."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 class _ExpertLinear16(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets, rows, place, K):
@@ -141,8 +154,9 @@ def expert_linear16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, row
 
     x [T, C], w [G, N, C] of one type, bfloat16 or float16, C a multiple of 8, and
     N too where x or w needs a gradient; offsets, rows and place: one layer of
-    group_rows' outputs (offsets, order, place), rows and place together.  Without
-    them x is in grouped order itself.  Returns [R, N]."""
+    group_rows' outputs (offsets, order, place), rows and place together (K at
+    most 64 where x needs a gradient).  Without them x is in grouped order itself.
+    Returns [R, N]."""
     if x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1]:
         raise ValueError("x [T, C] and w [G, N, C] expected")
     if x.shape[1] % 8 != 0:
@@ -153,6 +167,12 @@ def expert_linear16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, row
         raise ValueError("rows and place go together")
     if rows is not None and (rows.shape[0] != x.shape[0] * K or place.numel() != x.shape[0] * K):
         raise ValueError(f"rows and place must be [{x.shape[0] * K}]")
+    if rows is not None and x.requires_grad and torch.is_grad_enabled():
+        if K > MOST_CHOICES:
+            raise ValueError(f"K must be at most {MOST_CHOICES} for the gradient of x, got {K}")
+        if place.shape not in ((x.shape[0], K), (x.shape[0] * K,), (1, x.shape[0] * K)):
+            raise ValueError(f"place must be [{x.shape[0] * K}], got {list(place.shape)}")
+        _index(place, "place", x)
     return _ExpertLinear16.apply(x, w, offsets, rows, place, K)
 
 
@@ -181,4 +201,6 @@ def combine(y: torch.Tensor, weights: torch.Tensor, place: torch.Tensor, order: 
         raise ValueError("y [T * K, C] and weights [T, K] expected")
     if place.numel() != weights.numel() or order.numel() != weights.numel():
         raise ValueError(f"place and order must be [{weights.numel()}]")
+    if torch.is_grad_enabled() and (y.requires_grad or weights.requires_grad):
+        _index(order, "order", y)
     return _Combine.apply(y, weights, place, order, dtype)
