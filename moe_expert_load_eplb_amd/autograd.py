@@ -136,6 +136,8 @@ class _ExpertLinear16(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offsets, rows, place = ctx.saved_tensors
         dy = dy.contiguous()
+        if dy.data_ptr() % 16 != 0:      # the products' rows start at 16 bytes; a part of a larger gradient starts anywhere
+            dy = dy.clone()
         dx = dw = None
         if ctx.needs_input_grad[0]:
             # a token's rows are summed in 32 bits, in the order of its choices, and rounded once

@@ -72,3 +72,32 @@ def test_index_arrays(noted):
     refused(noted, lambda: noted.expert_linear16(x, w, offsets, order, order.view(K, T), K), ValueError)
     for place in (order, order.view(T, K), order.view(1, T * K)):
         noted.expert_linear16(x, w, offsets, order, place, K).sum().backward()
+
+
+def test_gradients_that_start_anywhere(noted, monkeypatch):
+    """A gradient that is a part of a larger one, as behind a concatenation, may start at any element; what the products
+    get starts at 16 bytes and holds the same."""
+    seen = []
+
+    def expert_matmul16(x, w, offsets, rows=None, K=1, transpose=False, dtype=None):
+        if transpose:
+            seen.append(x)
+        return x.new_zeros((x.shape[0], w.shape[2 if transpose else 1]))
+
+    def expert_wgrad16(dy, x, offsets, rows=None, K=1, dtype=None):
+        seen.append(dy)
+        return x.new_zeros((offsets.shape[0] - 1, dy.shape[1], x.shape[1]))
+
+    monkeypatch.setattr(noted, "expert_matmul16", expert_matmul16)
+    monkeypatch.setattr(noted, "expert_wgrad16", expert_wgrad16)
+    offsets = torch.tensor([0, 2, 5], dtype=torch.int32)
+    for ahead in (0, 1, 3, 4, 8):
+        x = torch.randn((5, 16)).bfloat16().requires_grad_(True)
+        w = torch.randn((2, 8, 16)).bfloat16().requires_grad_(True)
+        y = noted.expert_linear16(x, w, offsets)
+        whole = torch.randn((ahead + y.numel(),)).bfloat16()
+        seen.clear()
+        torch.cat([torch.zeros((ahead,), dtype=torch.bfloat16), y.reshape(-1)]).backward(whole)
+        assert len(seen) == 2
+        for dy in seen:
+            assert dy.data_ptr() % 16 == 0 and torch.equal(dy, whole[ahead:].view(5, 8))
