@@ -1087,7 +1087,9 @@ def combine_rows_backward(d_out: torch.Tensor, y: torch.Tensor, place: torch.Ten
 
     d_out [T, C]; y [T * K, C]; place and order: group_rows', each the inverse of
     the other.  A choice whose place is outside y gets d_weights 0, a row that is
-    not the place of its own order gets zeros."""
+    not the place of its own order gets zeros.  Where d_weights is not wanted, y is
+    one element expanded to its shape, y.new_empty(()).expand(T * K, C): only the
+    type counts, no rows are read, and None stands for d_weights, in out too."""
     T, K = _choices(place, weights)
     if d_out.dim() != 2 or d_out.shape[0] != T:
         raise ValueError(f"d_out must be [{T}, C]")
@@ -1095,13 +1097,19 @@ def combine_rows_backward(d_out: torch.Tensor, y: torch.Tensor, place: torch.Ten
     _shapes((y,), ((T * K, C),), "y")
     if order.numel() != T * K:
         raise ValueError(f"order must have {T * K} elements")
+    both = y.stride() != (0, 0) or y.is_contiguous()          # an expanded y of one element has it
     dev = _together(d_out, y, place, order, weights, *(out or ()))
     if out is None:
-        out = (torch.empty((T * K, C), dtype=y.dtype, device=dev), torch.empty((T, K), dtype=torch.float32, device=dev))
-    else:
+        out = (torch.empty((T * K, C), dtype=y.dtype, device=dev),
+               torch.empty((T, K), dtype=torch.float32, device=dev) if both else None)
+    elif both:
         _shapes(out, ((T * K, C), (T, K)), "out")
+    else:
+        _shapes(out[:1], ((T * K, C),), "out")
+        if len(out) != 2 or out[1] is not None:
+            raise ValueError("out must be (d_y, None) without y's rows")
     _launch("eplb_combine_rows_backward", dev, _dev(d_out, d_out.dtype, "d_out"), _dtype(d_out.dtype, "d_out"),
-            _dev(y, y.dtype, "y"), _dtype(y.dtype, "y"), C, _dev(place, torch.int32, "place"),
+            _dev(y, y.dtype, "y") if both else None, _dtype(y.dtype, "y"), C, _dev(place, torch.int32, "place"),
             _dev(order, torch.int32, "order"), _optional(weights, torch.float32, (T, K), "weights"), T, K,
-            _dev(out[0], y.dtype, "d_y"), _dev(out[1], torch.float32, "d_weights"))
+            _dev(out[0], y.dtype, "d_y"), _dev(out[1], torch.float32, "d_weights") if both else None)
     return out

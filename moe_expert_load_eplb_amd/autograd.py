@@ -181,7 +181,8 @@ def expert_linear16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, row
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, place, order, dtype):
-        ctx.save_for_backward(y, weights, place, order)
+        # y is read again for the gradient of the weights only; without it its type and shape are kept
+        ctx.save_for_backward(y if ctx.needs_input_grad[1] else y.new_empty(()).expand(y.shape), weights, place, order)
         return combine_rows(y, place, weights, dtype=dtype)
 
     @staticmethod
