@@ -1,0 +1,74 @@
+"""Every form of the 16-bit and 4-bit products for few rows: HIP path against plain
+sums in 64 bits (needs an MI355X).  Which form a case takes is checked on the host, where the rules are.
+
+Tolerances: those of the products of few rows, (C + C / 32 + 16) * 2^-23 * sum |x|
+|w| and half a step of the output's type.  They hold for half-precision rows with
+4-bit weights in every form: a product of such a value and a 4-bit one has 13 bits
+and is exact, each of C additions is off by 2^-23 of what it has, and each 32 of
+the row take one multiply-add by their scale."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+eplb = pytest.importorskip("moe_expert_load_eplb_amd")
+
+from layer_forms import STREAM  # noqa: E402
+from test_gpu_linear_few import DEV, TYPES, check, product, rand, weights  # noqa: E402
+
+
+def note(*a):
+    print("[forms]", *a, flush=True)
+
+
+def grouping(counts, head, tail, topk):
+    """(offsets, rows, source of every row or -1, X) with a row before the first and one past the last among them."""
+    R = head + sum(counts) + tail
+    off = torch.tensor(head + np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+    X = R // topk + 1
+    idx = torch.randint(0, X * topk, (R,), generator=torch.Generator().manual_seed(R), dtype=torch.int32)
+    if R > 3:
+        idx[R // 2], idx[R // 3] = -1, X * topk
+    src = torch.where(idx >= 0, idx.long() // topk, -1)
+    return off, idx, torch.where(src < X, src, -1), X
+
+
+def taken(x, src):
+    out = torch.zeros((src.numel(), x.shape[1]), dtype=torch.float64)
+    out[src >= 0] = x.double()[src[src >= 0]]
+    return out
+
+
+def held(y, xr, values, off, transpose=False):
+    """y against the sums of 64 bits, group by group; rows of no group are zeros."""
+    inside = torch.zeros(y.shape[0], dtype=torch.bool)
+    for i in range(off.numel() - 1):
+        a, b = int(off[i]), int(off[i + 1])
+        inside[a:b] = True
+        w = values[i] if transpose else values[i].t()
+        check(y[a:b], xr[a:b] @ w, xr[a:b].abs() @ w.abs(), xr.shape[1], i)
+    assert (y.cpu()[~inside] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,out,long", [("bf16", "f32", False), ("bf16", "f32", True), ("f16", "f32", True),
+                                            ("f16", "bf16", False)])
+@pytest.mark.parametrize("four,form,counts,head,tail,N,short_c,long_c", STREAM)
+def test_few_rows(four, form, counts, head, tail, N, short_c, long_c, dtype, out, long):
+    C, topk = (long_c if long else short_c), 2 if sum(counts) % 2 else 1
+    note(four, form, counts[:6], head, tail, N, C, dtype, out)
+    off, idx, src, X = grouping(counts, head, tail, topk)
+    R = idx.numel()
+    x = rand((X, C), dtype, N + C)
+    wide = torch.full((X, C + 8), float("nan"), dtype=x.dtype)
+    wide[:, :C] = x
+    w, values = weights(four, len(counts), N, C, dtype, N)
+    whole = torch.full((R * N + 128,), 7.0, dtype=TYPES[out], device=DEV)
+    y = whole[64:64 + R * N].view(R, N)
+    product(four, wide.to(DEV)[:, :C], w, off.to(DEV), rows=idx.to(DEV), K=topk, out=y)
+    held(y, taken(x, src), values, off)
+    assert (y.cpu()[src < 0] == 0).all() and (whole[:64] == 7).all() and (whole[64 + R * N:] == 7).all()
+    again = product(four, x.to(DEV), w, off.to(DEV), rows=idx.to(DEV), K=topk, dtype=TYPES[out])
+    assert torch.equal(again, y)
