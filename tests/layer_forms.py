@@ -1,5 +1,6 @@
-"""Sizes of the 16-bit and 4-bit products of few rows by the form that they are
-meant to take, for the tests of the forms."""
+"""Sizes of the 16-bit and 4-bit products by the form that they are meant to take
+(few rows: rows of a tile / 16 and waves that share K;
+many rows: tiles of 256 x 256), for the tests of the forms."""
 from __future__ import annotations
 
 # four, (rows of a tile / 16, waves that share K), counts of the groups, rows before and behind them, N, a short C and one
@@ -34,3 +35,12 @@ STREAM = [
 # every pair that the launches tell apart
 STREAM_FORMS = {False: {(mt, share) for mt in (1, 2, 4, 8) for share in (1, 2, 4, 8) if share * mt <= 16},
                 True: {(mt, share) for mt in (1, 2, 4) for share in (1, 2, 4) if share * mt <= 4}}
+
+# four, counts, rows before and behind them, outputs (their width, whichever side of the weights it is), K: most groups
+# end in a rest, of one row, 128 and just above
+LARGE = [
+    (False, [384, 130, 129, 513, 1], 0, 5, 10760, 64),
+    (False, [128, 128, 256, 257, 255], 3, 0, 11000, 136),
+    (True, [384, 130, 129, 513, 1], 0, 5, 5377, 160),
+    (True, [128, 128, 256, 257, 255], 3, 0, 5600, 96),
+]

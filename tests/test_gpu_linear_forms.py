@@ -1,5 +1,6 @@
-"""Every form of the 16-bit and 4-bit products for few rows: HIP path against plain
-sums in 64 bits (needs an MI355X).  Which form a case takes is checked on the host, where the rules are.
+"""Every form of the 16-bit and 4-bit products for few rows, and the large tiles at
+groups that end in a rest: HIP path against plain sums in 64 bits (needs an
+MI355X).  Which form a case takes is checked on the host, where the rules are.
 
 Tolerances: those of the products of few rows, (C + C / 32 + 16) * 2^-23 * sum |x|
 |w| and half a step of the output's type.  They hold for half-precision rows with
@@ -16,7 +17,7 @@ pytestmark = pytest.mark.gpu
 
 eplb = pytest.importorskip("moe_expert_load_eplb_amd")
 
-from layer_forms import STREAM  # noqa: E402
+from layer_forms import LARGE, STREAM  # noqa: E402
 from test_gpu_linear_few import DEV, TYPES, check, product, rand, weights  # noqa: E402
 
 
@@ -72,3 +73,21 @@ def test_few_rows(four, form, counts, head, tail, N, short_c, long_c, dtype, out
     assert (y.cpu()[src < 0] == 0).all() and (whole[:64] == 7).all() and (whole[64 + R * N:] == 7).all()
     again = product(four, x.to(DEV), w, off.to(DEV), rows=idx.to(DEV), K=topk, dtype=TYPES[out])
     assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("four,counts,head,tail,width,K", LARGE)
+def test_large_tiles(four, counts, head, tail, width, K, dtype, out):
+    note("large", four, counts, head, tail, width, K, dtype, out)
+    off, idx, src, X = grouping(counts, head, tail, 2)
+    x = rand((X, K), dtype, width + K)
+    xr = taken(x, src)
+    w, values = weights(four, len(counts), width, K, dtype, width)
+    y = product(four, x.to(DEV), w, off.to(DEV), rows=idx.to(DEV), K=2, dtype=TYPES[out])
+    held(y, xr, values, off)
+    assert (y.cpu()[src < 0] == 0).all()
+    if not four:
+        wt = rand((len(counts), K, width), dtype, K)
+        y = eplb.expert_matmul16(x.to(DEV), wt.to(DEV), off.to(DEV), rows=idx.to(DEV), K=2, transpose=True, dtype=TYPES[out])
+        held(y, xr, wt.double(), off, transpose=True)
+        assert (y.cpu()[src < 0] == 0).all()

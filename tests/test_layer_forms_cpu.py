@@ -9,7 +9,7 @@ import subprocess
 
 import pytest
 
-from layer_forms import STREAM, STREAM_FORMS
+from layer_forms import LARGE, STREAM, STREAM_FORMS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -60,3 +60,11 @@ def test_streaming_forms(forms):
         assert got == "stream %d %d" % case[1], case
     for four, want in STREAM_FORMS.items():
         assert {c[1] for c in STREAM if c[0] == four} == want
+
+
+def test_large_tiles(forms):
+    for transposed in (0, 1):
+        listed = [c for c in LARGE if not (transposed and c[0])]
+        sizes = [(head + sum(counts) + tail, width, len(counts), four, transposed)
+                 for four, counts, head, tail, width, _ in listed]
+        assert forms(sizes) == ["large"] * len(listed)
