@@ -3,8 +3,9 @@
 // y[r] = x[src(r)] w[g]^T, its gradient of the rows dy[r] w[g] with the weights read
 // as they lie, and of the weights dw[g] = sum over r of dy[r]^T x[src(r)], rows of x
 // gathered by the loads.  Large ones are bound by the matrix unit at the clock that
-// power leaves, and by the start and the end of a tile: 16384 rows on 9, 4096 x 4096:
-// 490 us, 1.12 PFLOP/s; rows' gradient 500, into 32 bits 520; weights' 548, 1.00.
+// power leaves, and by the start and the end of a tile: 16384 rows on 9, 4096 x 4096,
+// launches back to back: 498 us, 1.10 PFLOP/s; rows' gradient 512, into 32 bits 529;
+// weights' 611, 0.90.
 #include "stream16.h"
 
 namespace eplb {
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(WI* WO * 64) void wgrad16_kernel(Wgrad16Args a, int
                [&](int r) -> int64_t { return o0 + r < a.N ? ((int64_t)g * a.N + o0 + r) * a.C + i0 : -1; },
                [&](int) { return K > 0; });
 }
-// 128 tiles: 28.7 us in small ones, 24.4 in large ones (8 groups of 512 rows, 512 x 2048), 256: 50 and 26 (4 groups of 512
+// 128 tiles: 28.7 us in small ones, 23.0 in large ones (8 groups of 512 rows, 512 x 2048), 256: 50 and 24.8 (4 groups of 512
 // rows, 2048 x 2048).
 bool large_wgrad(int64_t N, int64_t C, int32_t G) { return G * ceil_div(N, 256) * ceil_div(C, 256) >= 128; }
 

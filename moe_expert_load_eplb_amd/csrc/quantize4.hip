@@ -5,7 +5,7 @@
 // lies between 6 and 7 rounds to 6, off by at most the half step that values
 // between 4 and 6 are off by.
 //
-// Bound by memory: 9 experts of 2048 x 4096 in 32 bits: 61 us, 5.6 TB/s.  Four lanes to
+// Bound by memory: 9 experts of 2048 x 4096 in 32 bits: 59 us, 5.8 TB/s.  Four lanes to
 // a block, 16 or 32 bytes of each, so that a wave reads whole lines.
 #include "experts_device.h"
 #include "layer_internal.h"

@@ -11,9 +11,14 @@
 // behind a branch: what lies past the end of a row, a group or the outputs has an
 // offset outside its descriptor and arrives as zeros.
 //
-// Measured, weights not in any cache: a token's 8 rows on 32 groups, 4096 x 2048:
-// 23.5 us, 5.7 TB/s (4-bit weights 13.6 us); 512 rows on 9, 2048 x 4096: 44 us (30);
-// tiles of 128 x 128: 26 (33) and 50 (59).
+// Measured, launches back to back with the weights of many calls in rotation, so
+// that none is in a cache: a token's 8 rows on 32 groups, 4096 x 2048: 23.2 us, 5.8
+// TB/s (4-bit weights 13.4; traced among others 28.1 and 13.9); 512 uneven rows on
+// 9, 2048 x 4096: 43 us (30); tiles of 128 x 128: 24.2 (28) and 46 (54).
+//
+// What is not there is multiplied all the same, as zeros: the sets of waves past a
+// workgroup's outputs, the rows of a tile past its group's last, and the rounds of
+// stages past the end of K (`kStages` at a time).
 #pragma once
 
 #include <cmath>
@@ -289,13 +294,21 @@ struct StreamPlan {
 // Tiles of `tile` rows: every group adds at most one that is not full, and a tile has a row.
 inline int64_t row_tiles(int64_t R, int32_t G, int tile) { return std::min(R, R / tile + G) + 2; }
 
-// Few rows: past these a tile of 128 x 128 is as good or better.  4096 x 2048 on 9, 64 rows each: 46 us here, 50 in tiles;
-// of 64 groups with 80 rows: 72 and 61; 4-bit weights, 64 rows: 31 and 59, of 64 groups with 80: 58 and 47.
+// Few rows.  Uneven groups (the largest has one and a half times the mean on 9, three times on 32 and 64), here and in
+// tiles, us, at 47, 64, 71, 80 and 95 rows to a group.  16-bit weights:
+//   2048 x 4096 on 9   39 43 43 45 49 | 45 46 47 47 48      4096 x 2048 on 9   40 44 44 45 50 | 50 51 51 52 51
+//   1024 x 2048 on 32  49 56 53 58 62 | 49 49 48 50 48      on 64              62 79 78 88 97 | 64 72 73 73 72
+// 4-bit weights:
+//   2048 x 4096 on 9   29 31 39 44 44 | 53 55 55 55 55      4096 x 2048 on 9   28 31 39 40 42 | 39 39 39 40 40
+//   1024 x 2048 on 32  36 39 31 31 40 | 31 39 39 39 39      on 64              51 54 61 57 67 | 40 64 65 64 70
+// One limit for both: no mean tells all of these apart.  What it costs most: 4-bit weights of long rows on few groups, a
+// third just past it.
 inline bool stream_suits(int64_t R, int32_t G) { return R <= 64 * (int64_t)G; }
 
 // The busiest compute unit ends last, and what it can have in flight is the same whatever is on it: the form is the one
 // for which ceil(workgroups / compute units) times what a workgroup costs, its sets of outputs and its start and end, is
-// least.  512 rows on 9, 4096 x 2048 outputs: 40 us with 6 sets of 64 rows to a workgroup (224 of them), 65 with 5 (265).
+// least.  512 rows on 9, 2048 outputs, K 4096, 5 sets to a workgroup: 37 us in tiles of 64 rows and 42 in those of 128
+// where every group has 57 rows; where groups have up to 84, some two tiles of 64, 61 and 43.
 inline StreamPlan plan_stream(int64_t R, int64_t N, int32_t G, bool four) {
   constexpr int kUnits = 256;
   // rows to a group: as chance deals them out, and a fifth of the mean besides, which a balanced placement leaves

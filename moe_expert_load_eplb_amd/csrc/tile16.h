@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t lds_address(uint8_t* p) {
 // What the two operands hold.  kScaled: the first 4-bit values without their scales, as half precision, the second half
 // precision; what an instruction adds up, 32 of k, is multiplied by the scales then.  (A value times its scale is a
 // bfloat16 number, but not one of half precision; with the rows as two bfloat16 numbers each, 16384 rows on 9, 4096 x
-// 4096, took 1210 us, so 855.)
+// 4096, took 1210 us, so 778.)
 enum Mode { kBothBf16, kBothF16, kScaled };
 
 // Eight 4-bit values times a power of two as bfloat16.  Of the scale only the exponent counts; all bits of it set (255
@@ -755,10 +755,11 @@ inline int64_t large_blocks(int64_t R, int64_t width, int32_t G) {
   return R / 256 * columns + kUnits / 2 + 2 * columns * std::min(R, (int64_t)G + 2);
 }
 
-// Large tiles where there are enough of them for the chip: 16-bit weights, 256 tiles: 122 us in small ones, 105 in large ones
-// (4096 rows of one group, 4096 x 4096), 288: 147 and 140 (8192 rows on 9, 2048 x 4096), 160: 86 and 105 (4096 rows), 192: 50
-// and 68 (8192 rows on 32, 1024 x 2048).  4-bit weights are converted once for twice the rows there: 224 tiles: 130 and 114
-// (6144 rows on 9), 160: 112 and 110, 128: 36.2 and 35.3 (4096 rows on 32, 1024 x 2048), 40: 29 and 33.
+// Large tiles where there are enough of them for the chip: 16-bit weights, 256 tiles: 120 us in small ones, 100 in large ones
+// (4096 rows of one group, 4096 x 4096), 288: 139 and 142 (8192 rows on 9, 2048 x 4096), 160: 82 and 105 (4096 rows), 192: 49
+// and 69 (8192 rows on 32, 1024 x 2048).  4-bit weights are converted once for twice the rows there: 224 tiles: 126 and 113
+// (6144 rows on 9), 160: 111 and 111, 128: 36 and 34 (4096 rows on 32, 1024 x 2048; 36 and 53 where the largest group has
+// three times the mean: nearly every group ends in a rest of its own), 48: 29 and 32.
 inline bool large_suits(int64_t R, int64_t width, int32_t G, bool four) {
   return R >= 128 * (int64_t)G && (R / 256 + G / 2) * ceil_div(width, 256) >= (four ? 128 : 256);
 }
