@@ -91,3 +91,33 @@ def test_large_tiles(four, counts, head, tail, width, K, dtype, out):
         y = eplb.expert_matmul16(x.to(DEV), wt.to(DEV), off.to(DEV), rows=idx.to(DEV), K=2, transpose=True, dtype=TYPES[out])
         held(y, xr, wt.double(), off, transpose=True)
         assert (y.cpu()[src < 0] == 0).all()
+
+
+@pytest.mark.parametrize("four,form,counts,head,tail,N,short_c,long_c", STREAM)
+def test_infinities_and_nan_of_few_rows(four, form, counts, head, tail, N, short_c, long_c):
+    """A row's infinities and NaN reach that row's outputs only, a weight's that output's of its group, as the formula has
+    them (0 times an infinity is NaN); what a tile, a stage or a set of outputs has none of is not multiplied with them."""
+    note("not finite", four, form)
+    G, R, C = len(counts), head + sum(counts) + tail, short_c
+    dtype = torch.float16 if four else torch.bfloat16
+    off, g = torch.tensor(head + np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32), torch.Generator().manual_seed(N)
+    x = torch.randn((R, C), generator=g).to(dtype)
+    hit = torch.randint(0, R, (3,), generator=g).tolist()
+    x[hit[0], 0], x[hit[1], C - 1], x[hit[2], C // 2] = float("inf"), float("-inf"), float("nan")
+    if four:
+        w, values = weights(True, G, N, C, "f16", N)
+        w[1][:, N - 1, C // 32 - 1], w[1][0, 0, 0] = 255, 255        # NaN
+        values[:, N - 1, C - 32:], values[0, 0, :32] = float("nan"), float("nan")
+    else:
+        values = torch.randn((G, N, C), generator=g).to(dtype)
+        values[:, N - 1, C - 1], values[0, 0, 0], values[:, 3, 1], values[:, 4] = float("nan"), float("inf"), 0, 0
+        w, values = (values.to(DEV),), values.double()
+    y = product(four, x.to(DEV), w, off.to(DEV), dtype=torch.float32).double()
+    want = torch.zeros((R, N), dtype=torch.float64, device=DEV)
+    xd, values = x.double().to(DEV), values.to(DEV)
+    for i in range(G):
+        for r in range(int(off[i]), int(off[i + 1])):
+            want[r] = (values[i] * xd[r]).sum(1)
+    odd = ~torch.isfinite(want)
+    assert odd.any() and not odd.all() and torch.equal(~torch.isfinite(y), odd)
+    assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(y[odd & ~torch.isnan(y)], want[odd & ~torch.isnan(y)])
