@@ -1051,7 +1051,8 @@ def _choices(place: torch.Tensor, weights: torch.Tensor | None) -> tuple[int, in
     if shaped.dim() != 2:
         raise ValueError("weights must be [T, K]" if weights is not None else "place must be [T, K] without weights")
     T, K = shaped.shape
-    if place.dim() > 2 or place.numel() != T * K or (place.shape != (T, K) and max(place.shape, default=1) != T * K):
+    if place.numel() != T * K or place.dim() > 1 and (
+            place.dim() > 2 or place.shape != (T, K) and max(place.shape) != T * K):
         raise ValueError(f"place must have {T * K} elements, as [{T}, {K}] or [{T * K}]")
     return T, K
 

@@ -172,7 +172,7 @@ def expert_linear16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, row
     if rows is not None and x.requires_grad and torch.is_grad_enabled():
         if K > MOST_CHOICES:
             raise ValueError(f"K must be at most {MOST_CHOICES} for the gradient of x, got {K}")
-        if place.dim() > 2 or (place.shape != (x.shape[0], K) and max(place.shape, default=1) != x.shape[0] * K):
+        if place.dim() > 1 and (place.dim() > 2 or place.shape != (x.shape[0], K) and max(place.shape) != place.numel()):
             raise ValueError(f"place must be [{x.shape[0] * K}], got {list(place.shape)}")
         _index(place, "place", x)
     return _ExpertLinear16.apply(x, w, offsets, rows, place, K)
